@@ -48,11 +48,25 @@ AR_SF_SWIZZLED = 1
 AR_ACC_FP32 = 0
 AR_ACC_ELEMENT = 1
 
+# enum ar_score
+AR_SCORE_SOFTMAX = 0
+AR_SCORE_SIGMOID = 1
+# enum ar_group_score
+AR_GROUP_MAX = 0
+AR_GROUP_TOP2 = 1
+# enum ar_activation
+AR_ACT_NONE = 0
+AR_ACT_SILU_MUL = 1
+
 AR_MAX_RANKS = 16
 AR_ONESHOT_MAX_TOKENS = 128
 AR_BARRIER_FLAG_COUNT = 256
 AR_MAX_HIDDEN = 32768
 AR_NOALLOC_SLOT_BYTES = 4 << 20
+AR_MAX_EXPERTS = 1024
+AR_MAX_TOPK = 32
+AR_MAX_GROUPS = 32
+AR_QUANT_BLOCK = 128
 
 PATTERNS = {
     "res_norm": AR_RESIDUAL_OUT | AR_NORM_OUT,
@@ -137,6 +151,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ar_fusion_run_noalloc.argtypes = [ctypes.POINTER(_vp), _i, _i, _i, _i, _vp, _vp,
                                         ctypes.c_float, _i, _vp, _vp, _vp, _vp, _vp, _vp]
     L.ar_fusion_noalloc_status.argtypes = [_vp, ctypes.POINTER(_i)]
+    L.ar_fusion_route.argtypes = [_vp, _i, _i, _i, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_float,
+                                  _vp, _vp, _vp]
+    L.ar_fusion_expert_plan.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
+    L.ar_fusion_quant_blocks.argtypes = [_vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp]
+    L.ar_fusion_matmul_fp8.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]
+    L.ar_fusion_expert_matmul_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                                              _vp]
+    L.ar_fusion_combine.argtypes = [_vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]
     for name in ("ar_fusion_workspace_bytes", "ar_fusion_workspace_create",
                  "ar_fusion_workspace_destroy", "ar_fusion_workspace_info",
                  "ar_fusion_workspace_copy_state", "ar_fusion_workspace_status",
@@ -147,7 +169,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "ar_fusion_sum_ex",
                  "ar_fusion_workspace_stage", "ar_fusion_workspace_partial_ptr",
                  "ar_fusion_run", "ar_fusion_norm_amax",
-                 "ar_fusion_sum", "ar_fusion_run_noalloc", "ar_fusion_noalloc_status"):
+                 "ar_fusion_sum", "ar_fusion_run_noalloc", "ar_fusion_noalloc_status",
+                 "ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",
+                 "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8", "ar_fusion_combine"):
         getattr(L, name).restype = _i
     _lib = L
     return L
@@ -420,3 +444,162 @@ def ar_fusion_noalloc_status(stream=None):
     if rc not in (AR_OK, AR_ERR_TIMEOUT):
         _check(rc)
     return rc, d.value
+
+
+# ----------------------------------------------------------- expert layers
+
+def _expect(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _typed(name: str, t: torch.Tensor, dtypes, shape=None) -> None:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported type {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _on_current(*ts) -> None:
+    """The library launches on the current device: operands of another one are refused."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"expected tensors of the current device cuda:{dev}, got {t.device}")
+
+
+_ELEM = (torch.bfloat16, torch.float16, torch.float32)
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def _quant_blocks(depth: int) -> int:
+    return (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
+
+
+def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: torch.Tensor,
+                    weights_out: torch.Tensor, score: int = AR_SCORE_SIGMOID, groups: int = 1,
+                    groups_kept: int = 1, group_score: int = AR_GROUP_TOP2,
+                    renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """logits [tokens, experts]; bias [experts] fp32 or None; ids_out (int32)
+    and weights_out (fp32) [tokens, topk]."""
+    _typed("logits", logits, _ELEM)
+    _expect(logits.dim() == 2 and ids_out.dim() == 2, "logits and ids_out have two dimensions")
+    tokens, experts = logits.shape
+    topk = ids_out.shape[1]
+    _typed("ids_out", ids_out, _I32, (tokens, topk))
+    _typed("weights_out", weights_out, _F32, (tokens, topk))
+    if bias is not None:
+        _typed("bias", bias, _F32, (experts,))
+    _on_current(logits, bias, ids_out, weights_out)
+    _check(lib().ar_fusion_route(_ptr(logits), tokens, experts, _dtype_id(logits), _ptr(bias),
+                                 int(score), int(groups), int(groups_kept), int(group_score),
+                                 topk, int(renormalize), ctypes.c_float(scale), _ptr(ids_out),
+                                 _ptr(weights_out), _stream(stream)))
+
+
+def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Tensor,
+                          position_out: torch.Tensor, first_expert: int = 0,
+                          stream=None) -> None:
+    """ids [tokens, topk] int32; offsets_out [experts + 1] and position_out
+    [tokens, topk] int32, for the experts first_expert .. first_expert + experts - 1."""
+    _expect(ids.dim() == 2, "ids has two dimensions")
+    _typed("ids", ids, _I32)
+    _typed("offsets_out", offsets_out, _I32, (experts + 1,))
+    _typed("position_out", position_out, _I32, ids.shape)
+    _on_current(ids, offsets_out, position_out)
+    _check(lib().ar_fusion_expert_plan(_ptr(ids), ids.shape[0], ids.shape[1], int(first_expert),
+                                       int(experts), _ptr(offsets_out), _ptr(position_out),
+                                       _stream(stream)))
+
+
+def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: torch.Tensor,
+                           position: torch.Tensor | None = None,
+                           activation: int = AR_ACT_NONE,
+                           row_count: torch.Tensor | None = None, stream=None) -> None:
+    """x [rows, hidden] ([rows, 2 * hidden] with AR_ACT_SILU_MUL); quant_out
+    [out_rows, hidden] (uint8 or float8_e4m3fn); scale_out [out_rows,
+    ceil(hidden / 128)] fp32; position [rows, copies] int32 or None; row_count: a
+    one-element int32 tensor or None (a view of the plan's last offset)."""
+    _typed("x", x, _ELEM)
+    _expect(x.dim() == 2 and quant_out.dim() == 2, "x and quant_out have two dimensions")
+    rows = x.shape[0]
+    out_rows, hidden = quant_out.shape
+    _typed("x", x, _ELEM, (rows, hidden * (2 if activation == AR_ACT_SILU_MUL else 1)))
+    _typed("quant_out", quant_out, _FP8)
+    _typed("scale_out", scale_out, _F32, (out_rows, _quant_blocks(hidden)))
+    copies = 1
+    if position is not None:
+        _expect(position.dim() == 2 and position.shape[0] == rows, "position is [rows, copies]")
+        _typed("position", position, _I32)
+        copies = position.shape[1]
+    if row_count is not None:
+        _typed("row_count", row_count, _I32)
+        _expect(row_count.numel() == 1, "row_count has one element")
+    _on_current(x, quant_out, scale_out, position, row_count)
+    _check(lib().ar_fusion_quant_blocks(_ptr(x), rows, hidden, _dtype_id(x), int(activation),
+                                        _ptr(position), copies, _ptr(row_count), out_rows,
+                                        _ptr(quant_out), _ptr(scale_out), _stream(stream)))
+
+
+def ar_fusion_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
+                         b_scale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """a [rows, depth], b [cols, depth] (uint8 or float8_e4m3fn); a_scale [rows,
+    ceil(depth / 128)], b_scale [ceil(cols / 128), ceil(depth / 128)] fp32; out [rows, cols]."""
+    _expect(a.dim() == 2 and b.dim() == 2, "a and b have two dimensions")
+    (rows, depth), cols = a.shape, b.shape[0]
+    blocks = _quant_blocks(depth)
+    _typed("a", a, _FP8)
+    _typed("b", b, _FP8, (cols, depth))
+    _typed("a_scale", a_scale, _F32, (rows, blocks))
+    _typed("b_scale", b_scale, _F32, (_quant_blocks(cols), blocks))
+    _typed("out", out, _ELEM, (rows, cols))
+    _on_current(a, a_scale, b, b_scale, out)
+    _check(lib().ar_fusion_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), rows, cols,
+                                      depth, _dtype_id(out), _ptr(out), _stream(stream)))
+
+
+def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
+                                b_scale: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor,
+                                stream=None) -> None:
+    """ar_fusion_matmul_fp8 by experts: b [experts, cols, depth], b_scale
+    [experts, ceil(cols / 128), ceil(depth / 128)], offsets [experts + 1] int32."""
+    _expect(a.dim() == 2 and b.dim() == 3, "a has two dimensions, b three")
+    (rows, depth), (experts, cols) = a.shape, b.shape[:2]
+    blocks = _quant_blocks(depth)
+    _typed("a", a, _FP8)
+    _typed("b", b, _FP8, (experts, cols, depth))
+    _typed("a_scale", a_scale, _F32, (rows, blocks))
+    _typed("b_scale", b_scale, _F32, (experts, _quant_blocks(cols), blocks))
+    _typed("offsets", offsets, _I32, (experts + 1,))
+    _typed("out", out, _ELEM, (rows, cols))
+    _on_current(a, a_scale, b, b_scale, offsets, out)
+    _check(lib().ar_fusion_expert_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
+                                             _ptr(offsets), experts, rows, cols, depth,
+                                             _dtype_id(out), _ptr(out), _stream(stream)))
+
+
+def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
+                      out: torch.Tensor, add: torch.Tensor | None = None, stream=None) -> None:
+    """rows_in [in_rows, hidden]; position (int32) and weights (fp32) [tokens,
+    topk]; out and add [tokens, hidden], of rows_in's type."""
+    _typed("rows_in", rows_in, _ELEM)
+    _expect(rows_in.dim() == 2 and position.dim() == 2, "rows_in and position have two dimensions")
+    in_rows, hidden = rows_in.shape
+    tokens, topk = position.shape
+    _typed("position", position, _I32)
+    _typed("weights", weights, _F32, (tokens, topk))
+    _typed("out", out, (rows_in.dtype,), (tokens, hidden))
+    if add is not None:
+        _typed("add", add, (rows_in.dtype,), (tokens, hidden))
+    _on_current(rows_in, position, weights, out, add)
+    _check(lib().ar_fusion_combine(_ptr(rows_in), in_rows, _ptr(position), _ptr(weights), tokens,
+                                   topk, hidden, _dtype_id(rows_in), _ptr(add), _ptr(out),
+                                   _stream(stream)))

@@ -446,6 +446,159 @@ int ar_fusion_run_noalloc(const void* const* partials, int nranks, int tokens, i
  * AR_ERR_CUDA if reading the status word fails. */
 int ar_fusion_noalloc_status(void* stream, int* detail);
 
+/* ------------------------------------------------- expert layers -- */
+
+/* The work between two fused epilogues of a mixture-of-experts layer (the
+ * pages stop at the epilogue; these calls have no counterpart there): the
+ * normed rows are routed to experts (ar_fusion_route), the routing becomes a
+ * row layout sorted by expert (ar_fusion_expert_plan), rows are quantised in
+ * blocks of 128 and written where that layout wants them
+ * (ar_fusion_quant_blocks), multiplied with 8-bit weights
+ * (ar_fusion_expert_matmul_fp8, or ar_fusion_matmul_fp8 where there are no
+ * experts), and combined back into token rows (ar_fusion_combine), which are
+ * a rank's partial of the next fused call.  A dense product writes a partial
+ * straight into the workspace through ar_fusion_workspace_partial_ptr in
+ * AR_MODE_BUFFER (its outputs may hold -0.0, which a Lamport slot may not).
+ *
+ * All of them are asynchronous on `stream`, run on the current device, take
+ * no workspace and keep nothing between calls, so calls on several streams
+ * and captured calls are independent of one another.  Arrays of elements,
+ * codes and outputs are 16-byte aligned; scales, weights, ids, positions,
+ * offsets and biases 4-byte aligned.  Outputs must not overlap inputs. */
+
+/* Experts, chosen experts and groups of one routing call. */
+#define AR_MAX_EXPERTS 1024
+#define AR_MAX_TOPK 32
+#define AR_MAX_GROUPS 32
+/* Elements that share a scale of the block quantiser and of the products. */
+#define AR_QUANT_BLOCK 128
+
+enum ar_score {
+    AR_SCORE_SOFTMAX = 0,     /* s = exp(x - max) / sum exp(x - max) over the row */
+    AR_SCORE_SIGMOID = 1      /* s = 1 / (1 + exp(-x)) */
+};
+
+/* Value of a group of experts, from the choice values c of its experts. */
+enum ar_group_score {
+    AR_GROUP_MAX = 0,         /* the largest */
+    AR_GROUP_TOP2 = 1         /* the sum of the two largest (of one where there is one) */
+};
+
+/* What ar_fusion_quant_blocks does before it quantises. */
+enum ar_activation {
+    AR_ACT_NONE = 0,          /* y = x, in [rows][hidden] */
+    AR_ACT_SILU_MUL = 1       /* y = g / (1 + exp(-g)) * u, in [rows][2 * hidden]: g then u */
+};
+
+/* Routing to experts.  For each token row x of `logits`:
+ *   s_e = score(x_e),  c_e = s_e + bias_e                       (choice value)
+ *   with groups > 1: group g holds experts [g * experts / groups, ...); the
+ *     groups_kept groups of largest group_score stay, the others' experts
+ *     are out;
+ *   ids[j] = expert of the j-th largest c among those left, j < topk;
+ *   weights[j] = scale * s_{ids[j]}, divided by the sum of the chosen s if
+ *     `renormalize`.
+ * The order is that of the c_e before any rounding to 32 bits; equal values go
+ * to the lower index, of experts and of groups.
+ * Masks: an expert whose logit or bias is -inf takes no part: it is in no
+ * softmax sum and no group, and never chosen.  Where fewer than topk experts
+ * are left, the slots behind the last one get id -1 and weight 0.  Any finite
+ * mask value is a number like the others.  A NaN choice value ranks below
+ * every number; ids stay distinct and in range, weights of that row that the
+ * NaN reaches are NaN.
+ *   logits       [tokens][experts] of `dtype`
+ *   experts      1..AR_MAX_EXPERTS;  topk 1..AR_MAX_TOPK, at most the experts
+ *                of groups_kept groups
+ *   bias         device [experts] fp32 or NULL; it moves the choice, not the weights
+ *   score        enum ar_score
+ *   groups       1..AR_MAX_GROUPS, divides experts;  groups_kept 1..groups
+ *   group_score  enum ar_group_score
+ *   renormalize  0 or 1;  scale: fp32 factor of the weights
+ *   ids_out      [tokens][topk] int32;  weights_out [tokens][topk] fp32
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, counts over the limits),
+ * AR_ERR_CUDA.  tokens == 0: nothing launched. */
+int ar_fusion_route(const void* logits, int tokens, int experts, int dtype, const float* bias,
+                    int score, int groups, int groups_kept, int group_score, int topk,
+                    int renormalize, float scale, int32_t* ids_out, float* weights_out,
+                    void* stream);
+
+/* Row layout sorted by expert.  The slots [tokens][topk] of `ids` that name a
+ * local expert (first_expert <= id < first_expert + experts) are numbered by
+ * expert, slots of one expert in slot order:
+ *   offsets_out[e]   first row of local expert e, offsets_out[experts] the number of
+ *                    rows in all; int32 [experts + 1]
+ *   position_out[t][j]  the slot's row, -1 for a slot of no local expert (an id of
+ *                    another rank's expert, or -1)
+ *   tokens >= 0 (0: the offsets are written as zeros), topk >= 1,
+ *   tokens * topk < 2^31;  experts 1..AR_MAX_EXPERTS.
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED, AR_ERR_CUDA. */
+int ar_fusion_expert_plan(const int32_t* ids, int tokens, int topk, int first_expert,
+                          int experts, int32_t* offsets_out, int32_t* position_out,
+                          void* stream);
+
+/* Block quantisation of rows to FP8 E4M3.  With y = x or the activation (fp32)
+ * and A the largest finite-or-infinite |y| of a block of AR_QUANT_BLOCK
+ * consecutive elements of a row (the last block may be shorter), at least
+ * 2^-100:
+ *   scale = A / 448,  code = E4M3(y * (448 / A))      (nearest even, saturating)
+ * A NaN element becomes the NaN code and does not enter A; an infinite one
+ * makes the block's scale infinite, itself NaN and the others zero.
+ *   in         [rows][hidden] of `dtype` ([rows][2 * hidden] with AR_ACT_SILU_MUL)
+ *   hidden     multiple of 16
+ *   position   NULL: row t is written to row t (copies must be 1).  Else int32
+ *              [rows][copies]: row t is written to row position[t][j] for each
+ *              j; entries outside 0..out_rows - 1 are skipped; no two may be equal
+ *   row_count  NULL, or a device int32: rows t >= *row_count are not read
+ *              (offsets_out + experts of the plan, where not every slot is local)
+ *   out_rows   rows of the outputs; at least `rows` without position
+ *   quant_out  [out_rows][hidden] E4M3 bytes
+ *   scale_out  [out_rows][ceil(hidden / 128)] fp32
+ * Rows that nothing is written to are left as they were.
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int activation,
+                           const int32_t* position, int copies, const int32_t* row_count,
+                           int out_rows, void* quant_out, float* scale_out, void* stream);
+
+/* Product of FP8 E4M3 matrices with a scale per block of 128:
+ *   out[m][n] = sum_b a_scale[m][b] * b_scale[n / 128][b]
+ *                 * sum_{k in block b} a[m][k] * b[n][k]
+ * (block b: k from 128 b to 128 b + 127 or the end), sums in fp32, rounded to
+ * the output type once.
+ *   a          [rows][depth] E4M3;  a_scale [rows][ceil(depth / 128)] fp32
+ *   b          [cols][depth] E4M3;  b_scale [ceil(cols / 128)][ceil(depth / 128)] fp32
+ *   rows       >= 0 (0: nothing launched);  cols >= 1;  depth multiple of 16, >= 16
+ *   dtype      enum ar_dtype of out;  out [rows][cols]
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+int ar_fusion_matmul_fp8(const void* a, const float* a_scale, const void* b,
+                         const float* b_scale, int rows, int cols, int depth, int dtype,
+                         void* out, void* stream);
+
+/* The same product by experts: rows offsets[e] <= m < offsets[e + 1] of a are
+ * multiplied with expert e's matrix.
+ *   b        [experts][cols][depth];  b_scale [experts][ceil(cols / 128)][ceil(depth / 128)]
+ *   offsets  device int32 [experts + 1], not decreasing, read on the device (no
+ *            host synchronisation); values are clamped to 0..rows
+ *   experts  1..AR_MAX_EXPERTS;  rows: rows of a and out, an upper bound of
+ *            offsets[experts]
+ * Rows of no expert are left as they were.  Errors as ar_fusion_matmul_fp8. */
+int ar_fusion_expert_matmul_fp8(const void* a, const float* a_scale, const void* b,
+                                const float* b_scale, const int32_t* offsets, int experts,
+                                int rows, int cols, int depth, int dtype, void* out,
+                                void* stream);
+
+/* Expert rows back to token rows:
+ *   out[t] = add[t] + sum_j weights[t][j] * rows_in[position[t][j]]
+ * in fp32, add first, then j in order, rounded to the element type once.
+ * Positions outside 0..in_rows - 1 are skipped; a token without any gets add[t]
+ * (or zeros).
+ *   rows_in   [in_rows][hidden] of `dtype`;  hidden multiple of 8
+ *   position  int32 [tokens][topk];  weights fp32 [tokens][topk];  topk >= 1
+ *   add       [tokens][hidden] of `dtype` or NULL;  out [tokens][hidden]
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
+                      const float* weights, int tokens, int topk, int hidden, int dtype,
+                      const void* add, void* out, void* stream);
+
 /* ---------------------------------------------------------- utilities -- */
 
 /* Message for the last failed call on this thread ("" if none). */
