@@ -159,6 +159,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ar_fusion_expert_matmul_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
                                               _vp]
     L.ar_fusion_combine.argtypes = [_vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]
+    L.ar_fusion_matmul_status.argtypes = [_vp, ctypes.POINTER(_i)]
     for name in ("ar_fusion_workspace_bytes", "ar_fusion_workspace_create",
                  "ar_fusion_workspace_destroy", "ar_fusion_workspace_info",
                  "ar_fusion_workspace_copy_state", "ar_fusion_workspace_status",
@@ -171,7 +172,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "ar_fusion_run", "ar_fusion_norm_amax",
                  "ar_fusion_sum", "ar_fusion_run_noalloc", "ar_fusion_noalloc_status",
                  "ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",
-                 "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8", "ar_fusion_combine"):
+                 "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8", "ar_fusion_combine",
+                 "ar_fusion_matmul_status"):
         getattr(L, name).restype = _i
     _lib = L
     return L
@@ -584,6 +586,17 @@ def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch
     _check(lib().ar_fusion_expert_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
                                              _ptr(offsets), experts, rows, cols, depth,
                                              _dtype_id(out), _ptr(out), _stream(stream)))
+
+
+def ar_fusion_matmul_status(stream=None):
+    """(status, detail) of the products on the current device: the first
+    device-side error since the previous query (AR_OK if none), which the query
+    clears.  Synchronises the stream."""
+    d = ctypes.c_int(-1)
+    rc = lib().ar_fusion_matmul_status(_stream(stream), ctypes.byref(d))
+    if rc not in (AR_OK, AR_ERR_TIMEOUT):
+        _check(rc)
+    return rc, d.value
 
 
 def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,

@@ -48,6 +48,9 @@ int check_matmul(const MatmulArgs& m, int dtype)
         return efail(AR_ERR_INVALID, "experts %d < 1", m.experts);
     if (m.experts > AR_MAX_EXPERTS)
         return efail(AR_ERR_UNSUPPORTED, "experts %d > %d", m.experts, AR_MAX_EXPERTS);
+    if ((long long)m.experts * m.cols > INT_MAX - 256 || m.rows > INT_MAX - 256)
+        return efail(AR_ERR_UNSUPPORTED, "experts %d x cols %d or rows %d beyond 2^31 - 257",
+                     m.experts, m.cols, m.rows);
     if (m.rows == 0)
         return AR_OK;
     if (!aligned(m.a, 16) || !aligned(m.b, 16) || !aligned(m.out, 16))

@@ -1,105 +1,127 @@
-// Product of FP8 E4M3 matrices with an fp32 scale per block of 128, dense or
-// by experts: out = sum over blocks of sa * sb * (a . b), in fp32.
-//
-// A 64 x 64 tile per thread block, 4 x 4 outputs per thread, 32 of the depth
-// at a time through shared memory as fp32.
-#include "expert_internal.h"
-#include "expert_vec.cuh"
+// Host side of the 8-bit products: tensor maps, the choice of kernel, and the
+// status words of their bounded waits.
+#include <mutex>
+
+#include "ar_internal.h"
+#include "matmul_internal.h"
 
 namespace arf {
 namespace {
 
-constexpr int kTile = 64, kStep = 32;
+// code and detail of the first wait that gave up, per device
+__device__ int g_status[2];
 
-template <class D>
-__device__ __forceinline__ void store1(void* out, uint64_t i, float v)
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
 {
-    if constexpr (D::bytes == 4)
-        static_cast<float*>(out)[i] = v;
-    else if constexpr (D::id == AR_DT_BF16)
-        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(out)[i] = __float2half_rn(v);
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                               cudaEnableDefault, &r);
+        return e == cudaSuccess && r == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiled>(p)
+                   : nullptr;
+    }();
+    return fn;
 }
 
-template <class D>
-__global__ void __launch_bounds__(256) matmul_kernel(MatmulArgs a)
+// Looked up once per device
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+DeviceInfo g_info[kMaxDevices] = {};
+
+cudaError_t device_info(DeviceInfo* out)
 {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
-    const int e = blockIdx.z;
-    int row0 = 0, row1 = a.rows;
-    if (a.offsets) {
-        row0 = min(max(a.offsets[e], 0), a.rows);
-        row1 = min(max(a.offsets[e + 1], row0), a.rows);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceInfo& d = g_info[dev];
+    if (!d.status) {
+        int sms = 0;
+        void* p = nullptr;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaGetSymbolAddress(&p, g_status);
+        if (e != cudaSuccess)
+            return e;
+        d.sms = sms;
+        d.status = static_cast<int*>(p);
     }
-    const int nb = (a.depth + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK;
-    const int ncb = (a.cols + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK;
-    const int n0 = blockIdx.x * kTile;
-    const uint8_t* b = a.b + (uint64_t)e * a.cols * a.depth;
-    const float* sb = a.sb + ((uint64_t)e * ncb + n0 / AR_QUANT_BLOCK) * nb;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t m0 = row0 + (int64_t)blockIdx.y * kTile; m0 < row1;
-         m0 += (int64_t)gridDim.y * kTile) {
-        float acc[4][4] = {};
-        for (int kb = 0; kb < nb; ++kb) {
-            float part[4][4] = {};
-            const int kend = min(a.depth, (kb + 1) * AR_QUANT_BLOCK);
-            for (int k0 = kb * AR_QUANT_BLOCK; k0 < kend; k0 += kStep) {
-                __syncthreads();
-                for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-                    const int r = i / kStep, k = i % kStep;
-                    const bool in = k0 + k < kend;
-                    as[k][r] = in && m0 + r < row1
-                                   ? e4m3_to_f32(a.a[(uint64_t)(m0 + r) * a.depth + k0 + k])
-                                   : 0.0f;
-                    bs[k][r] = in && n0 + r < a.cols
-                                   ? e4m3_to_f32(b[(uint64_t)(n0 + r) * a.depth + k0 + k])
-                                   : 0.0f;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < kStep; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            part[i][j] = fmaf(as[k][ty + 16 * i], bs[k][tx + 16 * j], part[i][j]);
-            }
-            const float sbk = sb[kb];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t m = m0 + ty + 16 * i;
-                const float s = m < row1 ? a.sa[(uint64_t)m * nb + kb] * sbk : 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(part[i][j], s, acc[i][j]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty + 16 * i;
-                const int n = n0 + tx + 16 * j;
-                if (m < row1 && n < a.cols)
-                    store1<D>(a.out, (uint64_t)m * a.cols + n, acc[i][j]);
-            }
-    }
+    *out = d;
+    return cudaSuccess;
 }
 
 }  // namespace
 
+bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t depth,
+                     uint32_t box_rows)
+{
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {depth, rows};
+    const cuuint64_t strides[1] = {depth};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t steps[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_matmul(int dtype, const MatmulArgs& a, cudaStream_t s)
 {
+    DeviceInfo d;
+    const cudaError_t e = device_info(&d);
+    if (e != cudaSuccess)
+        return e;
     const int per = (a.rows + a.experts - 1) / a.experts;
-    const int my = (per + kTile - 1) / kTile;
-    const dim3 grid((a.cols + kTile - 1) / kTile, my > 1024 ? 1024 : my, a.experts);
-    switch (dtype) {
-    case AR_DT_BF16: matmul_kernel<Bf16><<<grid, 256, 0, s>>>(a); break;
-    case AR_DT_FP16: matmul_kernel<Fp16><<<grid, 256, 0, s>>>(a); break;
-    default: matmul_kernel<F32><<<grid, 256, 0, s>>>(a); break;
-    }
-    return cudaGetLastError();
+    const int tokens = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+    if (per > 128)
+        return launch_matmul_wide(dtype, a, d, s);
+    // blocks without a split, and the split that fills two blocks per SM
+    const int64_t blocks = (int64_t)((a.cols + 127) / 128) *
+                           (a.experts < a.rows ? a.experts : a.rows);
+    int split = 1;
+    while (split < 8 && blocks * split * 2 <= 2 * d.sms && split * 2 <= quant_blocks(a.depth))
+        split *= 2;
+    return launch_matmul_narrow(dtype, a, tokens, split, d, s);
 }
 
 }  // namespace arf
+
+extern "C" int ar_fusion_matmul_status(void* stream, int* detail)
+{
+    using namespace arf;
+    if (detail)
+        *detail = -1;
+    DeviceInfo d;
+    cudaError_t e = device_info(&d);
+    int st[2] = {0, 0};
+    const int clear[2] = {0, 0};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (e == cudaSuccess)
+        e = cudaMemcpyAsync(st, d.status, sizeof st, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && st[0] != 0) {
+        e = cudaMemcpyAsync(d.status, clear, sizeof clear, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(s);
+    }
+    if (e != cudaSuccess)
+        return set_last_error(AR_ERR_CUDA, cudaGetErrorString(e));
+    if (st[0] == 0)
+        return AR_OK;
+    if (detail)
+        *detail = st[1];
+    return set_last_error(st[0], "a product's device-side wait gave up");
+}

@@ -1,0 +1,28 @@
+// The two kernels behind the 8-bit products and what they share on the host.
+#pragma once
+
+#include <cuda.h>
+
+#include "expert_internal.h"
+
+namespace arf {
+
+// A byte matrix [rows][depth] read in boxes of box_rows x 128 bytes, 128-byte
+// swizzle, zeros outside.  False if the driver refuses.
+bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t depth,
+                     uint32_t box_rows);
+
+struct DeviceInfo {
+    int sms;
+    int* status;                // device status words of the products: code, detail
+};
+
+// Tokens on the lanes of tensor memory, 128 x 256 outputs per block: many rows.
+cudaError_t launch_matmul_wide(int dtype, const MatmulArgs& a, const DeviceInfo& d,
+                               cudaStream_t s);
+// Weights on the lanes, `tokens` (16, 32, 64 or 128) rows at a time, the depth
+// split over `split` blocks of a cluster: few rows per expert.
+cudaError_t launch_matmul_narrow(int dtype, const MatmulArgs& a, int tokens, int split,
+                                 const DeviceInfo& d, cudaStream_t s);
+
+}  // namespace arf

@@ -1,0 +1,324 @@
+// 8-bit product for few rows per expert: the weights are read once and bound
+// the time, so they take the 128 lanes of tensor memory (128 columns of the
+// output per block) and the token rows its columns, 16 to 128 at a time.
+//
+// The depth is split over the blocks of a cluster where one block per 128
+// columns would leave SMs idle; their fp32 sums meet in distributed shared
+// memory, added in rank order by the block that stores them, so no workspace
+// and no atomics are needed and the result does not depend on timing.
+//
+// Each block of 128 of the depth goes to a tensor-memory buffer of its own and
+// is added, times sa * sb, to fp32 registers: a thread has one column of the
+// output, the rows' scales come through shared memory.
+//
+// Shared memory is sized so that at most two blocks share an SM, which keeps
+// their tensor memory (256 columns each at most) within the SM's 512: no block
+// of a cluster can wait for tensor memory that waits for its cluster.
+//
+// Warps 0-3: add and store; warp 4: copies; warp 5: products.
+#include "matmul_internal.h"
+#include "tensor_core.cuh"
+
+namespace arf {
+namespace {
+
+constexpr int kN = 128, kK = 128;          // columns per block, depth per step
+constexpr int kBytesW = kN * kK;
+constexpr int kThreads = 192;
+constexpr int kMaxStages = 10;
+constexpr int kScaleSlots = 4;
+
+__host__ __device__ constexpr int buffers(int tokens) { return tokens <= 64 ? 4 : 2; }
+
+template <class D>
+__device__ __forceinline__ void store1(void* out, uint64_t i, float v)
+{
+    if constexpr (D::bytes == 4)
+        static_cast<float*>(out)[i] = v;
+    else if constexpr (D::id == AR_DT_BF16)
+        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(out)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(const float* local, unsigned rank)
+{
+    uint32_t ra;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    return v;
+}
+
+template <class D, int TOK>
+__global__ void __launch_bounds__(kThreads)
+    matmul_narrow_kernel(const __grid_constant__ CUtensorMap map_a,
+                         const __grid_constant__ CUtensorMap map_b, MatmulArgs a, int* status,
+                         int split, int stages)
+{
+    constexpr int kBufs = buffers(TOK);
+    constexpr uint32_t kCols = TOK * kBufs;
+    constexpr int kStage = kBytesW + TOK * kK;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(16) float scale_sh[kScaleSlots][TOK];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kBufs + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    const int e = blockIdx.z;
+    int row0 = 0, row1 = a.rows;
+    if (a.offsets) {
+        row0 = min(max(a.offsets[e], 0), a.rows);
+        row1 = min(max(a.offsets[e + 1], row0), a.rows);
+    }
+    // the same for every block of the cluster: all leave, or none
+    if (row0 + (int64_t)blockIdx.y * TOK >= row1)
+        return;
+
+    const uint32_t stage0 = (smem_u32(dyn) + 1023u) & ~1023u;
+    float* sums = reinterpret_cast<float*>(dyn + (stage0 - smem_u32(dyn)) + stages * kStage);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages,
+                   tfull = empty + 8 * kMaxStages, tempty = tfull + 8 * kBufs,
+                   done = tempty + 8 * kBufs;
+    const Bail bail{&dead, status};
+    if (tid == 0) {
+        dead = 0;
+        for (int s = 0; s < stages; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < kBufs; ++b) {
+            bar_init(tfull + 8 * b, 1);
+            bar_init(tempty + 8 * b, 4);
+        }
+        bar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+    }
+    if (warp == 5)
+        tmem_alloc(smem_u32(&tmem_slot), kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    const int rank = blockIdx.x % split;
+    const int n0 = blockIdx.x / split * kN;
+    const int nkb = (a.depth + kK - 1) / kK;
+    const int kb0 = (int)((int64_t)nkb * rank / split), kb1 = (int)((int64_t)nkb * (rank + 1) / split);
+    const int64_t step = (int64_t)gridDim.y * TOK;
+
+    // per role: position in the ring of stages and of tensor-memory buffers
+    uint32_t s = 0, ph = 0, it = 0, issued = 0;
+    bool ok = true;
+    for (int64_t m0 = row0 + (int64_t)blockIdx.y * TOK; m0 < row1; m0 += step) {
+        if (warp == 4) {
+            if (lane == 0) {
+                const int brow = e * a.cols + n0;
+                for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                    if (!(ok = bar_wait(empty + 8 * s, ph ^ 1, bail, 1)))
+                        break;
+                    const uint32_t at = stage0 + s * kStage;
+                    bar_expect(full + 8 * s, kStage);
+                    tma_load_2d(at, &map_b, full + 8 * s, kb * kK, brow);
+                    tma_load_2d(at + kBytesW, &map_a, full + 8 * s, kb * kK, (int)m0);
+                    ++issued;
+                    if (++s == (uint32_t)stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 5) {
+            if (lane == 0) {
+                constexpr uint32_t idesc = fp8_idesc(kN, TOK);
+                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                    const uint32_t b = it % kBufs;
+                    if (!(ok = bar_wait(tempty + 8 * b, (it / kBufs & 1) ^ 1, bail, 2)) ||
+                        !(ok = bar_wait(full + 8 * s, ph, bail, 3)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t dw = smem_desc(stage0 + s * kStage);
+                    const uint64_t dx = smem_desc(stage0 + s * kStage + kBytesW);
+#pragma unroll
+                    for (int k = 0; k < kK / 32; ++k)
+                        mma_fp8(tmem + b * TOK, dw + 2 * k, dx + 2 * k, idesc, k > 0);
+                    mma_commit(empty + 8 * s);
+                    mma_commit(tfull + 8 * b);
+                    if (++s == (uint32_t)stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            const int have = (int)min((int64_t)TOK, row1 - m0);
+            const int n = n0 + tid;
+            const int ncb = (a.cols + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK;
+            const float* sb = a.sb + ((uint64_t)e * ncb + n0 / AR_QUANT_BLOCK) * nkb;
+            const float* sa = a.sa + (uint64_t)(m0 + (tid < have ? tid : 0)) * nkb;
+            uint64_t acc[TOK / 2];
+#pragma unroll
+            for (int i = 0; i < TOK / 2; ++i)
+                acc[i] = 0ull;
+            float next = tid < TOK && kb0 < kb1 ? sa[kb0] * sb[kb0] : 0.0f;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                // a slot is read no later than one barrier after this one: of
+                // four slots the one written here is out of use
+                if (tid < TOK)
+                    scale_sh[it % kScaleSlots][tid] = next;
+                if (tid < TOK && kb + 1 < kb1)
+                    next = sa[kb + 1] * sb[kb + 1];
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const uint32_t b = it % kBufs;
+                ok = ok && __all_sync(0xffffffffu, bar_wait(tfull + 8 * b, it / kBufs & 1, bail, 4));
+                if (!ok)
+                    continue;           // the barrier above still counts every warp
+                tc_fence_after();
+                const float4* sc = reinterpret_cast<const float4*>(scale_sh[it % kScaleSlots]);
+                const uint32_t from = tmem + ((uint32_t)(32 * warp) << 16) + b * TOK;
+                uint32_t d[2][16];
+                tmem_ld16(from, d[0]);
+#pragma unroll
+                for (int c = 0; c < TOK / 16; ++c) {
+                    tmem_wait(d[c & 1]);
+                    if (c + 1 < TOK / 16)
+                        tmem_ld16(from + 16 * (c + 1), d[(c + 1) & 1]);
+                    if (c + 1 == TOK / 16) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(tempty + 8 * b);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = sc[4 * c + i];
+                        fma_pair(acc[8 * c + 2 * i],
+                                 pack_pair(d[c & 1][4 * i], d[c & 1][4 * i + 1]),
+                                 pack_pair(__float_as_uint(f.x), __float_as_uint(f.y)));
+                        fma_pair(acc[8 * c + 2 * i + 1],
+                                 pack_pair(d[c & 1][4 * i + 2], d[c & 1][4 * i + 3]),
+                                 pack_pair(__float_as_uint(f.z), __float_as_uint(f.w)));
+                    }
+                }
+            }
+            if (split == 1) {
+                if (ok && n < a.cols) {
+#pragma unroll
+                    for (int i = 0; i < TOK / 2; ++i) {
+                        const float2 f = unpack_pair(acc[i]);
+                        if (2 * i < have)
+                            store1<D>(a.out, (uint64_t)(m0 + 2 * i) * a.cols + n, f.x);
+                        if (2 * i + 1 < have)
+                            store1<D>(a.out, (uint64_t)(m0 + 2 * i + 1) * a.cols + n, f.y);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < TOK / 2; ++i) {
+                    const float2 f = unpack_pair(acc[i]);
+                    sums[(2 * i) * kN + tid] = f.x;
+                    sums[(2 * i + 1) * kN + tid] = f.y;
+                }
+            }
+        }
+        if (split > 1) {
+            cluster_barrier();
+            if (warp < 4) {
+                const int have = (int)min((int64_t)TOK, row1 - m0);
+                const int n = n0 + tid;
+                for (int c = rank; c < have; c += split) {
+                    float v = 0.0f;
+                    for (int q = 0; q < split; ++q)
+                        v += ld_dsmem_f32(sums + c * kN + tid, q);
+                    if (n < a.cols)
+                        store1<D>(a.out, (uint64_t)(m0 + c) * a.cols + n, v);
+                }
+            }
+            cluster_barrier();
+        }
+    }
+    if (!ok && lane == 0) {
+        if (warp == 4) {
+            // a block that gave up waits for its copies in flight
+            for (uint32_t i = 0; i < (uint32_t)stages && i < issued; ++i) {
+                ph ^= s == 0;
+                s = s == 0 ? stages - 1 : s - 1;
+                bar_drain(full + 8 * s, ph);
+            }
+        } else if (warp == 5) {
+            mma_commit(done);
+            bar_drain(done, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5)
+        tmem_free(tmem, kCols);
+}
+
+template <class D, int TOK>
+cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaStream_t s)
+{
+    CUtensorMap map_a, map_b;
+    if (!byte_tensor_map(&map_a, a.a, (uint64_t)a.rows, (uint64_t)a.depth, TOK) ||
+        !byte_tensor_map(&map_b, a.b, (uint64_t)a.experts * a.cols, (uint64_t)a.depth, kN))
+        return cudaErrorInvalidValue;
+    constexpr int kStage = kBytesW + TOK * kK;
+    // two blocks per SM (112 KB each) up to 64 rows at a time, else one
+    const int budget = TOK <= 64 ? 108 * 1024 : 200 * 1024;
+    const int sums = split > 1 ? TOK * kN * 4 : 0;
+    int stages = (budget - sums - 1024) / kStage;
+    stages = stages > kMaxStages ? kMaxStages : stages;
+    const int smem = budget;        // the whole of it: never three blocks per SM
+    const auto kernel = matmul_narrow_kernel<D, TOK>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               smem);
+    if (e != cudaSuccess)
+        return e;
+    const int per = (a.rows + a.experts - 1) / a.experts;
+    const int y = (per + TOK - 1) / TOK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.cols + kN - 1) / kN) * split, y > 65535 ? 65535 : y, a.experts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, d.status, split, stages);
+}
+
+template <class D>
+cudaError_t launch_d(const MatmulArgs& a, int tokens, int split, const DeviceInfo& d,
+                     cudaStream_t s)
+{
+    switch (tokens) {
+    case 16: return launch_t<D, 16>(a, split, d, s);
+    case 32: return launch_t<D, 32>(a, split, d, s);
+    case 64: return launch_t<D, 64>(a, split, d, s);
+    default: return launch_t<D, 128>(a, split, d, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_narrow(int dtype, const MatmulArgs& a, int tokens, int split,
+                                 const DeviceInfo& d, cudaStream_t s)
+{
+    switch (dtype) {
+    case AR_DT_BF16: return launch_d<Bf16>(a, tokens, split, d, s);
+    case AR_DT_FP16: return launch_d<Fp16>(a, tokens, split, d, s);
+    default: return launch_d<F32>(a, tokens, split, d, s);
+    }
+}
+
+}  // namespace arf

@@ -1,0 +1,201 @@
+// sm_103a building blocks of the 8-bit products: mbarriers with bounded waits,
+// tensor-map copies, tcgen05 matrix instructions and tensor memory.
+#pragma once
+
+#include <cuda.h>
+
+#include "expert_vec.cuh"
+
+namespace arf {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ------------------------------------------------------------- mbarriers
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile(
+        "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Every wait ends: after kWaitNs, or as soon as another wait of the block gave
+// up (*dead), it returns false, and the first one to give up records
+// AR_ERR_TIMEOUT and `where` in the device's status words.
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct Bail {
+    volatile int* dead;         // shared memory
+    int* status;                // device status words: code, detail
+};
+
+__device__ __noinline__ inline bool bar_wait_slow(uint32_t bar, uint32_t parity, const Bail& b,
+                                                  int where)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!bar_try(bar, parity)) {
+        if (*b.dead)
+            return false;
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            *b.dead = 1;
+            if (atomicCAS(b.status, 0, AR_ERR_TIMEOUT) == 0)
+                atomicExch(b.status + 1, where);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Bail& b, int where)
+{
+    return bar_try(bar, parity) || bar_wait_slow(bar, parity, b, where);
+}
+// A last wait for work in flight, taken only after the block gave up.
+__device__ __noinline__ inline void bar_drain(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!bar_try(bar, parity) && globaltimer_ns() - t0 < 200000000ull) {
+    }
+}
+
+// ------------------------------------------------------ tensor-map copies
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// -------------------------------------------------- tcgen05: tensor memory
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 16 columns of this warp's 32 lanes: register i is column i of the thread's
+// lane.  The registers may be read after tmem_wait on the same array.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&d)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),
+          "=r"(d[7]), "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]),
+          "=r"(d[14]), "=r"(d[15])
+        : "r"(addr));
+}
+// Waits for this thread's loads; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&d)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3]), "+r"(d[4]), "+r"(d[5]),
+                   "+r"(d[6]), "+r"(d[7]), "+r"(d[8]), "+r"(d[9]), "+r"(d[10]), "+r"(d[11]),
+                   "+r"(d[12]), "+r"(d[13]), "+r"(d[14]), "+r"(d[15])
+                 :
+                 : "memory");
+}
+
+// ----------------------------------------------- tcgen05: matrix products
+
+// Shared-memory operand: K-major rows of 128 bytes in the 128-byte swizzle, 8
+// rows per 1024-byte group (stride 1024 >> 4 = 64; the leading offset is
+// unused for this layout; descriptor version 1; swizzle code 2).  A step of 32
+// bytes along K within the 128 adds 2 to the address field.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// E4M3 x E4M3 -> fp32, both K-major, M x N per instruction
+__host__ __device__ constexpr uint32_t fp8_idesc(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// d (+)= a * b over 32 of K, by one thread
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// one arrival on `bar` once every product issued so far by this thread is done
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+// ----------------------------------------------------- packed fp32 pairs
+
+__device__ __forceinline__ uint64_t pack_pair(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_pair(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+// acc = d * s + acc in both halves, each rounded once
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t d, uint64_t s)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
+}
+
+}  // namespace arf

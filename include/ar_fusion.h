@@ -563,12 +563,14 @@ int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int 
  *   out[m][n] = sum_b a_scale[m][b] * b_scale[n / 128][b]
  *                 * sum_{k in block b} a[m][k] * b[n][k]
  * (block b: k from 128 b to 128 b + 127 or the end), sums in fp32, rounded to
- * the output type once.
+ * the output type once.  Device-side waits are bounded (2 s each); one that
+ * gives up leaves the outputs undefined and is reported by
+ * ar_fusion_matmul_status.
  *   a          [rows][depth] E4M3;  a_scale [rows][ceil(depth / 128)] fp32
  *   b          [cols][depth] E4M3;  b_scale [ceil(cols / 128)][ceil(depth / 128)] fp32
  *   rows       >= 0 (0: nothing launched);  cols >= 1;  depth multiple of 16, >= 16
  *   dtype      enum ar_dtype of out;  out [rows][cols]
- * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, sizes near 2^31), AR_ERR_CUDA. */
 int ar_fusion_matmul_fp8(const void* a, const float* a_scale, const void* b,
                          const float* b_scale, int rows, int cols, int depth, int dtype,
                          void* out, void* stream);
@@ -585,6 +587,14 @@ int ar_fusion_expert_matmul_fp8(const void* a, const float* a_scale, const void*
                                 const float* b_scale, const int32_t* offsets, int experts,
                                 int rows, int cols, int depth, int dtype, void* out,
                                 void* stream);
+
+/* Device-side status of the two products on the current device: synchronises
+ * `stream`, returns AR_OK or the first error recorded since the previous query
+ * (AR_ERR_TIMEOUT), and clears it.  *detail (may be NULL) receives which wait
+ * gave up (1: the copies for a free stage, 2: the products for a free
+ * accumulator, 3: for data, 4: the sums for products) or -1.  AR_ERR_CUDA if
+ * reading the status fails. */
+int ar_fusion_matmul_status(void* stream, int* detail);
 
 /* Expert rows back to token rows:
  *   out[t] = add[t] + sum_j weights[t][j] * rows_in[position[t][j]]
