@@ -213,7 +213,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building the Stream object takes 2.8 us, most of a launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -450,40 +451,58 @@ def ar_fusion_noalloc_status(stream=None):
 
 # ----------------------------------------------------------- expert layers
 
-def _expect(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
+class _Refused(Exception):
+    """An operand failed the quick check; the caller's slow check names it."""
 
 
-def _typed(name: str, t: torch.Tensor, dtypes, shape=None) -> None:
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported type {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _operand(t: torch.Tensor, dtypes, shape, dev: int):
+    if (t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise _Refused
 
 
-def _on_current(*ts) -> None:
-    """The library launches on the current device: operands of another one are refused."""
-    dev = None
-    for t in ts:
+def _device_of(t: torch.Tensor) -> int:
+    """The operands' device, which is the current one: the library launches there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _Refused
+    return dev
+
+
+def _explain(*operands) -> None:
+    """Names what is wrong with (name, tensor or None, types, shape or None): types
+    and shapes of all of them first, then where they are and how they lie."""
+    for name, t, dtypes, shape in operands:
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: unsupported type {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for name, t, _, _ in operands:
         if t is None:
             continue
         if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"expected tensors of the current device cuda:{dev}, got {t.device}")
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {t.device}, and the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+    raise ValueError("operands do not fit together")
 
 
-_ELEM = (torch.bfloat16, torch.float16, torch.float32)
+def _dims(n: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t.dim() != n:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected {n}")
+
+
+_ELEM = {torch.bfloat16: AR_DT_BF16, torch.float16: AR_DT_FP16, torch.float32: AR_DT_FP32}
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
-
-
-def _quant_blocks(depth: int) -> int:
-    return (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
 
 
 def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: torch.Tensor,
@@ -492,19 +511,22 @@ def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: to
                     renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
     """logits [tokens, experts]; bias [experts] fp32 or None; ids_out (int32)
     and weights_out (fp32) [tokens, topk]."""
-    _typed("logits", logits, _ELEM)
-    _expect(logits.dim() == 2 and ids_out.dim() == 2, "logits and ids_out have two dimensions")
+    _dims(2, logits=logits, ids_out=ids_out)
     tokens, experts = logits.shape
     topk = ids_out.shape[1]
-    _typed("ids_out", ids_out, _I32, (tokens, topk))
-    _typed("weights_out", weights_out, _F32, (tokens, topk))
-    if bias is not None:
-        _typed("bias", bias, _F32, (experts,))
-    _on_current(logits, bias, ids_out, weights_out)
-    _check(lib().ar_fusion_route(_ptr(logits), tokens, experts, _dtype_id(logits), _ptr(bias),
-                                 int(score), int(groups), int(groups_kept), int(group_score),
-                                 topk, int(renormalize), ctypes.c_float(scale), _ptr(ids_out),
-                                 _ptr(weights_out), _stream(stream)))
+    slots = (tokens, topk)
+    try:
+        dev = _device_of(logits)
+        args = (_operand(logits, _ELEM, (tokens, experts), dev), tokens, experts,
+                _ELEM[logits.dtype],
+                None if bias is None else _operand(bias, _F32, (experts,), dev), score, groups,
+                groups_kept, group_score, topk, 1 if renormalize else 0, scale,
+                _operand(ids_out, _I32, slots, dev), _operand(weights_out, _F32, slots, dev),
+                _stream(stream))
+    except _Refused:
+        _explain(("logits", logits, _ELEM, None), ("ids_out", ids_out, _I32, slots),
+                 ("weights_out", weights_out, _F32, slots), ("bias", bias, _F32, (experts,)))
+    _check(lib().ar_fusion_route(*args))
 
 
 def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Tensor,
@@ -512,14 +534,17 @@ def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Te
                           stream=None) -> None:
     """ids [tokens, topk] int32; offsets_out [experts + 1] and position_out
     [tokens, topk] int32, for the experts first_expert .. first_expert + experts - 1."""
-    _expect(ids.dim() == 2, "ids has two dimensions")
-    _typed("ids", ids, _I32)
-    _typed("offsets_out", offsets_out, _I32, (experts + 1,))
-    _typed("position_out", position_out, _I32, ids.shape)
-    _on_current(ids, offsets_out, position_out)
-    _check(lib().ar_fusion_expert_plan(_ptr(ids), ids.shape[0], ids.shape[1], int(first_expert),
-                                       int(experts), _ptr(offsets_out), _ptr(position_out),
-                                       _stream(stream)))
+    _dims(2, ids=ids)
+    slots = ids.shape
+    try:
+        dev = _device_of(ids)
+        args = (_operand(ids, _I32, slots, dev), slots[0], slots[1], first_expert, experts,
+                _operand(offsets_out, _I32, (experts + 1,), dev),
+                _operand(position_out, _I32, slots, dev), _stream(stream))
+    except _Refused:
+        _explain(("ids", ids, _I32, None), ("offsets_out", offsets_out, _I32, (experts + 1,)),
+                 ("position_out", position_out, _I32, slots))
+    _check(lib().ar_fusion_expert_plan(*args))
 
 
 def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: torch.Tensor,
@@ -530,42 +555,51 @@ def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: 
     [out_rows, hidden] (uint8 or float8_e4m3fn); scale_out [out_rows,
     ceil(hidden / 128)] fp32; position [rows, copies] int32 or None; row_count: a
     one-element int32 tensor or None (a view of the plan's last offset)."""
-    _typed("x", x, _ELEM)
-    _expect(x.dim() == 2 and quant_out.dim() == 2, "x and quant_out have two dimensions")
+    _dims(2, x=x, quant_out=quant_out)
     rows = x.shape[0]
     out_rows, hidden = quant_out.shape
-    _typed("x", x, _ELEM, (rows, hidden * (2 if activation == AR_ACT_SILU_MUL else 1)))
-    _typed("quant_out", quant_out, _FP8)
-    _typed("scale_out", scale_out, _F32, (out_rows, _quant_blocks(hidden)))
     copies = 1
     if position is not None:
-        _expect(position.dim() == 2 and position.shape[0] == rows, "position is [rows, copies]")
-        _typed("position", position, _I32)
+        _dims(2, position=position)
         copies = position.shape[1]
-    if row_count is not None:
-        _typed("row_count", row_count, _I32)
-        _expect(row_count.numel() == 1, "row_count has one element")
-    _on_current(x, quant_out, scale_out, position, row_count)
-    _check(lib().ar_fusion_quant_blocks(_ptr(x), rows, hidden, _dtype_id(x), int(activation),
-                                        _ptr(position), copies, _ptr(row_count), out_rows,
-                                        _ptr(quant_out), _ptr(scale_out), _stream(stream)))
+    shape = (rows, 2 * hidden if activation == AR_ACT_SILU_MUL else hidden)
+    scales = (out_rows, (hidden + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK)
+    try:
+        dev = _device_of(x)
+        args = (_operand(x, _ELEM, shape, dev), rows, hidden, _ELEM[x.dtype], activation,
+                None if position is None else _operand(position, _I32, (rows, copies), dev),
+                copies, None if row_count is None else _operand(row_count, _I32, (1,), dev),
+                out_rows, _operand(quant_out, _FP8, (out_rows, hidden), dev),
+                _operand(scale_out, _F32, scales, dev), _stream(stream))
+    except _Refused:
+        _explain(("x", x, _ELEM, shape), ("quant_out", quant_out, _FP8, None),
+                 ("scale_out", scale_out, _F32, scales),
+                 ("position", position, _I32, (rows, copies)),
+                 ("row_count", row_count, _I32, (1,)))
+    _check(lib().ar_fusion_quant_blocks(*args))
 
 
 def ar_fusion_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
                          b_scale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """a [rows, depth], b [cols, depth] (uint8 or float8_e4m3fn); a_scale [rows,
     ceil(depth / 128)], b_scale [ceil(cols / 128), ceil(depth / 128)] fp32; out [rows, cols]."""
-    _expect(a.dim() == 2 and b.dim() == 2, "a and b have two dimensions")
-    (rows, depth), cols = a.shape, b.shape[0]
-    blocks = _quant_blocks(depth)
-    _typed("a", a, _FP8)
-    _typed("b", b, _FP8, (cols, depth))
-    _typed("a_scale", a_scale, _F32, (rows, blocks))
-    _typed("b_scale", b_scale, _F32, (_quant_blocks(cols), blocks))
-    _typed("out", out, _ELEM, (rows, cols))
-    _on_current(a, a_scale, b, b_scale, out)
-    _check(lib().ar_fusion_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), rows, cols,
-                                      depth, _dtype_id(out), _ptr(out), _stream(stream)))
+    _dims(2, a=a, b=b)
+    rows, depth = a.shape
+    cols = b.shape[0]
+    blocks = (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
+    col_blocks = (cols + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
+    try:
+        dev = _device_of(a)
+        args = (_operand(a, _FP8, (rows, depth), dev), _operand(a_scale, _F32, (rows, blocks), dev),
+                _operand(b, _FP8, (cols, depth), dev),
+                _operand(b_scale, _F32, (col_blocks, blocks), dev), rows, cols, depth,
+                _ELEM.get(out.dtype), _operand(out, _ELEM, (rows, cols), dev), _stream(stream))
+    except _Refused:
+        _explain(("a", a, _FP8, None), ("b", b, _FP8, (cols, depth)),
+                 ("a_scale", a_scale, _F32, (rows, blocks)),
+                 ("b_scale", b_scale, _F32, (col_blocks, blocks)),
+                 ("out", out, _ELEM, (rows, cols)))
+    _check(lib().ar_fusion_matmul_fp8(*args))
 
 
 def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
@@ -573,19 +607,25 @@ def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch
                                 stream=None) -> None:
     """ar_fusion_matmul_fp8 by experts: b [experts, cols, depth], b_scale
     [experts, ceil(cols / 128), ceil(depth / 128)], offsets [experts + 1] int32."""
-    _expect(a.dim() == 2 and b.dim() == 3, "a has two dimensions, b three")
-    (rows, depth), (experts, cols) = a.shape, b.shape[:2]
-    blocks = _quant_blocks(depth)
-    _typed("a", a, _FP8)
-    _typed("b", b, _FP8, (experts, cols, depth))
-    _typed("a_scale", a_scale, _F32, (rows, blocks))
-    _typed("b_scale", b_scale, _F32, (experts, _quant_blocks(cols), blocks))
-    _typed("offsets", offsets, _I32, (experts + 1,))
-    _typed("out", out, _ELEM, (rows, cols))
-    _on_current(a, a_scale, b, b_scale, offsets, out)
-    _check(lib().ar_fusion_expert_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
-                                             _ptr(offsets), experts, rows, cols, depth,
-                                             _dtype_id(out), _ptr(out), _stream(stream)))
+    _dims(2, a=a)
+    _dims(3, b=b)
+    rows, depth = a.shape
+    experts, cols, _ = b.shape
+    blocks = (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
+    col_blocks = (cols + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
+    try:
+        dev = _device_of(a)
+        args = (_operand(a, _FP8, (rows, depth), dev), _operand(a_scale, _F32, (rows, blocks), dev),
+                _operand(b, _FP8, (experts, cols, depth), dev),
+                _operand(b_scale, _F32, (experts, col_blocks, blocks), dev),
+                _operand(offsets, _I32, (experts + 1,), dev), experts, rows, cols, depth,
+                _ELEM.get(out.dtype), _operand(out, _ELEM, (rows, cols), dev), _stream(stream))
+    except _Refused:
+        _explain(("a", a, _FP8, None), ("b", b, _FP8, (experts, cols, depth)),
+                 ("a_scale", a_scale, _F32, (rows, blocks)),
+                 ("b_scale", b_scale, _F32, (experts, col_blocks, blocks)),
+                 ("offsets", offsets, _I32, (experts + 1,)), ("out", out, _ELEM, (rows, cols)))
+    _check(lib().ar_fusion_expert_matmul_fp8(*args))
 
 
 def ar_fusion_matmul_status(stream=None):
@@ -603,16 +643,19 @@ def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: to
                       out: torch.Tensor, add: torch.Tensor | None = None, stream=None) -> None:
     """rows_in [in_rows, hidden]; position (int32) and weights (fp32) [tokens,
     topk]; out and add [tokens, hidden], of rows_in's type."""
-    _typed("rows_in", rows_in, _ELEM)
-    _expect(rows_in.dim() == 2 and position.dim() == 2, "rows_in and position have two dimensions")
+    _dims(2, rows_in=rows_in, position=position)
     in_rows, hidden = rows_in.shape
-    tokens, topk = position.shape
-    _typed("position", position, _I32)
-    _typed("weights", weights, _F32, (tokens, topk))
-    _typed("out", out, (rows_in.dtype,), (tokens, hidden))
-    if add is not None:
-        _typed("add", add, (rows_in.dtype,), (tokens, hidden))
-    _on_current(rows_in, position, weights, out, add)
-    _check(lib().ar_fusion_combine(_ptr(rows_in), in_rows, _ptr(position), _ptr(weights), tokens,
-                                   topk, hidden, _dtype_id(rows_in), _ptr(add), _ptr(out),
-                                   _stream(stream)))
+    slots = tokens, topk = position.shape
+    same, shape = (rows_in.dtype,), (tokens, hidden)
+    try:
+        dev = _device_of(rows_in)
+        args = (_operand(rows_in, _ELEM, (in_rows, hidden), dev), in_rows,
+                _operand(position, _I32, slots, dev), _operand(weights, _F32, slots, dev), tokens,
+                topk, hidden, _ELEM[rows_in.dtype],
+                None if add is None else _operand(add, same, shape, dev),
+                _operand(out, same, shape, dev), _stream(stream))
+    except _Refused:
+        _explain(("rows_in", rows_in, _ELEM, None), ("position", position, _I32, None),
+                 ("weights", weights, _F32, slots), ("out", out, same, shape),
+                 ("add", add, same, shape))
+    _check(lib().ar_fusion_combine(*args))
