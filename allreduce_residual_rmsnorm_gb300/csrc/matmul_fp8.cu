@@ -77,6 +77,24 @@ bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, int dtype,
+                    uint32_t box_rows, uint32_t box_cols)
+{
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return false;
+    const CUtensorMapDataType type = dtype == AR_DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : dtype == AR_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols * (uint64_t)elem_bytes(dtype)};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t steps[2] = {1, 1};
+    return fn(map, type, 2, base, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_matmul(int dtype, const MatmulArgs& a, cudaStream_t s)
 {
     DeviceInfo d;

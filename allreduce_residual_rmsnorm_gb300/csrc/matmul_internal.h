@@ -12,12 +12,17 @@ namespace arf {
 bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t depth,
                      uint32_t box_rows);
 
+// The output [rows][cols] as a target of stores of box_rows x box_cols, in the
+// 64-byte swizzle (box_cols elements are 64 bytes).  cols * elem is a multiple of 16.
+bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, int dtype,
+                    uint32_t box_rows, uint32_t box_cols);
+
 struct DeviceInfo {
     int sms;
     int* status;                // device status words of the products: code, detail
 };
 
-// Tokens on the lanes of tensor memory, 128 x 256 outputs per block: many rows.
+// Tokens on the lanes of tensor memory, 256 x 256 outputs per pair of blocks: many rows.
 cudaError_t launch_matmul_wide(int dtype, const MatmulArgs& a, const DeviceInfo& d,
                                cudaStream_t s);
 // Weights on the lanes, `tokens` (16, 32, 64 or 128) rows at a time, the depth

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages,
                    tfull = empty + 8 * kMaxStages, tempty = tfull + 8 * kBufs,
                    done = tempty + 8 * kBufs;
-    const Bail bail{&dead, status};
+    const Bail bail{smem_u32(&dead), status};
     if (tid == 0) {
         dead = 0;
         for (int s = 0; s < stages; ++s) {
@@ -115,46 +115,50 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     for (int64_t m0 = row0 + (int64_t)blockIdx.y * TOK; m0 < row1; m0 += step) {
         if (warp == 4) {
-            if (lane == 0) {
-                const int brow = e * a.cols + n0;
-                for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                    if (!(ok = bar_wait(empty + 8 * s, ph ^ 1, bail, 1)))
-                        break;
+            const int brow = e * a.cols + n0;
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * s, ph ^ 1, bail, 1));
+                if (!ok)
+                    break;
+                if (elect_one()) {
                     const uint32_t at = stage0 + s * kStage;
                     bar_expect(full + 8 * s, kStage);
                     tma_load_2d(at, &map_b, full + 8 * s, kb * kK, brow);
                     tma_load_2d(at + kBytesW, &map_a, full + 8 * s, kb * kK, (int)m0);
-                    ++issued;
-                    if (++s == (uint32_t)stages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++s == (uint32_t)stages) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            __syncwarp();
         } else if (warp == 5) {
-            if (lane == 0) {
-                constexpr uint32_t idesc = fp8_idesc(kN, TOK);
-                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                    const uint32_t b = it % kBufs;
-                    if (!(ok = bar_wait(tempty + 8 * b, (it / kBufs & 1) ^ 1, bail, 2)) ||
-                        !(ok = bar_wait(full + 8 * s, ph, bail, 3)))
-                        break;
-                    tc_fence_after();
-                    const uint64_t dw = smem_desc(stage0 + s * kStage);
-                    const uint64_t dx = smem_desc(stage0 + s * kStage + kBytesW);
+            constexpr uint32_t idesc = fp8_idesc(kN, TOK);
+            const uint64_t desc0 = smem_desc(stage0);
+            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                const uint32_t b = it % kBufs;
+                ok = __all_sync(0xffffffffu,
+                                bar_wait(tempty + 8 * b, (it / kBufs & 1) ^ 1, bail, 2) &&
+                                    bar_wait(full + 8 * s, ph, bail, 3));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dw = desc0 + (uint64_t)(s * (kStage >> 4));
+                    const uint64_t dx = dw + (kBytesW >> 4);
 #pragma unroll
                     for (int k = 0; k < kK / 32; ++k)
                         mma_fp8(tmem + b * TOK, dw + 2 * k, dx + 2 * k, idesc, k > 0);
                     mma_commit(empty + 8 * s);
                     mma_commit(tfull + 8 * b);
-                    if (++s == (uint32_t)stages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++s == (uint32_t)stages) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            __syncwarp();
         } else {
             const int have = (int)min((int64_t)TOK, row1 - m0);
             const int n = n0 + tid;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kThreads)
             cluster_barrier();
         }
     }
-    if (!ok && lane == 0) {
+    if (!ok) {
         if (warp == 4) {
             // a block that gave up waits for its copies in flight
             for (uint32_t i = 0; i < (uint32_t)stages && i < issued; ++i) {
@@ -251,7 +255,9 @@ __global__ void __launch_bounds__(kThreads)
                 bar_drain(full + 8 * s, ph);
             }
         } else if (warp == 5) {
-            mma_commit(done);
+            if (elect_one())
+                mma_commit(done);
+            __syncwarp();
             bar_drain(done, 0);
         }
     }

@@ -45,24 +45,31 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 }
 
 // Every wait ends: after kWaitNs, or as soon as another wait of the block gave
-// up (*dead), it returns false, and the first one to give up records
+// up (its flag is set), it returns false, and the first one to give up records
 // AR_ERR_TIMEOUT and `where` in the device's status words.
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct Bail {
-    volatile int* dead;         // shared memory
+    uint32_t dead;              // shared-memory address of the block's flag
     int* status;                // device status words: code, detail
 };
 
-__device__ __noinline__ inline bool bar_wait_slow(uint32_t bar, uint32_t parity, const Bail& b,
-                                                  int where)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Bail& b, int where)
 {
-    const uint64_t t0 = globaltimer_ns();
-    while (!bar_try(bar, parity)) {
-        if (*b.dead)
+    if (bar_try(bar, parity))
+        return true;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
+        if (n & 15u)
+            continue;
+        uint32_t dead;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(dead) : "r"(b.dead) : "memory");
+        if (dead)
             return false;
-        if (globaltimer_ns() - t0 > kWaitNs) {
-            *b.dead = 1;
+        const uint64_t t = globaltimer_ns();
+        t0 = t0 ? t0 : t;
+        if (t - t0 > kWaitNs) {
+            asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(b.dead) : "memory");
             if (atomicCAS(b.status, 0, AR_ERR_TIMEOUT) == 0)
                 atomicExch(b.status + 1, where);
             return false;
@@ -70,16 +77,23 @@ __device__ __noinline__ inline bool bar_wait_slow(uint32_t bar, uint32_t parity,
     }
     return true;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Bail& b, int where)
-{
-    return bar_try(bar, parity) || bar_wait_slow(bar, parity, b, where);
-}
 // A last wait for work in flight, taken only after the block gave up.
-__device__ __noinline__ inline void bar_drain(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
 {
     const uint64_t t0 = globaltimer_ns();
     while (!bar_try(bar, parity) && globaltimer_ns() - t0 < 200000000ull) {
     }
+}
+
+// One lane of a converged warp, the same one every time.  Copies and products are
+// issued under this rather than under lane == 0: the compiler then knows that
+// one thread runs them, and keeps their descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(yes));
+    return yes != 0;
 }
 
 // ------------------------------------------------------ tensor-map copies
@@ -98,6 +112,43 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Pairs of blocks (cta_group::2): the address of `bar` in the pair's first
+// block, copies into this block's memory that signal there, and stores.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_remote(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map,
+                                              uint32_t cluster_bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(cluster_bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(map),
+        "r"(src), "r"(x), "r"(y)
+        : "memory");
+}
+// until all but `N` of this thread's stores have been read from shared memory
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // -------------------------------------------------- tcgen05: tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols)
@@ -110,6 +161,19 @@ __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols)
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+// the same for a pair: one warp of each block
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t smem_slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
                  : "memory");
 }
 __device__ __forceinline__ void tc_fence_before()
@@ -140,6 +204,33 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&d)[16])
                  : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3]), "+r"(d[4]), "+r"(d[5]),
                    "+r"(d[6]), "+r"(d[7]), "+r"(d[8]), "+r"(d[9]), "+r"(d[10]), "+r"(d[11]),
                    "+r"(d[12]), "+r"(d[13]), "+r"(d[14]), "+r"(d[15])
+                 :
+                 : "memory");
+}
+
+// 32 columns, likewise
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&d)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),
+          "=r"(d[7]), "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]),
+          "=r"(d[14]), "=r"(d[15]), "=r"(d[16]), "=r"(d[17]), "=r"(d[18]), "=r"(d[19]),
+          "=r"(d[20]), "=r"(d[21]), "=r"(d[22]), "=r"(d[23]), "=r"(d[24]), "=r"(d[25]),
+          "=r"(d[26]), "=r"(d[27]), "=r"(d[28]), "=r"(d[29]), "=r"(d[30]), "=r"(d[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&d)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3]), "+r"(d[4]), "+r"(d[5]),
+                   "+r"(d[6]), "+r"(d[7]), "+r"(d[8]), "+r"(d[9]), "+r"(d[10]), "+r"(d[11]),
+                   "+r"(d[12]), "+r"(d[13]), "+r"(d[14]), "+r"(d[15]), "+r"(d[16]), "+r"(d[17]),
+                   "+r"(d[18]), "+r"(d[19]), "+r"(d[20]), "+r"(d[21]), "+r"(d[22]), "+r"(d[23]),
+                   "+r"(d[24]), "+r"(d[25]), "+r"(d[26]), "+r"(d[27]), "+r"(d[28]), "+r"(d[29]),
+                   "+r"(d[30]), "+r"(d[31])
                  :
                  : "memory");
 }
@@ -176,6 +267,56 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
+}
+
+// Four products, 128 of K, of a pair, issued by its first block: M counts the
+// rows of both, each block holds its rows of a and half the rows of b.  `a` and
+// `b` are the low words of the descriptors, `hi` their common high word.  One
+// asm block, and the loop around it run by one thread: with votes and
+// descriptor arithmetic between them the products were issued every 110 cycles
+// at best (64 is what 128 columns take), and later still while other warps of
+// the scheduler had arithmetic to issue.
+__device__ __forceinline__ void mma4_fp8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                              uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .b64 p, q;\n\t.reg .b32 x, y;\n\t.reg .pred no, yes;\n\t"
+        "setp.ne.b32 no, 0, 0;\n\tsetp.ne.b32 yes, 1, 0;\n\t"
+        "mov.b64 p, {%1, %3};\n\tmov.b64 q, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, no;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc)
+        : "memory");
+}
+// The commit arrives at the same barrier of both blocks.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Registers per thread of this warpgroup from here on.  The shares of a block's
+// warpgroups may not exceed what it was launched with (threads x registers).
+template <int N>
+__device__ __forceinline__ void regs_fewer()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_more()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ----------------------------------------------------- packed fp32 pairs

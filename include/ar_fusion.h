@@ -592,7 +592,8 @@ int ar_fusion_expert_matmul_fp8(const void* a, const float* a_scale, const void*
  * `stream`, returns AR_OK or the first error recorded since the previous query
  * (AR_ERR_TIMEOUT), and clears it.  *detail (may be NULL) receives which wait
  * gave up (1: the copies for a free stage, 2: the products for a free
- * accumulator, 3: for data, 4: the sums for products) or -1.  AR_ERR_CUDA if
+ * accumulator, 3: for data, 4: the sums for products, 5: for a
+ * free scale slot, 6: for scales) or -1.  AR_ERR_CUDA if
  * reading the status fails. */
 int ar_fusion_matmul_status(void* stream, int* detail);
 
