@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(kThreads) block_quant_kernel(BlockQuantArgs a,
     const uint64_t row = item / (unsigned)chunks;
     const int blk = (int)(item - row * (unsigned)chunks);
     const int at = blk * AR_QUANT_BLOCK + sub * kElems;
+    pdl_trigger();
+    pdl_wait();
     uint64_t rows = (uint64_t)a.rows;
     if (a.row_count)
         rows = (uint64_t)min(max(*a.row_count, 0), a.rows);
@@ -99,10 +101,8 @@ cudaError_t launch_t(const BlockQuantArgs& a, cudaStream_t s)
     if (blocks > 0x7fffffffull)
         return cudaErrorInvalidValue;
     if (a.act == AR_ACT_SILU_MUL)
-        block_quant_kernel<D, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, chunks);
-    else
-        block_quant_kernel<D, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, chunks);
-    return cudaGetLastError();
+        return launch_after(block_quant_kernel<D, true>, (unsigned)blocks, kThreads, 0, s, a, chunks);
+    return launch_after(block_quant_kernel<D, false>, (unsigned)blocks, kThreads, 0, s, a, chunks);
 }
 
 }  // namespace

@@ -16,6 +16,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a, int ve
 {
     const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
     const uint64_t t = i / (unsigned)vecs;
+    pdl_trigger();
+    pdl_wait();
     if (t >= (uint64_t)a.T)
         return;
     const uint64_t at = (i - t * (unsigned)vecs) * 8 * D::bytes;
@@ -67,8 +69,7 @@ cudaError_t launch_t(const CombineArgs& a, cudaStream_t s)
     const uint64_t blocks = ((uint64_t)a.T * vecs + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffffull)
         return cudaErrorInvalidValue;
-    combine_kernel<D><<<(unsigned)blocks, kThreads, 0, s>>>(a, vecs);
-    return cudaGetLastError();
+    return launch_after(combine_kernel<D>, (unsigned)blocks, kThreads, 0, s, a, vecs);
 }
 
 }  // namespace

@@ -61,6 +61,26 @@ struct CombineArgs {
 };
 cudaError_t launch_combine(int dtype, const CombineArgs& a, cudaStream_t s);
 
+// Launch with programmatic dependent launch: the blocks may be scheduled while
+// the kernel before them on the stream finishes, and wait on the device
+// (griddepcontrol.wait) before their first access to global memory.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 inline int quant_blocks(int depth) { return (depth + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK; }
 
 }  // namespace arf

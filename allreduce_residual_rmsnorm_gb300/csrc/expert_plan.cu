@@ -3,15 +3,19 @@
 // could show.  Each warp owns a run of consecutive slots and counts it by
 // expert in shared memory; the counts are summed over the warps of a block
 // and, through distributed shared memory, over the blocks of the cluster; the
-// second pass over the same slots (an L2 hit) numbers them.
+// second pass over the same slots (a cache hit) numbers them.
+//
+// Bounded by latency: the ids are 256 KB at 8192 tokens of 8 experts.  So the
+// loads of 8 rounds are in flight at once, and small calls take few warps.
 #include "expert_internal.h"
 #include "expert_vec.cuh"
 
 namespace arf {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 32;
+constexpr int kRounds = 8;      // of 32 slots, loaded together
+constexpr int kPerThread = 4;   // experts of a thread, in a block of 256 threads or more
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* local, unsigned rank)
 {
@@ -22,54 +26,109 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* local, unsigned ran
     return v;
 }
 
-// shared memory: count[kWarps][E], total[E]
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a)
+// The local experts of the slots of 8 rounds (~0 for a slot of none), and the
+// lanes of each round with the same one.  The latter by one ballot per bit of
+// the expert's number: a few instructions of full rate each, where one
+// match.any took 8192 tokens of 8 experts 13 us in all.
+__device__ __forceinline__ void load_rounds(const PlanArgs& a, int bits, int64_t i, int64_t hi,
+                                            uint32_t (&e)[kRounds], uint32_t (&same)[kRounds])
+{
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        e[r] = i + 32 * r < hi ? (uint32_t)a.ids[i + 32 * r] : 0xffffffffu;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const uint32_t local = e[r] - (uint32_t)a.first;
+        const bool in = i + 32 * r < hi && local < (uint32_t)a.E;
+        e[r] = in ? local : 0xffffffffu;
+        same[r] = __ballot_sync(0xffffffffu, in);
+    }
+    for (int k = 0; k < bits; ++k) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint32_t ones = __ballot_sync(0xffffffffu, e[r] >> k & 1u);
+            same[r] &= e[r] >> k & 1u ? ones : ~ones;
+        }
+    }
+}
+
+// shared memory: count[warps][E], total[E]
+__global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bits)
 {
     extern __shared__ uint32_t sh[];
-    __shared__ uint32_t warp_sum[kWarps];
+    __shared__ uint32_t warp_sum[kMaxWarps];
     const int E = a.E;
-    uint32_t* total = sh + kWarps * E;
+    const int threads = blockDim.x, warps = threads / 32;
+    uint32_t* total = sh + warps * E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t* count = sh + warp * E;
     const unsigned blocks = cluster_size(), me = cluster_rank();
 
     // this warp's run of slots, whole rounds of 32 but for the last
     const int64_t rounds = ((int64_t)a.slots + 31) / 32;
-    const int64_t warps = (int64_t)blocks * kWarps, w = (int64_t)me * kWarps + warp;
-    const int64_t lo = rounds * w / warps * 32;
-    const int64_t hi0 = rounds * (w + 1) / warps * 32;
+    const int64_t all_warps = (int64_t)blocks * warps, w = (int64_t)me * warps + warp;
+    const int64_t lo = rounds * w / all_warps * 32;
+    const int64_t hi0 = rounds * (w + 1) / all_warps * 32;
     const int64_t hi = hi0 < a.slots ? hi0 : a.slots;
 
+    pdl_trigger();
     for (int e = lane; e < E; e += 32)
         count[e] = 0;
+    pdl_wait();
+    const uint32_t below = (1u << lane) - 1u;
+    uint32_t e[kRounds], same[kRounds];
+    load_rounds(a, bits, lo + lane, hi, e, same);
     __syncwarp();
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-        const uint32_t e = (uint32_t)a.ids[i] - (uint32_t)a.first;
-        if (e < (uint32_t)E)
-            atomicAdd(&count[e], 1u);
+    for (int64_t i = lo;;) {
+        // the first lane of each expert adds for all: no two lanes of a warp
+        // touch the same counter
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (e[r] != 0xffffffffu && (same[r] & below) == 0)
+                atomicAdd(&count[e[r]], (uint32_t)__popc(same[r]));
+        i += 32 * kRounds;
+        if (i >= hi)
+            break;
+        load_rounds(a, bits, i + lane, hi, e, same);
     }
     __syncthreads();
     // counts of the warps before, per expert
-    if (tid < E) {
+    for (int x = tid; x < E; x += threads) {
         uint32_t run = 0;
-        for (int v = 0; v < kWarps; ++v) {
-            const uint32_t c = sh[v * E + tid];
-            sh[v * E + tid] = run;
+#pragma unroll 8
+        for (int v = 0; v < warps; ++v) {
+            const uint32_t c = sh[v * E + x];
+            sh[v * E + x] = run;
             run += c;
         }
-        total[tid] = run;
+        total[x] = run;
     }
-    cluster_barrier();
-    uint32_t all = 0, before = 0;
-    if (tid < E) {
-        for (unsigned b = 0; b < blocks; ++b) {
-            const uint32_t c = ld_dsmem_u32(&total[tid], b);
-            before += b < me ? c : 0u;
-            all += c;
+    if (blocks > 1)
+        cluster_barrier();
+    else
+        __syncthreads();
+    // kPerThread consecutive experts of a thread: rows of the cluster, and of
+    // the blocks before this one
+    uint32_t all[kPerThread], before[kPerThread], mine = 0;
+#pragma unroll
+    for (int q = 0; q < kPerThread; ++q) {
+        const int x = tid * kPerThread + q;
+        all[q] = before[q] = 0;
+        if (x < E) {
+            if (blocks > 1) {
+                for (unsigned b = 0; b < blocks; ++b) {
+                    const uint32_t c = ld_dsmem_u32(&total[x], b);
+                    before[q] += b < me ? c : 0u;
+                    all[q] += c;
+                }
+            } else {
+                all[q] = total[x];
+            }
         }
+        mine += all[q];
     }
-    // exclusive sum over experts (threads)
-    uint32_t inc = all;
+    // exclusive sum over threads
+    uint32_t inc = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const uint32_t v = __shfl_up_sync(0xffffffffu, inc, m);
@@ -77,32 +136,45 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a)
     }
     if (lane == 31)
         warp_sum[warp] = inc;
-    cluster_barrier();          // every total has been read
-    uint32_t first = inc - all;
+    if (blocks > 1)
+        cluster_barrier();      // every total has been read
+    else
+        __syncthreads();
+    uint32_t first = inc - mine;
     for (int v = 0; v < warp; ++v)
         first += warp_sum[v];
-    if (tid < E) {
-        total[tid] = first + before;
-        if (me == 0) {
-            a.offsets[tid] = (int32_t)first;
-            if (tid == E - 1)
-                a.offsets[E] = (int32_t)(first + all);
+#pragma unroll
+    for (int q = 0; q < kPerThread; ++q) {
+        const int x = tid * kPerThread + q;
+        if (x < E) {
+            total[x] = first + before[q];
+            if (me == 0) {
+                a.offsets[x] = (int32_t)first;
+                if (x == E - 1)
+                    a.offsets[E] = (int32_t)(first + all[q]);
+            }
+            first += all[q];
         }
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const uint32_t e = i < hi ? (uint32_t)a.ids[i] - (uint32_t)a.first : 0xffffffffu;
-        const bool local = e < (uint32_t)E;
-        const uint32_t same = __match_any_sync(0xffffffffu, local ? e : 0xffffffffu);
-        const uint32_t earlier = __popc(same & ((1u << lane) - 1u));
-        const uint32_t base = local ? total[e] + count[e] : 0u;
-        if (i < hi)
-            a.position[i] = local ? (int32_t)(base + earlier) : -1;
-        __syncwarp();
-        if (local && earlier == 0)
-            count[e] += __popc(same);
-        __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRounds) {
+        if (hi - lo > 32 * kRounds)     // else they are still in registers
+            load_rounds(a, bits, i0 + lane, hi, e, same);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int64_t i = i0 + 32 * r + lane;
+            if (i0 + 32 * r >= hi)
+                break;
+            const bool local = e[r] != 0xffffffffu;
+            const uint32_t earlier = __popc(same[r] & below);
+            const uint32_t base = local ? total[e[r]] + count[e[r]] : 0u;
+            if (i < hi)
+                a.position[i] = local ? (int32_t)(base + earlier) : -1;
+            __syncwarp();
+            if (local && earlier == 0)
+                count[e[r]] += __popc(same[r]);
+            __syncwarp();
+        }
     }
 }
 
@@ -110,24 +182,32 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a)
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s)
 {
-    const size_t smem = sizeof(uint32_t) * (size_t)(kWarps + 1) * a.E;
     cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(uint32_t) * (kWarps + 1) * AR_MAX_EXPERTS));
+                                         (int)(sizeof(uint32_t) * (kMaxWarps + 1) * AR_MAX_EXPERTS));
     if (e != cudaSuccess)
         return e;
+    // one block up to four rounds a warp; 8 warps at least, for the experts
+    const int rounds = (a.slots + 31) / 32;
+    const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : 8;
+    const int warps = rounds <= 8 ? 8 : rounds <= 16 ? 16 : kMaxWarps;
+    static_assert(8 * 32 * kPerThread >= AR_MAX_EXPERTS, "experts of a block of 8 warps");
     cudaLaunchConfig_t cfg = {};
-    const unsigned blocks = a.slots <= 4 * kThreads ? 1 : 8;
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t)(warps + 1) * a.E;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = blocks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = blocks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, plan_kernel, a);
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    int bits = 0;               // of the largest local expert's number
+    while ((1 << bits) < a.E)
+        ++bits;
+    return cudaLaunchKernelEx(&cfg, plan_kernel, a, bits);
 }
 
 }  // namespace arf

@@ -1,19 +1,24 @@
 // Routing to experts: scores, groups, top-k and weights of one token row per
-// warp.  Expert e = lane + 32 i sits in register i of its lane.
+// warp.  Expert e = lane + 32 i starts in register i of its lane; each lane
+// sorts its own, and a pick is the largest of the 32 heads.  Bounded by its
+// instructions, about 900 a row at 256 experts and 8 chosen (8192 rows: 9 MB,
+// 1.4 us of memory time).
 //
 // The order of the choice values c = s + bias is that of the real numbers.
 // Without a bias, or with the same one everywhere, it is the order of the
 // logits, and no score is compared at all.  Otherwise c is computed in fp32
-// with a known error bound, and a pick whose runner-up lies within that bound
-// is decided again in fp64 for the values within it alone.  fp64 runs at about
-// 1/60 of the fp32 rate here, so deciding everything in fp64 would take longer
-// than the whole kernel; a border that close comes up in about one row of 300
-// (256 sigmoid scores, 8 chosen).
+// with a known error bound, and a row where a pick's runner-up, or a group's,
+// lies within that bound is decided again in fp64 for the values within it.
+// fp64 runs at 1/64 of the fp32 rate here, so deciding everything in fp64 would
+// take longer than the whole kernel; a border that close comes up in about one
+// row of 300 (256 sigmoid scores, 8 chosen).
 //
-// Error bound, relative to the largest score: sigmoid: expf 2^-23 (1 ulp),
-// 1 + e and the division 2^-24 each, below 2^-22 in all; softmax also has the
-// fp32 sum of up to 32 values a lane and 5 butterfly steps, below 2^-18.8.
-// c itself is rounded once, 2^-24 |c|.  Two values compared: twice that.
+// Error bound, relative to the largest score, with u = 2^-24: __expf is off by
+// (2 + 1.17 |x|) 2u of its value, which moves a sigmoid by s (1 - s) of that,
+// below 0.76 * 2u; 1 + e is off by u, __fdividef by 4u: below 1.7 * 2^-22 in
+// all.  Softmax also has the fp32 sum of up to 32 values a lane and 5 butterfly
+// steps, below 2^-18.4.  c itself is rounded once, u |c|.  Two values compared:
+// twice that.
 #include <math.h>
 
 #include "expert_internal.h"
@@ -49,6 +54,12 @@ __device__ __forceinline__ float score_of(const Row& r, float x)
     return r.softmax ? expf(x - r.max) * r.inv_sum : 1.0f / (1.0f + expf(-x));
 }
 
+// the same with the fast exponential and division, for the order
+__device__ __forceinline__ float quick_score(const Row& r, float x)
+{
+    return r.softmax ? __expf(x - r.max) * r.inv_sum : __fdividef(1.0f, 1.0f + __expf(-x));
+}
+
 // the choice value in fp64
 __device__ __noinline__ double exact_choice(int softmax, float max, double sum, float x, float b)
 {
@@ -72,10 +83,10 @@ __device__ __noinline__ double exact_sum(const void* logits, const float* bias, 
     return z;
 }
 
-// Groups that stay, as a mask over lanes: group g is bit g * team.  `choice`
-// holds the ordering values of the row (-inf: out).
+// Groups that stay, as a mask over lanes: group g is bit g * team.  `key` holds
+// the row's ordering values as keys (0: out).
 template <class D>
-__device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, const float* choice,
+__device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, const uint32_t* key,
                                                 uint64_t at, bool by_logit, float bias0,
                                                 float base_err, int lane, int team)
 {
@@ -84,9 +95,9 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
     const int g = lane / team, sub = lane & (team - 1);
     uint32_t k1 = 0, k2 = 0;
     if (g < a.G) {
+#pragma unroll 4
         for (int t = sub; t < size; t += team) {
-            const float v = choice[g * size + t];
-            const uint32_t k = v == -INFINITY ? 0u : to_key(v);
+            const uint32_t k = key[g * size + t];
             k2 = max(k2, min(k1, k));
             k1 = max(k1, k);
         }
@@ -100,9 +111,9 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
     uint32_t gk = k1;
     float err = 0.0f;
     if (k1 != 0 && (top2 || !by_logit)) {
-        const float v1 = by_logit ? score_of(r, from_key(k1)) + bias0 : from_key(k1);
+        const float v1 = by_logit ? quick_score(r, from_key(k1)) + bias0 : from_key(k1);
         const float v2 = !top2 || k2 == 0 ? 0.0f
-                         : by_logit       ? score_of(r, from_key(k2)) + bias0
+                         : by_logit       ? quick_score(r, from_key(k2)) + bias0
                                           : from_key(k2);
         gk = to_key(v1 + v2);
         err = base_err + 0x1p-22f * (fabsf(v1) + fabsf(v2));
@@ -129,23 +140,35 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
             if (r.softmax && r.sum == 0.0)
                 r.sum = exact_sum<D>(a.logits, a.bias, at, a.E, r.max, lane);
             // the values that can be among the largest (two) of their group
-            const float cut = from_key(top2 && k2 > 1 ? k2 : k1);
-            const uint32_t from = by_logit ? (top2 && k2 > 1 ? k2 : k1)
-                                           : max(2u, to_key(cut - 2.0f * err));
+            const uint32_t last = top2 && k2 > 1 ? k2 : k1;
+            const uint32_t from = by_logit ? last : max(2u, to_key(from_key(last) - 2.0f * err));
             double d1 = -INFINITY, d2 = -INFINITY;
+            const auto weigh = [&](int e) {
+                const double c = exact_choice(r.softmax, r.max, r.sum,
+                                              load1<D>(a.logits, at + e),
+                                              a.bias ? a.bias[e] : 0.0f);
+                d2 = fmax(d2, fmin(d1, c));
+                d1 = fmax(d1, c);
+            };
+            // found first, then weighed together: fp64 is slow, and the lanes
+            // find theirs in different steps
+            int hits = 0, h0 = 0, h1 = 0;
             if (g < a.G && gk > 1) {
                 for (int t = sub; t < size; t += team) {
                     const int e = g * size + t;
-                    const float v = choice[e];
-                    if (v == -INFINITY || to_key(v) < from)
-                        continue;
-                    const double c = exact_choice(r.softmax, r.max, r.sum,
-                                                  load1<D>(a.logits, at + e),
-                                                  a.bias ? a.bias[e] : 0.0f);
-                    d2 = fmax(d2, fmin(d1, c));
-                    d1 = fmax(d1, c);
+                    if (key[e] >= from) {
+                        h1 = hits == 1 ? e : h1;
+                        h0 = hits == 0 ? e : h0;
+                        if (++hits > 2)
+                            weigh(e);
+                    }
                 }
             }
+            if (hits > 0)
+                weigh(h0);
+            if (hits > 1)
+                weigh(h1);
+            __syncwarp();
             for (int m = team >> 1; m >= 1; m >>= 1) {
                 const double o1 = __shfl_xor_sync(full, d1, m), o2 = __shfl_xor_sync(full, d2, m);
                 d2 = fmax(fmin(d1, o1), fmax(d2, o2));
@@ -159,39 +182,140 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
     return __ballot_sync(full, kept);
 }
 
+// The picks of a row with a border within the error bound: values within it of
+// the largest left are compared in fp64.  Returns lane j's pick, or -1.  Reads
+// the row again for each pick: rare, and small beside the registers that
+// keeping everything would cost the common path.
+template <class D>
+__device__ __noinline__ int exact_picks(const RouteArgs& a, const Row& r0, uint64_t at,
+                                        uint32_t kept, int team, float inv_size, float base_err,
+                                        int lane)
+{
+    const uint32_t full = 0xffffffffu;
+    Row r = r0;
+    if (r.softmax && r.sum == 0.0)
+        r.sum = exact_sum<D>(a.logits, a.bias, at, a.E, r.max, lane);
+    uint32_t taken = 0;         // bit i: expert lane + 32 i
+    const auto key_of = [&](int e) {
+        const float x = load1<D>(a.logits, at + e), b = a.bias[e];
+        const bool out = x == -INFINITY || b == -INFINITY || (taken >> (e >> 5) & 1u) ||
+                         (a.G > 1 && !(kept >> ((int)(((float)e + 0.5f) * inv_size) * team) & 1u));
+        return out ? 0u : to_key(quick_score(r, x) + b);
+    };
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t lb = 0;
+        for (int e = lane; e < a.E; e += 32)
+            lb = max(lb, key_of(e));
+        const uint32_t best = __reduce_max_sync(full, lb);
+        if (best == 0)
+            break;
+        uint32_t thr = best;
+        if (best > 1) {
+            const float v = from_key(best), low = v - (base_err + 0x1p-22f * fabsf(v));
+            thr = low > -INFINITY ? to_key(low) : best;
+        }
+        double c = -INFINITY;
+        int pick = INT_MAX;
+        for (int e = lane; e < a.E; e += 32) {
+            if (key_of(e) < thr)
+                continue;
+            const double v = best == 1 ? 0.0
+                                       : exact_choice(r.softmax, r.max, r.sum,
+                                                      load1<D>(a.logits, at + e), a.bias[e]);
+            if (pick == INT_MAX || v > c) {
+                c = v;
+                pick = e;
+            }
+        }
+        for (int m = 16; m >= 1; m >>= 1) {
+            const double oc = __shfl_xor_sync(full, c, m);
+            const int op = __shfl_xor_sync(full, pick, m);
+            if (op != INT_MAX && (pick == INT_MAX || oc > c || (oc == c && op < pick))) {
+                c = oc;
+                pick = op;
+            }
+        }
+        if (lane == j)
+            mine = pick;
+        if ((pick & 31) == lane)
+            taken |= 1u << (pick >> 5);
+    }
+    return mine;
+}
+
+// Descending order of a lane's values: Batcher's odd-even merge sort, written as
+// templates so that every index is a constant and the values stay in registers.
+template <int A, int B, int V>
+__device__ __forceinline__ void larger_first(uint64_t (&v)[V])
+{
+    const uint64_t a = v[A], b = v[B];
+    v[A] = a > b ? a : b;
+    v[B] = a > b ? b : a;
+}
+template <int I, int R, int END, int V>
+__device__ __forceinline__ void larger_first_from(uint64_t (&v)[V])
+{
+    if constexpr (I + R < END) {
+        larger_first<I, I + R>(v);
+        larger_first_from<I + 2 * R, R, END>(v);
+    }
+}
+template <int LO, int N, int R, int V>
+__device__ __forceinline__ void merge_down(uint64_t (&v)[V])
+{
+    if constexpr (2 * R < N) {
+        merge_down<LO, N, 2 * R>(v);
+        merge_down<LO + R, N, 2 * R>(v);
+        larger_first_from<LO + R, R, LO + N>(v);
+    } else {
+        larger_first<LO, LO + R>(v);
+    }
+}
+template <int LO, int N, int V>
+__device__ __forceinline__ void sort_down(uint64_t (&v)[V])
+{
+    if constexpr (N > 1) {
+        sort_down<LO, N / 2>(v);
+        sort_down<LO + N / 2, N / 2>(v);
+        merge_down<LO, N, 1>(v);
+    }
+}
+
 template <class D, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int team)
 {
-    extern __shared__ float choice_sh[];       // [kWarps][E] with groups
+    extern __shared__ uint32_t key_sh[];        // [kWarps][E] with groups
     const uint32_t full = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kWarps + warp;
+    pdl_trigger();
     if (t >= a.T)
         return;
+    pdl_wait();
     const uint64_t at = (uint64_t)t * a.E;
 
     // logits (-inf: out) and whether the bias moves the order at all
-    float x[V];
-    float blo = INFINITY, bhi = -INFINITY;
-    bool bnan = false;
+    float x[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
         x[i] = e < a.E ? load1<D>(a.logits, at + e) : -INFINITY;
-        if (a.bias && e < a.E) {
-            const float b = a.bias[e];
-            if (b == -INFINITY)
-                x[i] = -INFINITY;
-            if (x[i] != -INFINITY) {
-                blo = fminf(blo, b);
-                bhi = fmaxf(bhi, b);
-                bnan |= b != b;
-            }
-        }
+        b[i] = a.bias && e < a.E ? a.bias[e] : 0.0f;
     }
     bool by_logit = true;
     float bias0 = 0.0f;
     if (a.bias) {
+        float blo = INFINITY, bhi = -INFINITY;
+        bool bnan = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = b[i] == -INFINITY ? -INFINITY : x[i];
+            const bool in = x[i] != -INFINITY;
+            blo = in ? fminf(blo, b[i]) : blo;
+            bhi = in ? fmaxf(bhi, b[i]) : bhi;
+            bnan |= in && b[i] != b[i];
+        }
         blo = from_key(__reduce_min_sync(full, to_key(blo)));
         bhi = from_key(__reduce_max_sync(full, to_key(bhi)));
         by_logit = !__any_sync(full, bnan) && blo >= bhi && fabsf(bhi) < INFINITY;
@@ -217,98 +341,104 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
     // twice the error bound of a choice value, without its 2^-22 |c|
     const float base_err = r.softmax ? 0x1p-17f * r.inv_sum : 0x1p-20f;
 
-    // ordering values: logits, or choice values
-    float o[V];
+    // keys of the ordering values: logits, or choice values
+    uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        o[i] = x[i];
-        if (!by_logit && x[i] != -INFINITY)
-            o[i] = score_of(r, x[i]) + a.bias[lane + 32 * i];
+        const float o = by_logit ? x[i] : quick_score(r, x[i]) + b[i];
+        key[i] = x[i] == -INFINITY ? 0u : to_key(o);
     }
     uint32_t kept = full;
     float inv_size = 0.0f;
     if (a.G > 1) {
-        float* choice = choice_sh + warp * a.E;
+        uint32_t* keys = key_sh + warp * a.E;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (lane + 32 * i < a.E)
-                choice[lane + 32 * i] = o[i];
+                keys[lane + 32 * i] = key[i];
         __syncwarp();
-        kept = kept_groups<D>(a, r, choice, at, by_logit, bias0, base_err, lane, team);
+        kept = kept_groups<D>(a, r, keys, at, by_logit, bias0, base_err, lane, team);
         inv_size = 1.0f / (float)(a.E / a.G);
-    }
-    uint32_t key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        key[i] = x[i] == -INFINITY ? 0u : to_key(o[i]);
-        if (a.G > 1) {
-            // e < 1024: (e + 1/2) / size in fp32 is below the next whole number
+        for (int i = 0; i < V; ++i) {
+            // e < 1024: (e + 1/2) / size in fp32 is below the next whole number;
+            // an expert behind the last one has key 0 already
             const int g = (int)(((float)(lane + 32 * i) + 0.5f) * inv_size);
-            if (g >= a.G || !(kept >> (g * team) & 1u))
+            if (!(kept >> (g * team & 31) & 1u))
                 key[i] = 0u;
         }
     }
+    // key, then the lower expert
+    uint64_t v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = (uint64_t)key[i] << 32 | (uint32_t)~(lane + 32 * i);
+    sort_down<0, V>(v);
 
+    // Picks in fp32 order, past the last one while the next is too close to it.
     int mine = -1;              // lane j: the j-th pick
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t lb = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            lb = max(lb, key[i]);
-        const uint32_t best = __reduce_max_sync(full, lb);
-        if (best == 0)
+    uint32_t my_key = 0;
+    uint32_t border = full;     // a next pick with this key or more is too close
+    bool close = false;
+    int picks = 0;
+    for (; picks < 32; ++picks) {
+        const uint32_t head = (uint32_t)(v[0] >> 32);
+        const uint32_t best = __reduce_max_sync(full, head);
+        close |= best >= border;
+        if (best == 0 || (picks >= a.k && best < border))
             break;
-        int pick = INT_MAX;
-        bool exact = false;
-        uint32_t thr = best;
-        if (!by_logit && best > 1) {
-            const float v = from_key(best);
-            const float low = v - (base_err + 0x1p-22f * fabsf(v));
-            thr = low > -INFINITY ? to_key(low) : best;
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                n += key[i] >= thr;
-            const uint32_t who = __ballot_sync(full, n > 0);
-            exact = __any_sync(full, n > 1) || (who & (who - 1)) != 0;
+        const uint32_t who = __ballot_sync(full, head == best);
+        int pick;
+        if ((who & (who - 1)) == 0)
+            pick = (int)~__shfl_sync(full, (uint32_t)v[0], __ffs(who) - 1);
+        else
+            pick = (int)__reduce_min_sync(full, head == best ? ~(uint32_t)v[0] : full);
+        if (lane == picks) {
+            mine = pick;
+            my_key = best;
         }
-        if (!exact) {
+        if ((pick & 31) == lane) {
 #pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-                if (key[i] == best)
-                    pick = lane + 32 * i;
-            pick = (int)__reduce_min_sync(full, (uint32_t)pick);
+            for (int i = 0; i + 1 < V; ++i)
+                v[i] = v[i + 1];
+            v[V - 1] = 0ull;
+        }
+        border = full;
+        if (!by_logit && best > 1) {
+            const float c = from_key(best), low = c - (base_err + 0x1p-22f * fabsf(c));
+            border = low > -INFINITY ? to_key(low) : full;
+        }
+    }
+    if (close) {
+        // 32 picks and no end of close ones (or 32 chosen): one by one
+        const uint32_t rest = __reduce_max_sync(full, (uint32_t)(v[0] >> 32));
+        if (picks == 32 && rest >= border) {
+            mine = exact_picks<D>(a, r, at, kept, team, inv_size, base_err, lane);
         } else {
+            // every value left is below all of these: order them in fp64
             if (r.softmax && r.sum == 0.0)
                 r.sum = exact_sum<D>(a.logits, a.bias, at, a.E, r.max, lane);
-            double c = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (key[i] >= thr) {
-                    const int e = lane + 32 * i;
-                    const double v = exact_choice(r.softmax, r.max, r.sum, x[i], a.bias[e]);
-                    if (pick == INT_MAX || v > c) {
-                        c = v;
-                        pick = e;
-                    }
-                }
+            double c = -INFINITY;       // NaN: behind the numbers
+            if (mine >= 0 && my_key > 1)
+                c = exact_choice(r.softmax, r.max, r.sum, load1<D>(a.logits, at + mine),
+                                 a.bias[mine]);
+            __syncwarp();
+            int rank = 0;
+            for (int o = 0; o < picks; ++o) {
+                const double oc = __shfl_sync(full, c, o);
+                const int oe = __shfl_sync(full, mine, o);
+                rank += oc > c || (oc == c && oe < mine);
             }
-            for (int m = 16; m >= 1; m >>= 1) {
-                const double oc = __shfl_xor_sync(full, c, m);
-                const int op = __shfl_xor_sync(full, pick, m);
-                if (op != INT_MAX && (pick == INT_MAX || oc > c || (oc == c && op < pick))) {
-                    c = oc;
-                    pick = op;
-                }
+            int sorted = -1;
+            for (int o = 0; o < picks; ++o) {
+                const int orank = __shfl_sync(full, rank, o), oe = __shfl_sync(full, mine, o);
+                sorted = orank == lane ? oe : sorted;
             }
+            mine = sorted;
         }
-        if (lane == j)
-            mine = pick;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane + 32 * i == pick)
-                key[i] = 0u;
     }
+    if (lane >= a.k)
+        mine = -1;
 
     // Weights.  Renormalised ones divide out the largest exponential of the
     // chosen first, so that scores below the fp32 range keep their ratios.
@@ -346,21 +476,19 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s)
     while (team * a.G > 32)
         team >>= 1;
     const unsigned grid = (unsigned)((a.T - 1) / kWarps + 1);
-    const size_t smem = a.G > 1 ? sizeof(float) * kWarps * a.E : 0;
+    const size_t smem = a.G > 1 ? sizeof(uint32_t) * kWarps * a.E : 0;
     const int per_lane = (a.E + 31) / 32;
     if (per_lane <= 1)
-        route_kernel<D, 1><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    else if (per_lane <= 2)
-        route_kernel<D, 2><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    else if (per_lane <= 4)
-        route_kernel<D, 4><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    else if (per_lane <= 8)
-        route_kernel<D, 8><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    else if (per_lane <= 16)
-        route_kernel<D, 16><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    else
-        route_kernel<D, 32><<<grid, 32 * kWarps, smem, s>>>(a, team);
-    return cudaGetLastError();
+        return launch_after(route_kernel<D, 1>, grid, 32 * kWarps, smem, s, a, team);
+    if (per_lane <= 2)
+        return launch_after(route_kernel<D, 2>, grid, 32 * kWarps, smem, s, a, team);
+    if (per_lane <= 4)
+        return launch_after(route_kernel<D, 4>, grid, 32 * kWarps, smem, s, a, team);
+    if (per_lane <= 8)
+        return launch_after(route_kernel<D, 8>, grid, 32 * kWarps, smem, s, a, team);
+    if (per_lane <= 16)
+        return launch_after(route_kernel<D, 16>, grid, 32 * kWarps, smem, s, a, team);
+    return launch_after(route_kernel<D, 32>, grid, 32 * kWarps, smem, s, a, team);
 }
 
 }  // namespace

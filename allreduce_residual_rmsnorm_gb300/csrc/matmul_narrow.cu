@@ -67,8 +67,10 @@ __global__ void __launch_bounds__(kThreads)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const int e = blockIdx.z;
+    pdl_trigger();
     int row0 = 0, row1 = a.rows;
     if (a.offsets) {
+        pdl_wait();
         row0 = min(max(a.offsets[e], 0), a.rows);
         row1 = min(max(a.offsets[e + 1], row0), a.rows);
     }
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    pdl_wait();
 
     const int rank = blockIdx.x % split;
     const int n0 = blockIdx.x / split * kN;
@@ -294,12 +297,14 @@ cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaSt
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, d.status, split, stages);
 }
 

@@ -149,6 +149,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 9)
         tmem_alloc_pair(smem_u32(&tmem_slot), kCols);
+    pdl_trigger();
+    pdl_wait();
     // rows and row tiles before each expert
     if (warp == 0) {
         int tiles = 0, before = 0;
@@ -470,9 +472,8 @@ cudaError_t launch_t(const MatmulArgs& a, const DeviceInfo& d, cudaStream_t s)
     if (most > 0x7fffffffll - d.sms)
         return cudaErrorInvalidValue;
     const int pairs = most < d.sms / 2 ? (int)most : d.sms / 2;
-    matmul_wide_kernel<D><<<2 * pairs, kThreads, kSmem, s>>>(map_a, map_b, map_out, a, d.status,
-                                                             aligned);
-    return cudaGetLastError();
+    return launch_after(matmul_wide_kernel<D>, 2 * pairs, kThreads, kSmem, s, map_a, map_b, map_out, a,
+                        d.status, aligned);
 }
 
 }  // namespace
