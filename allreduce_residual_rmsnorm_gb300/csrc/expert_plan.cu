@@ -15,7 +15,8 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 constexpr int kRounds = 8;      // of 32 slots, loaded together
-constexpr int kPerThread = 4;   // experts of a thread, in a block of 256 threads or more
+constexpr int kPerThread = 4;   // experts of a thread at most: blocks have 256 threads or more
+constexpr int kMaxBlocks = 8;   // of the cluster
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* local, unsigned rank)
 {
@@ -107,19 +108,24 @@ __global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bi
         cluster_barrier();
     else
         __syncthreads();
-    // kPerThread consecutive experts of a thread: rows of the cluster, and of
-    // the blocks before this one
+    // consecutive experts of a thread: their rows in the cluster, and in the
+    // blocks before this one
+    const int per = (E + threads - 1) / threads;
     uint32_t all[kPerThread], before[kPerThread], mine = 0;
 #pragma unroll
     for (int q = 0; q < kPerThread; ++q) {
-        const int x = tid * kPerThread + q;
+        const int x = tid * per + q;
         all[q] = before[q] = 0;
-        if (x < E) {
+        if (q < per && x < E) {
             if (blocks > 1) {
-                for (unsigned b = 0; b < blocks; ++b) {
-                    const uint32_t c = ld_dsmem_u32(&total[x], b);
-                    before[q] += b < me ? c : 0u;
-                    all[q] += c;
+                uint32_t c[kMaxBlocks];         // every block's at once
+#pragma unroll
+                for (unsigned b = 0; b < kMaxBlocks; ++b)
+                    c[b] = ld_dsmem_u32(&total[x], b);
+#pragma unroll
+                for (unsigned b = 0; b < kMaxBlocks; ++b) {
+                    before[q] += b < me ? c[b] : 0u;
+                    all[q] += c[b];
                 }
             } else {
                 all[q] = total[x];
@@ -141,12 +147,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bi
     else
         __syncthreads();
     uint32_t first = inc - mine;
-    for (int v = 0; v < warp; ++v)
-        first += warp_sum[v];
+    // sums of the warps before
+    uint32_t part = lane < warp ? warp_sum[lane] : 0u;
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        part += __shfl_xor_sync(0xffffffffu, part, m);
+    first += part;
 #pragma unroll
     for (int q = 0; q < kPerThread; ++q) {
-        const int x = tid * kPerThread + q;
-        if (x < E) {
+        const int x = tid * per + q;
+        if (q < per && x < E) {
             total[x] = first + before[q];
             if (me == 0) {
                 a.offsets[x] = (int32_t)first;
@@ -188,7 +198,7 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s)
         return e;
     // one block up to four rounds a warp; 8 warps at least, for the experts
     const int rounds = (a.slots + 31) / 32;
-    const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : 8;
+    const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : kMaxBlocks;
     const int warps = rounds <= 8 ? 8 : rounds <= 16 ? 16 : kMaxWarps;
     static_assert(8 * 32 * kPerThread >= AR_MAX_EXPERTS, "experts of a block of 8 warps");
     cudaLaunchConfig_t cfg = {};

@@ -375,66 +375,81 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
         v[i] = (uint64_t)key[i] << 32 | (uint32_t)~(lane + 32 * i);
     sort_down<0, V>(v);
 
-    // Picks in fp32 order, past the last one while the next is too close to it.
-    int mine = -1;              // lane j: the j-th pick
+    // Picks in fp32 order, one more than chosen (lane j: the j-th)
+    int mine = -1;
     uint32_t my_key = 0;
-    uint32_t border = full;     // a next pick with this key or more is too close
-    bool close = false;
-    int picks = 0;
-    for (; picks < 32; ++picks) {
+    const auto take = [&](int j) {
         const uint32_t head = (uint32_t)(v[0] >> 32);
         const uint32_t best = __reduce_max_sync(full, head);
-        close |= best >= border;
-        if (best == 0 || (picks >= a.k && best < border))
-            break;
+        if (best == 0)
+            return false;
         const uint32_t who = __ballot_sync(full, head == best);
-        int pick;
-        if ((who & (who - 1)) == 0)
-            pick = (int)~__shfl_sync(full, (uint32_t)v[0], __ffs(who) - 1);
-        else
-            pick = (int)__reduce_min_sync(full, head == best ? ~(uint32_t)v[0] : full);
-        if (lane == picks) {
-            mine = pick;
+        int src = __ffs(who) - 1;
+        uint32_t pick = ~__shfl_sync(full, (uint32_t)v[0], src);
+        if (who & (who - 1)) {
+            pick = __reduce_min_sync(full, head == best ? ~(uint32_t)v[0] : full);
+            src = (int)(pick & 31);
+        }
+        if (lane == j) {
+            mine = (int)pick;
             my_key = best;
         }
-        if ((pick & 31) == lane) {
+        if (lane == src) {
 #pragma unroll
             for (int i = 0; i + 1 < V; ++i)
                 v[i] = v[i + 1];
             v[V - 1] = 0ull;
         }
-        border = full;
-        if (!by_logit && best > 1) {
-            const float c = from_key(best), low = c - (base_err + 0x1p-22f * fabsf(c));
-            border = low > -INFINITY ? to_key(low) : full;
-        }
-    }
-    if (close) {
-        // 32 picks and no end of close ones (or 32 chosen): one by one
-        const uint32_t rest = __reduce_max_sync(full, (uint32_t)(v[0] >> 32));
-        if (picks == 32 && rest >= border) {
-            mine = exact_picks<D>(a, r, at, kept, team, inv_size, base_err, lane);
-        } else {
-            // every value left is below all of these: order them in fp64
-            if (r.softmax && r.sum == 0.0)
-                r.sum = exact_sum<D>(a.logits, a.bias, at, a.E, r.max, lane);
-            double c = -INFINITY;       // NaN: behind the numbers
-            if (mine >= 0 && my_key > 1)
-                c = exact_choice(r.softmax, r.max, r.sum, load1<D>(a.logits, at + mine),
-                                 a.bias[mine]);
-            __syncwarp();
-            int rank = 0;
-            for (int o = 0; o < picks; ++o) {
-                const double oc = __shfl_sync(full, c, o);
-                const int oe = __shfl_sync(full, mine, o);
-                rank += oc > c || (oc == c && oe < mine);
+        return true;
+    };
+    int picks = 0;
+    for (; picks <= min(a.k, 31); ++picks)
+        if (!take(picks))
+            break;
+    if (!by_logit) {
+        // a next pick with this key or more is too close to this lane's
+        const auto border_of = [&](uint32_t k) {
+            const float c = from_key(k), low = c - (base_err + 0x1p-22f * fabsf(c));
+            return k > 1 && low > -INFINITY ? to_key(low) : full;
+        };
+        const uint32_t border = border_of(my_key);
+        const uint32_t next = __shfl_down_sync(full, my_key, 1);
+        bool close = __any_sync(full, lane < picks - 1 && next >= border);
+        if (a.k == 32)          // its runner-up is no pick
+            close |= __reduce_max_sync(full, (uint32_t)(v[0] >> 32)) >= __shfl_sync(full, border, 31);
+        if (close) {
+            // past the last one while the next is too close to it
+            uint32_t edge = __shfl_sync(full, border, max(picks - 1, 0)), rest;
+            while ((rest = __reduce_max_sync(full, (uint32_t)(v[0] >> 32))) != 0 && rest >= edge &&
+                   picks < 32) {
+                take(picks++);
+                edge = border_of(rest);
             }
-            int sorted = -1;
-            for (int o = 0; o < picks; ++o) {
-                const int orank = __shfl_sync(full, rank, o), oe = __shfl_sync(full, mine, o);
-                sorted = orank == lane ? oe : sorted;
+            if (picks == 32 && rest >= edge) {
+                // 32 picks and no end of close ones: one by one
+                mine = exact_picks<D>(a, r, at, kept, team, inv_size, base_err, lane);
+            } else {
+                // every value left is below all of these: order them in fp64
+                if (r.softmax && r.sum == 0.0)
+                    r.sum = exact_sum<D>(a.logits, a.bias, at, a.E, r.max, lane);
+                double c = -INFINITY;       // NaN: behind the numbers
+                if (mine >= 0 && my_key > 1)
+                    c = exact_choice(r.softmax, r.max, r.sum, load1<D>(a.logits, at + mine),
+                                     a.bias[mine]);
+                __syncwarp();
+                int rank = 0;
+                for (int o = 0; o < picks; ++o) {
+                    const double oc = __shfl_sync(full, c, o);
+                    const int oe = __shfl_sync(full, mine, o);
+                    rank += oc > c || (oc == c && oe < mine);
+                }
+                int sorted = -1;
+                for (int o = 0; o < picks; ++o) {
+                    const int orank = __shfl_sync(full, rank, o), oe = __shfl_sync(full, mine, o);
+                    sorted = orank == lane ? oe : sorted;
+                }
+                mine = sorted;
             }
-            mine = sorted;
         }
     }
     if (lane >= a.k)
