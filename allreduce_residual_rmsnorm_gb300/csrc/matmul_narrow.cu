@@ -9,13 +9,13 @@
 //
 // Each block of 128 of the depth goes to a tensor-memory buffer of its own and
 // is added, times sa * sb, to fp32 registers: a thread has one column of the
-// output, the rows' scales come through shared memory.
+// output, the rows' scales come through shared memory, made ahead by two warps.
 //
 // Shared memory is sized so that at most two blocks share an SM, which keeps
 // their tensor memory (256 columns each at most) within the SM's 512: no block
 // of a cluster can wait for tensor memory that waits for its cluster.
 //
-// Warps 0-3: add and store; warp 4: copies; warp 5: products.
+// Warps 0-3: add and store; warp 4: copies; warp 5: products; warps 6, 7: scales.
 #include "matmul_internal.h"
 #include "tensor_core.cuh"
 
@@ -24,9 +24,9 @@ namespace {
 
 constexpr int kN = 128, kK = 128;          // columns per block, depth per step
 constexpr int kBytesW = kN * kK;
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kMaxStages = 10;
-constexpr int kScaleSlots = 4;
+constexpr int kAhead = 8;                  // blocks of the depth per group of scales
 
 __host__ __device__ constexpr int buffers(int tokens) { return tokens <= 64 ? 4 : 2; }
 
@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(kThreads)
     constexpr uint32_t kCols = TOK * kBufs;
     constexpr int kStage = kBytesW + TOK * kK;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(16) float scale_sh[kScaleSlots][TOK];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kBufs + 1];
+    __shared__ __align__(16) float scale_sh[2][kAhead][TOK];     // two groups of scales
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kBufs + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads)
     float* sums = reinterpret_cast<float*>(dyn + (stage0 - smem_u32(dyn)) + stages * kStage);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages,
                    tfull = empty + 8 * kMaxStages, tempty = tfull + 8 * kBufs,
-                   done = tempty + 8 * kBufs;
+                   sfull = tempty + 8 * kBufs, sempty = sfull + 16, done = sempty + 16;
     const Bail bail{smem_u32(&dead), status};
     if (tid == 0) {
         dead = 0;
@@ -93,6 +93,10 @@ __global__ void __launch_bounds__(kThreads)
         for (int b = 0; b < kBufs; ++b) {
             bar_init(tfull + 8 * b, 1);
             bar_init(tempty + 8 * b, 4);
+        }
+        for (int g = 0; g < 2; ++g) {
+            bar_init(sfull + 8 * g, 2);
+            bar_init(sempty + 8 * g, 4);
         }
         bar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t step = (int64_t)gridDim.y * TOK;
 
     // per role: position in the ring of stages and of tensor-memory buffers
-    uint32_t s = 0, ph = 0, it = 0, issued = 0;
+    uint32_t s = 0, ph = 0, it = 0, grp = 0, issued = 0;
     bool ok = true;
     for (int64_t m0 = row0 + (int64_t)blockIdx.y * TOK; m0 < row1; m0 += step) {
         if (warp == 4) {
@@ -137,84 +141,110 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
         } else if (warp == 5) {
-            constexpr uint32_t idesc = fp8_idesc(kN, TOK);
-            const uint64_t desc0 = smem_desc(stage0);
-            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                const uint32_t b = it % kBufs;
-                ok = __all_sync(0xffffffffu,
-                                bar_wait(tempty + 8 * b, (it / kBufs & 1) ^ 1, bail, 2) &&
-                                    bar_wait(full + 8 * s, ph, bail, 3));
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t dw = desc0 + (uint64_t)(s * (kStage >> 4));
-                    const uint64_t dx = dw + (kBytesW >> 4);
-#pragma unroll
-                    for (int k = 0; k < kK / 32; ++k)
-                        mma_fp8(tmem + b * TOK, dw + 2 * k, dx + 2 * k, idesc, k > 0);
+            if (elect_one()) {
+                constexpr uint32_t idesc = fp8_idesc(kN, TOK);
+                const uint64_t desc0 = smem_desc(stage0);
+                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                    const uint32_t b = it % kBufs;
+                    if (!(ok = bar_wait(full + 8 * s, ph, bail, 3)) ||
+                        !(ok = bar_wait(tempty + 8 * b, (it / kBufs & 1) ^ 1, bail, 2)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t w = (uint32_t)desc0 + s * (kStage >> 4);
+                    mma4_fp8(tmem + b * TOK, w, w + (kBytesW >> 4), (uint32_t)(desc0 >> 32), idesc);
                     mma_commit(empty + 8 * s);
                     mma_commit(tfull + 8 * b);
-                }
-                __syncwarp();
-                if (++s == (uint32_t)stages) {
-                    s = 0;
-                    ph ^= 1;
+                    if (++s == (uint32_t)stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
-        } else {
+            __syncwarp();
+        } else if (warp >= 6) {
+            // a group of blocks of the depth in flight per row
             const int have = (int)min((int64_t)TOK, row1 - m0);
-            const int n = n0 + tid;
             const int ncb = (a.cols + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK;
             const float* sb = a.sb + ((uint64_t)e * ncb + n0 / AR_QUANT_BLOCK) * nkb;
-            const float* sa = a.sa + (uint64_t)(m0 + (tid < have ? tid : 0)) * nkb;
+            for (int kb = kb0; kb < kb1 && ok; kb += kAhead, ++grp) {
+                const uint32_t g = grp & 1;
+                float v[kAhead], w[TOK > 64 ? kAhead : 1];
+                const int r = 32 * (warp - 6) + lane, r2 = r + 64;
+                const float* sa = a.sa + (uint64_t)(m0 + (r < have ? r : 0)) * nkb;
+                const float* sa2 = a.sa + (uint64_t)(m0 + (r2 < have ? r2 : 0)) * nkb;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int k = min(kb + j, kb1 - 1);
+                    const float f = sb[k];
+                    v[j] = r < TOK ? sa[k] * f : 0.0f;
+                    if constexpr (TOK > 64)
+                        w[j] = sa2[k] * f;
+                }
+                ok = __all_sync(0xffffffffu, bar_wait(sempty + 8 * g, (grp >> 1 & 1) ^ 1, bail, 5));
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (r < TOK)
+                        scale_sh[g][j][r] = v[j];
+                    if constexpr (TOK > 64)
+                        scale_sh[g][j][r2] = w[j];
+                }
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(sfull + 8 * g);
+            }
+        } else {
+            // A wait that gives up is not looked at here: the sums are then
+            // undefined as the status says, and every later wait returns at once.
+            const int have = (int)min((int64_t)TOK, row1 - m0);
+            const int n = n0 + tid;
             uint64_t acc[TOK / 2];
 #pragma unroll
             for (int i = 0; i < TOK / 2; ++i)
                 acc[i] = 0ull;
-            float next = tid < TOK && kb0 < kb1 ? sa[kb0] * sb[kb0] : 0.0f;
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                // a slot is read no later than one barrier after this one: of
-                // four slots the one written here is out of use
-                if (tid < TOK)
-                    scale_sh[it % kScaleSlots][tid] = next;
-                if (tid < TOK && kb + 1 < kb1)
-                    next = sa[kb + 1] * sb[kb + 1];
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                const uint32_t b = it % kBufs;
-                ok = ok && __all_sync(0xffffffffu, bar_wait(tfull + 8 * b, it / kBufs & 1, bail, 4));
-                if (!ok)
-                    continue;           // the barrier above still counts every warp
-                tc_fence_after();
-                const float4* sc = reinterpret_cast<const float4*>(scale_sh[it % kScaleSlots]);
-                const uint32_t from = tmem + ((uint32_t)(32 * warp) << 16) + b * TOK;
-                uint32_t d[2][16];
-                tmem_ld16(from, d[0]);
+            for (int kg = kb0; kg < kb1; kg += kAhead, ++grp) {
+                const uint32_t g = grp & 1;
+                bar_wait(sfull + 8 * g, grp >> 1 & 1, bail, 6);
+                const int steps = min(kAhead, kb1 - kg);
+                for (int j = 0; j < steps; ++j, ++it) {
+                    const uint32_t b = it % kBufs;
+                    bar_wait(tfull + 8 * b, it / kBufs & 1, bail, 4);
+                    __syncwarp();
+                    tc_fence_after();
+                    const float4* sc = reinterpret_cast<const float4*>(scale_sh[g][j]);
+                    const uint32_t from = tmem + ((uint32_t)(32 * warp) << 16) + b * TOK;
+                    uint32_t d[2][16];
+                    tmem_ld16(from, d[0]);
 #pragma unroll
-                for (int c = 0; c < TOK / 16; ++c) {
-                    tmem_wait(d[c & 1]);
-                    if (c + 1 < TOK / 16)
-                        tmem_ld16(from + 16 * (c + 1), d[(c + 1) & 1]);
-                    if (c + 1 == TOK / 16) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive(tempty + 8 * b);
-                    }
+                    for (int c = 0; c < TOK / 16; ++c) {
+                        tmem_wait(d[c & 1]);
+                        if (c + 1 < TOK / 16)
+                            tmem_ld16(from + 16 * (c + 1), d[(c + 1) & 1]);
+                        if (c + 1 == TOK / 16) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(tempty + 8 * b);
+                        }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = sc[4 * c + i];
-                        fma_pair(acc[8 * c + 2 * i],
-                                 pack_pair(d[c & 1][4 * i], d[c & 1][4 * i + 1]),
-                                 pack_pair(__float_as_uint(f.x), __float_as_uint(f.y)));
-                        fma_pair(acc[8 * c + 2 * i + 1],
-                                 pack_pair(d[c & 1][4 * i + 2], d[c & 1][4 * i + 3]),
-                                 pack_pair(__float_as_uint(f.z), __float_as_uint(f.w)));
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = sc[4 * c + i];
+                            fma_pair(acc[8 * c + 2 * i],
+                                     pack_pair(d[c & 1][4 * i], d[c & 1][4 * i + 1]),
+                                     pair_of(f.x, f.y));
+                            fma_pair(acc[8 * c + 2 * i + 1],
+                                     pack_pair(d[c & 1][4 * i + 2], d[c & 1][4 * i + 3]),
+                                     pair_of(f.z, f.w));
+                        }
                     }
                 }
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(sempty + 8 * g);
             }
             if (split == 1) {
-                if (ok && n < a.cols) {
+                if (n < a.cols) {
 #pragma unroll
                     for (int i = 0; i < TOK / 2; ++i) {
                         const float2 f = unpack_pair(acc[i]);
@@ -249,6 +279,8 @@ __global__ void __launch_bounds__(kThreads)
             cluster_barrier();
         }
     }
+    if (warp == 5)
+        ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
         if (warp == 4) {
             // a block that gave up waits for its copies in flight

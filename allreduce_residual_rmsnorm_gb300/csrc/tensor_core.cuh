@@ -224,16 +224,43 @@ __host__ __device__ constexpr uint32_t fp8_idesc(int M, int N)
 {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// d (+)= a * b over 32 of K, by one thread
-__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool add)
+// Four products, 128 of K: d = a * b.  `a` and `b` are the low words of the
+// descriptors, `hi` their common high word.  One asm block, and the loop around
+// it run by one thread: with votes and descriptor arithmetic between them the
+// products were issued every 110 cycles at best (64 is what 128 columns take),
+// and later still while other warps of the scheduler had arithmetic to issue.
+// GROUP: cta_group::1, or ::2 for a pair, whose first block issues; M then
+// counts the rows of both blocks, each of which holds its rows of a and half
+// the rows of b.
+#define ARF_MMA4(GROUP)                                                              \
+    asm volatile(                                                                    \
+        "{\n\t.reg .b64 p, q;\n\t.reg .b32 x, y;\n\t.reg .pred no, yes;\n\t"           \
+        "setp.ne.b32 no, 0, 0;\n\tsetp.ne.b32 yes, 1, 0;\n\t"                          \
+        "mov.b64 p, {%1, %3};\n\tmov.b64 q, {%2, %3};\n\t"                             \
+        "tcgen05.mma." GROUP ".kind::f8f6f4 [%0], p, q, %4, no;\n\t"                   \
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"                                   \
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"                               \
+        "tcgen05.mma." GROUP ".kind::f8f6f4 [%0], p, q, %4, yes;\n\t"                  \
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"                                   \
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"                               \
+        "tcgen05.mma." GROUP ".kind::f8f6f4 [%0], p, q, %4, yes;\n\t"                  \
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"                                   \
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"                               \
+        "tcgen05.mma." GROUP ".kind::f8f6f4 [%0], p, q, %4, yes;\n\t}" ::"r"(d),         \
+        "r"(a), "r"(b), "r"(hi), "r"(idesc)                                          \
+        : "memory")
+
+__device__ __forceinline__ void mma4_fp8(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                         uint32_t idesc)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+    ARF_MMA4("cta_group::1");
 }
+__device__ __forceinline__ void mma4_fp8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                              uint32_t idesc)
+{
+    ARF_MMA4("cta_group::2");
+}
+#undef ARF_MMA4
 // one arrival on `bar` once every product issued so far by this thread is done
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
@@ -242,33 +269,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
         : "memory");
 }
 
-// Four products, 128 of K, of a pair, issued by its first block: M counts the
-// rows of both, each block holds its rows of a and half the rows of b.  `a` and
-// `b` are the low words of the descriptors, `hi` their common high word.  One
-// asm block, and the loop around it run by one thread: with votes and
-// descriptor arithmetic between them the products were issued every 110 cycles
-// at best (64 is what 128 columns take), and later still while other warps of
-// the scheduler had arithmetic to issue.
-__device__ __forceinline__ void mma4_fp8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                              uint32_t idesc)
-{
-    asm volatile(
-        "{\n\t.reg .b64 p, q;\n\t.reg .b32 x, y;\n\t.reg .pred no, yes;\n\t"
-        "setp.ne.b32 no, 0, 0;\n\tsetp.ne.b32 yes, 1, 0;\n\t"
-        "mov.b64 p, {%1, %3};\n\tmov.b64 q, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, no;\n\t"
-        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
-        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t"
-        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
-        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t"
-        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
-        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], p, q, %4, yes;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(hi), "r"(idesc)
-        : "memory");
-}
 // The commit arrives at the same barrier of both blocks.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
 {
