@@ -25,7 +25,7 @@ struct DeviceInfo {
 // Tokens on the lanes of tensor memory, 256 x 256 outputs per pair of blocks: many rows.
 cudaError_t launch_matmul_wide(int dtype, const MatmulArgs& a, const DeviceInfo& d,
                                cudaStream_t s);
-// Weights on the lanes, `tokens` (16, 32, 64 or 128) rows at a time, the depth
+// Weights on the lanes, `tokens` (16, 32 or 64) rows at a time, the depth
 // split over `split` blocks of a cluster: few rows per expert.
 cudaError_t launch_matmul_narrow(int dtype, const MatmulArgs& a, int tokens, int split,
                                  const DeviceInfo& d, cudaStream_t s);

@@ -1,6 +1,6 @@
 // 8-bit product for few rows per expert: the weights are read once and bound
 // the time, so they take the 128 lanes of tensor memory (128 columns of the
-// output per block) and the token rows its columns, 16 to 128 at a time.
+// output per block) and the token rows its columns, 16 to 64 at a time.
 //
 // The depth is split over the blocks of a cluster where one block per 128
 // columns would leave SMs idle; their fp32 sums meet in distributed shared
@@ -25,10 +25,9 @@ namespace {
 constexpr int kN = 128, kK = 128;          // columns per block, depth per step
 constexpr int kBytesW = kN * kK;
 constexpr int kThreads = 256;
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 10, kMaxSplit = 8;
+constexpr int kBufs = 4;                   // of tensor memory
 constexpr int kAhead = 8;                  // blocks of the depth per group of scales
-
-__host__ __device__ constexpr int buffers(int tokens) { return tokens <= 64 ? 4 : 2; }
 
 template <class D>
 __device__ __forceinline__ void store1(void* out, uint64_t i, float v)
@@ -56,7 +55,6 @@ __global__ void __launch_bounds__(kThreads)
                          const __grid_constant__ CUtensorMap map_b, MatmulArgs a, int* status,
                          int split, int stages)
 {
-    constexpr int kBufs = buffers(TOK);
     constexpr uint32_t kCols = TOK * kBufs;
     constexpr int kStage = kBytesW + TOK * kK;
     extern __shared__ uint8_t dyn[];
@@ -168,17 +166,14 @@ __global__ void __launch_bounds__(kThreads)
             const float* sb = a.sb + ((uint64_t)e * ncb + n0 / AR_QUANT_BLOCK) * nkb;
             for (int kb = kb0; kb < kb1 && ok; kb += kAhead, ++grp) {
                 const uint32_t g = grp & 1;
-                float v[kAhead], w[TOK > 64 ? kAhead : 1];
-                const int r = 32 * (warp - 6) + lane, r2 = r + 64;
+                float v[kAhead];
+                const int r = 32 * (warp - 6) + lane;
                 const float* sa = a.sa + (uint64_t)(m0 + (r < have ? r : 0)) * nkb;
-                const float* sa2 = a.sa + (uint64_t)(m0 + (r2 < have ? r2 : 0)) * nkb;
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     const int k = min(kb + j, kb1 - 1);
                     const float f = sb[k];
                     v[j] = r < TOK ? sa[k] * f : 0.0f;
-                    if constexpr (TOK > 64)
-                        w[j] = sa2[k] * f;
                 }
                 ok = __all_sync(0xffffffffu, bar_wait(sempty + 8 * g, (grp >> 1 & 1) ^ 1, bail, 5));
                 if (!ok)
@@ -187,8 +182,6 @@ __global__ void __launch_bounds__(kThreads)
                 for (int j = 0; j < kAhead; ++j) {
                     if (r < TOK)
                         scale_sh[g][j][r] = v[j];
-                    if constexpr (TOK > 64)
-                        scale_sh[g][j][r2] = w[j];
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -268,12 +261,26 @@ __global__ void __launch_bounds__(kThreads)
             if (warp < 4) {
                 const int have = (int)min((int64_t)TOK, row1 - m0);
                 const int n = n0 + tid;
-                for (int c = rank; c < have; c += split) {
-                    float v = 0.0f;
-                    for (int q = 0; q < split; ++q)
-                        v += ld_dsmem_f32(sums + c * kN + tid, q);
-                    if (n < a.cols)
-                        store1<D>(a.out, (uint64_t)(m0 + c) * a.cols + n, v);
+                // four of this block's rows from all blocks before the first
+                // addition: one at a time their latency was most of a small call
+                for (int c0 = rank; c0 < have; c0 += 4 * split) {
+                    float part[4][kMaxSplit];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int q = 0; q < kMaxSplit; ++q)
+                            if (q < split && c0 + i * split < have)
+                                part[i][q] = ld_dsmem_f32(sums + (c0 + i * split) * kN + tid, q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = c0 + i * split;
+                        float v = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < kMaxSplit; ++q)
+                            v += q < split && c < have ? part[i][q] : 0.0f;
+                        if (c < have && n < a.cols)
+                            store1<D>(a.out, (uint64_t)(m0 + c) * a.cols + n, v);
+                    }
                 }
             }
             cluster_barrier();
@@ -311,8 +318,7 @@ cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaSt
         !byte_tensor_map(&map_b, a.b, (uint64_t)a.experts * a.cols, (uint64_t)a.depth, kN))
         return cudaErrorInvalidValue;
     constexpr int kStage = kBytesW + TOK * kK;
-    // two blocks per SM (112 KB each) up to 64 rows at a time, else one
-    const int budget = TOK <= 64 ? 108 * 1024 : 200 * 1024;
+    const int budget = 106 * 1024;  // two blocks per SM
     const int sums = split > 1 ? TOK * kN * 4 : 0;
     int stages = (budget - sums - 1024) / kStage;
     stages = stages > kMaxStages ? kMaxStages : stages;
@@ -347,8 +353,7 @@ cudaError_t launch_d(const MatmulArgs& a, int tokens, int split, const DeviceInf
     switch (tokens) {
     case 16: return launch_t<D, 16>(a, split, d, s);
     case 32: return launch_t<D, 32>(a, split, d, s);
-    case 64: return launch_t<D, 64>(a, split, d, s);
-    default: return launch_t<D, 128>(a, split, d, s);
+    default: return launch_t<D, 64>(a, split, d, s);
     }
 }
 
