@@ -382,6 +382,40 @@ def test_matmul(dt, rows, cols, depth):
     assert (guard[rows * cols:] == 77.0).all()
 
 
+# rows, columns and depths where 256 x 256 tiles of a pair of blocks are the faster
+# kernel: several tiles per pair, rows and columns that end inside a tile, rows whose
+# bytes are no multiple of 16, one block of the depth and a part of one
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,cols,depth", [
+    (1100, 1288, 656), (2000, 1027, 784), (700, 4104, 1040), (5200, 2312, 400),
+    (2561, 3976, 128), (4095, 2049, 144), (1, 70000, 2064), (1024, 2048, 1152)])
+def test_matmul_many_rows(dt, rows, cols, depth):
+    test_matmul(dt, rows, cols, depth)
+
+
+def test_matmul_status_is_clear():
+    assert B.ar_fusion_matmul_status() == (B.AR_OK, -1)
+
+
+def test_operands_that_are_not_contiguous_or_aligned_are_refused():
+    z = lambda d, *s: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+    u8, f32 = torch.uint8, torch.float32
+    a, sa, b, sb, out = z(u8, 64, 64), z(f32, 64, 1), z(u8, 64, 64), z(f32, 1, 1), z(f32, 64, 64)
+    with pytest.raises(ValueError, match="contiguous"):
+        B.ar_fusion_matmul_fp8(a.t(), sa, b, sb, out)
+    with pytest.raises(ValueError, match="out: expected a contiguous"):
+        B.ar_fusion_matmul_fp8(a, sa, b, sb, out.t())
+    with pytest.raises(B.ArFusionError, match="aligned"):
+        B.ar_fusion_matmul_fp8(z(u8, 64 * 64 + 8)[8:].view(64, 64), sa, b, sb, out)
+    with pytest.raises(B.ArFusionError, match="multiple of 16"):
+        B.ar_fusion_matmul_fp8(z(u8, 8, 40), z(f32, 8, 1), z(u8, 8, 40), sb, z(f32, 8, 8))
+    with pytest.raises(ValueError, match="scale_out: shape"):
+        B.ar_fusion_quant_blocks(z(f32, 4, 256), z(u8, 4, 256), z(f32, 4, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.ar_fusion_combine(z(f32, 4, 16), torch.zeros(2, 2, dtype=torch.int32), z(f32, 2, 2),
+                            z(f32, 2, 16))
+
+
 def test_matmul_nan_and_infinite_scales_stay_in_their_row():
     g = gen(21)
     for rows in (5, 200):
@@ -425,7 +459,10 @@ def check_experts(rows, cols, depth, bounds, dt, seed):
     (128, 128, [1]), (136, 160, [0, 3, 0]), (256, 512, [5, 0, 17, 1, 0, 0, 40]),
     (520, 400, [1, 1, 1, 1, 1, 1, 1, 1]), (384, 256, [300, 0, 2, 129]), (200, 144, [0, 0, 0]),
     (264, 640, [64, 65, 63, 1, 200, 128, 127]), (1000, 272, [700, 1, 30]),
-    (128, 256, [2] * 100), (256, 128, [0] * 40 + [500] + [3] * 9)])
+    (128, 256, [2] * 100), (256, 128, [0] * 40 + [500] + [3] * 9),
+    # pairs of blocks: tiles that end at, before and behind an expert's last row
+    (1288, 656, [300, 0, 2, 129, 500]), (1027, 784, [256, 255, 257, 1, 0, 512]),
+    (2312, 1040, [900, 130, 31, 33, 700])])
 def test_expert_matmul(dt, cols, depth, loads):
     bounds = np.concatenate([[0], np.cumsum(loads)]).tolist()
     rows = bounds[-1] + 9                    # rows behind the last expert stay as they were
