@@ -462,6 +462,12 @@ def _operand(t: torch.Tensor, dtypes, shape, dev: int):
     raise _Refused
 
 
+def _call(name: str, args) -> None:
+    rc = getattr(_lib or load(), name)(*args)
+    if rc:
+        _check(rc)
+
+
 def _device_of(t: torch.Tensor) -> int:
     """The operands' device, which is the current one: the library launches there."""
     dev = t.get_device()
@@ -493,8 +499,9 @@ def _explain(*operands) -> None:
     raise ValueError("operands do not fit together")
 
 
-def _dims(n: int, **tensors) -> None:
-    for name, t in tensors.items():
+def _shapes(*named) -> None:
+    """Raises for the first (name, tensor, n) that has not n dimensions."""
+    for name, t, n in named:
         if t.dim() != n:
             raise ValueError(f"{name}: {t.dim()} dimensions, expected {n}")
 
@@ -511,7 +518,8 @@ def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: to
                     renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
     """logits [tokens, experts]; bias [experts] fp32 or None; ids_out (int32)
     and weights_out (fp32) [tokens, topk]."""
-    _dims(2, logits=logits, ids_out=ids_out)
+    if logits.dim() != 2 or ids_out.dim() != 2:
+        _shapes(("logits", logits, 2), ("ids_out", ids_out, 2))
     tokens, experts = logits.shape
     topk = ids_out.shape[1]
     slots = (tokens, topk)
@@ -526,7 +534,7 @@ def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: to
     except _Refused:
         _explain(("logits", logits, _ELEM, None), ("ids_out", ids_out, _I32, slots),
                  ("weights_out", weights_out, _F32, slots), ("bias", bias, _F32, (experts,)))
-    _check(lib().ar_fusion_route(*args))
+    _call("ar_fusion_route", args)
 
 
 def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Tensor,
@@ -534,7 +542,8 @@ def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Te
                           stream=None) -> None:
     """ids [tokens, topk] int32; offsets_out [experts + 1] and position_out
     [tokens, topk] int32, for the experts first_expert .. first_expert + experts - 1."""
-    _dims(2, ids=ids)
+    if ids.dim() != 2:
+        _shapes(("ids", ids, 2))
     slots = ids.shape
     try:
         dev = _device_of(ids)
@@ -544,7 +553,7 @@ def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Te
     except _Refused:
         _explain(("ids", ids, _I32, None), ("offsets_out", offsets_out, _I32, (experts + 1,)),
                  ("position_out", position_out, _I32, slots))
-    _check(lib().ar_fusion_expert_plan(*args))
+    _call("ar_fusion_expert_plan", args)
 
 
 def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: torch.Tensor,
@@ -555,12 +564,14 @@ def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: 
     [out_rows, hidden] (uint8 or float8_e4m3fn); scale_out [out_rows,
     ceil(hidden / 128)] fp32; position [rows, copies] int32 or None; row_count: a
     one-element int32 tensor or None (a view of the plan's last offset)."""
-    _dims(2, x=x, quant_out=quant_out)
+    if x.dim() != 2 or quant_out.dim() != 2:
+        _shapes(("x", x, 2), ("quant_out", quant_out, 2))
     rows = x.shape[0]
     out_rows, hidden = quant_out.shape
     copies = 1
     if position is not None:
-        _dims(2, position=position)
+        if position.dim() != 2:
+            _shapes(("position", position, 2))
         copies = position.shape[1]
     shape = (rows, 2 * hidden if activation == AR_ACT_SILU_MUL else hidden)
     scales = (out_rows, (hidden + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK)
@@ -576,14 +587,15 @@ def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: 
                  ("scale_out", scale_out, _F32, scales),
                  ("position", position, _I32, (rows, copies)),
                  ("row_count", row_count, _I32, (1,)))
-    _check(lib().ar_fusion_quant_blocks(*args))
+    _call("ar_fusion_quant_blocks", args)
 
 
 def ar_fusion_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
                          b_scale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """a [rows, depth], b [cols, depth] (uint8 or float8_e4m3fn); a_scale [rows,
     ceil(depth / 128)], b_scale [ceil(cols / 128), ceil(depth / 128)] fp32; out [rows, cols]."""
-    _dims(2, a=a, b=b)
+    if a.dim() != 2 or b.dim() != 2:
+        _shapes(("a", a, 2), ("b", b, 2))
     rows, depth = a.shape
     cols = b.shape[0]
     blocks = (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
@@ -599,7 +611,7 @@ def ar_fusion_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor
                  ("a_scale", a_scale, _F32, (rows, blocks)),
                  ("b_scale", b_scale, _F32, (col_blocks, blocks)),
                  ("out", out, _ELEM, (rows, cols)))
-    _check(lib().ar_fusion_matmul_fp8(*args))
+    _call("ar_fusion_matmul_fp8", args)
 
 
 def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
@@ -607,8 +619,8 @@ def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch
                                 stream=None) -> None:
     """ar_fusion_matmul_fp8 by experts: b [experts, cols, depth], b_scale
     [experts, ceil(cols / 128), ceil(depth / 128)], offsets [experts + 1] int32."""
-    _dims(2, a=a)
-    _dims(3, b=b)
+    if a.dim() != 2 or b.dim() != 3:
+        _shapes(("a", a, 2), ("b", b, 3))
     rows, depth = a.shape
     experts, cols, _ = b.shape
     blocks = (depth + AR_QUANT_BLOCK - 1) // AR_QUANT_BLOCK
@@ -625,7 +637,7 @@ def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch
                  ("a_scale", a_scale, _F32, (rows, blocks)),
                  ("b_scale", b_scale, _F32, (experts, col_blocks, blocks)),
                  ("offsets", offsets, _I32, (experts + 1,)), ("out", out, _ELEM, (rows, cols)))
-    _check(lib().ar_fusion_expert_matmul_fp8(*args))
+    _call("ar_fusion_expert_matmul_fp8", args)
 
 
 def ar_fusion_matmul_status(stream=None):
@@ -643,7 +655,8 @@ def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: to
                       out: torch.Tensor, add: torch.Tensor | None = None, stream=None) -> None:
     """rows_in [in_rows, hidden]; position (int32) and weights (fp32) [tokens,
     topk]; out and add [tokens, hidden], of rows_in's type."""
-    _dims(2, rows_in=rows_in, position=position)
+    if rows_in.dim() != 2 or position.dim() != 2:
+        _shapes(("rows_in", rows_in, 2), ("position", position, 2))
     in_rows, hidden = rows_in.shape
     slots = tokens, topk = position.shape
     same, shape = (rows_in.dtype,), (tokens, hidden)
@@ -658,4 +671,4 @@ def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: to
         _explain(("rows_in", rows_in, _ELEM, None), ("position", position, _I32, None),
                  ("weights", weights, _F32, slots), ("out", out, same, shape),
                  ("add", add, same, shape))
-    _check(lib().ar_fusion_combine(*args))
+    _call("ar_fusion_combine", args)

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ar_fusion.h"
 
 namespace arf {
@@ -79,6 +81,24 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Runs `set` the first time on each device (below 64; on others every time): the
+// attributes of a kernel that outlast the call.  Two threads may both run it.
+template <class F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 inline int quant_blocks(int depth) { return (depth + AR_QUANT_BLOCK - 1) / AR_QUANT_BLOCK; }

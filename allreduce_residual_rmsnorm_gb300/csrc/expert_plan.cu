@@ -192,8 +192,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bi
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(uint32_t) * (kMaxWarps + 1) * AR_MAX_EXPERTS));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(sizeof(uint32_t) * (kMaxWarps + 1) * AR_MAX_EXPERTS));
+    });
     if (e != cudaSuccess)
         return e;
     // one block up to four rounds a warp; 8 warps at least, for the experts

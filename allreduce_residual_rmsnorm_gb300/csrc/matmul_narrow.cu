@@ -324,8 +324,10 @@ cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaSt
     stages = stages > kMaxStages ? kMaxStages : stages;
     const int smem = budget;        // the whole of it: never three blocks per SM
     const auto kernel = matmul_narrow_kernel<D, TOK>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
     if (e != cudaSuccess)
         return e;
     const int per = (a.rows + a.experts - 1) / a.experts;

@@ -455,17 +455,20 @@ cudaError_t launch_t(const MatmulArgs& a, const DeviceInfo& d, cudaStream_t s)
         (aligned && !out_tensor_map(&map_out, a.out, (uint64_t)a.rows, (uint64_t)a.cols, D::id, 32,
                                     kOutRow / D::bytes)))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(matmul_wide_kernel<D>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        // fewer registers at launch than the shares add up to would wait for ever
+        cudaFuncAttributes attr;
+        const cudaError_t ea = cudaFuncGetAttributes(&attr, matmul_wide_kernel<D>);
+        if (ea != cudaSuccess)
+            return ea;
+        if (attr.numRegs < kRegsLaunch)
+            return cudaErrorLaunchOutOfResources;
+        return cudaFuncSetAttribute(matmul_wide_kernel<D>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
     if (e != cudaSuccess)
         return e;
-    // fewer registers at launch than the shares add up to would wait for ever
-    cudaFuncAttributes attr;
-    const cudaError_t ea = cudaFuncGetAttributes(&attr, matmul_wide_kernel<D>);
-    if (ea != cudaSuccess)
-        return ea;
-    if (attr.numRegs < kRegsLaunch)
-        return cudaErrorLaunchOutOfResources;
     // at most this many tiles: every expert may end in a part of one
     const int64_t most = ((int64_t)a.rows / kM + (a.experts < a.rows ? a.experts : a.rows)) *
                          ((a.cols + kN - 1) / kN);
