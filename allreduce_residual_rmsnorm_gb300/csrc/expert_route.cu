@@ -34,14 +34,21 @@ constexpr int kWarps = 4;       // rows per block
 __device__ __forceinline__ uint32_t to_key(float v)
 {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     return v == v ? k : 1u;
 }
 __device__ __forceinline__ float from_key(uint32_t k)
 {
-    return k == 1u ? __uint_as_float(0x7fc00000u)
-                   : __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+    const uint32_t u = k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u);
+    return __uint_as_float(k == 1u ? 0x7fc00000u : u);
 }
+
+// a call's sizes, divided out on the host: experts per group, lanes per group and
+// their logarithm, 1 / experts per group
+struct Shape {
+    int size, team, shift;
+    float inv_size;
+};
 
 struct Row {
     int softmax;
@@ -88,18 +95,24 @@ __device__ __noinline__ double exact_sum(const void* logits, const float* bias, 
 template <class D>
 __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, const uint32_t* key,
                                                 uint64_t at, bool by_logit, float bias0,
-                                                float base_err, int lane, int team)
+                                                float base_err, int lane, const Shape& sh)
 {
     const uint32_t full = 0xffffffffu;
-    const int size = a.E / a.G;
-    const int g = lane / team, sub = lane & (team - 1);
+    const int size = sh.size, team = sh.team;
+    const int g = lane >> sh.shift, sub = lane & (team - 1);
     uint32_t k1 = 0, k2 = 0;
     if (g < a.G) {
+        // each team starts at a place of its own: with 32 experts a group they
+        // would all read the same bank
+        const int n = (size - sub + team - 1) >> sh.shift;
+        int t = sub + (g < n ? g * team : 0);
 #pragma unroll 4
-        for (int t = sub; t < size; t += team) {
+        for (int i = 0; i < n; ++i) {
             const uint32_t k = key[g * size + t];
             k2 = max(k2, min(k1, k));
             k1 = max(k1, k);
+            t += team;
+            t = t < size ? t : sub;
         }
     }
     for (int m = team >> 1; m >= 1; m >>= 1) {
@@ -123,7 +136,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
     const auto rank_among = [&](auto mine) {
         int rank = 0;
         for (int o = 0; o < a.G; ++o) {
-            const auto v = __shfl_sync(full, mine, o * team);
+            const auto v = __shfl_sync(full, mine, o << sh.shift);
             rank += v > mine || (v == mine && o < g);
         }
         return rank;
@@ -188,8 +201,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Row& r, cons
 // keeping everything would cost the common path.
 template <class D>
 __device__ __noinline__ int exact_picks(const RouteArgs& a, const Row& r0, uint64_t at,
-                                        uint32_t kept, int team, float inv_size, float base_err,
-                                        int lane)
+                                        uint32_t kept, const Shape& sh, float base_err, int lane)
 {
     const uint32_t full = 0xffffffffu;
     Row r = r0;
@@ -199,7 +211,8 @@ __device__ __noinline__ int exact_picks(const RouteArgs& a, const Row& r0, uint6
     const auto key_of = [&](int e) {
         const float x = load1<D>(a.logits, at + e), b = a.bias[e];
         const bool out = x == -INFINITY || b == -INFINITY || (taken >> (e >> 5) & 1u) ||
-                         (a.G > 1 && !(kept >> ((int)(((float)e + 0.5f) * inv_size) * team) & 1u));
+                         (a.G > 1 &&
+                          !(kept >> ((int)(((float)e + 0.5f) * sh.inv_size) * sh.team) & 1u));
         return out ? 0u : to_key(quick_score(r, x) + b);
     };
     int mine = -1;
@@ -283,7 +296,7 @@ __device__ __forceinline__ void sort_down(uint64_t (&v)[V])
 }
 
 template <class D, int V>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int team)
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, Shape sh)
 {
     extern __shared__ uint32_t key_sh[];        // [kWarps][E] with groups
     const uint32_t full = 0xffffffffu;
@@ -349,7 +362,6 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
         key[i] = x[i] == -INFINITY ? 0u : to_key(o);
     }
     uint32_t kept = full;
-    float inv_size = 0.0f;
     if (a.G > 1) {
         uint32_t* keys = key_sh + warp * a.E;
 #pragma unroll
@@ -357,15 +369,26 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
             if (lane + 32 * i < a.E)
                 keys[lane + 32 * i] = key[i];
         __syncwarp();
-        kept = kept_groups<D>(a, r, keys, at, by_logit, bias0, base_err, lane, team);
-        inv_size = 1.0f / (float)(a.E / a.G);
+        kept = kept_groups<D>(a, r, keys, at, by_logit, bias0, base_err, lane, sh);
+        if (sh.size % 32 == 0) {
+            // a register of all lanes lies in one group
+            int left = sh.size, bit = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            // e < 1024: (e + 1/2) / size in fp32 is below the next whole number;
-            // an expert behind the last one has key 0 already
-            const int g = (int)(((float)(lane + 32 * i) + 0.5f) * inv_size);
-            if (!(kept >> (g * team & 31) & 1u))
-                key[i] = 0u;
+            for (int i = 0; i < V; ++i) {
+                key[i] = kept >> (bit & 31) & 1u ? key[i] : 0u;
+                left -= 32;
+                bit += left == 0 ? sh.team : 0;
+                left = left == 0 ? sh.size : left;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                // e < 1024: (e + 1/2) / size in fp32 is below the next whole
+                // number; an expert behind the last one has key 0 already
+                const int g = (int)(((float)(lane + 32 * i) + 0.5f) * sh.inv_size);
+                if (!(kept >> (g << sh.shift & 31) & 1u))
+                    key[i] = 0u;
+            }
         }
     }
     // key, then the lower expert
@@ -427,7 +450,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
             }
             if (picks == 32 && rest >= edge) {
                 // 32 picks and no end of close ones: one by one
-                mine = exact_picks<D>(a, r, at, kept, team, inv_size, base_err, lane);
+                mine = exact_picks<D>(a, r, at, kept, sh, base_err, lane);
             } else {
                 // every value left is below all of these: order them in fp64
                 if (r.softmax && r.sum == 0.0)
@@ -487,23 +510,25 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a, int tea
 template <class D>
 cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s)
 {
-    int team = 32;              // lanes per group
-    while (team * a.G > 32)
-        team >>= 1;
+    Shape sh{a.E / a.G, 32, 5, 1.0f / (float)(a.E / a.G)};
+    while (sh.team * a.G > 32) {
+        sh.team >>= 1;
+        --sh.shift;
+    }
     const unsigned grid = (unsigned)((a.T - 1) / kWarps + 1);
     const size_t smem = a.G > 1 ? sizeof(uint32_t) * kWarps * a.E : 0;
     const int per_lane = (a.E + 31) / 32;
     if (per_lane <= 1)
-        return launch_after(route_kernel<D, 1>, grid, 32 * kWarps, smem, s, a, team);
+        return launch_after(route_kernel<D, 1>, grid, 32 * kWarps, smem, s, a, sh);
     if (per_lane <= 2)
-        return launch_after(route_kernel<D, 2>, grid, 32 * kWarps, smem, s, a, team);
+        return launch_after(route_kernel<D, 2>, grid, 32 * kWarps, smem, s, a, sh);
     if (per_lane <= 4)
-        return launch_after(route_kernel<D, 4>, grid, 32 * kWarps, smem, s, a, team);
+        return launch_after(route_kernel<D, 4>, grid, 32 * kWarps, smem, s, a, sh);
     if (per_lane <= 8)
-        return launch_after(route_kernel<D, 8>, grid, 32 * kWarps, smem, s, a, team);
+        return launch_after(route_kernel<D, 8>, grid, 32 * kWarps, smem, s, a, sh);
     if (per_lane <= 16)
-        return launch_after(route_kernel<D, 16>, grid, 32 * kWarps, smem, s, a, team);
-    return launch_after(route_kernel<D, 32>, grid, 32 * kWarps, smem, s, a, team);
+        return launch_after(route_kernel<D, 16>, grid, 32 * kWarps, smem, s, a, sh);
+    return launch_after(route_kernel<D, 32>, grid, 32 * kWarps, smem, s, a, sh);
 }
 
 }  // namespace
