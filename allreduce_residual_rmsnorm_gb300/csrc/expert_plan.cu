@@ -200,7 +200,7 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     // one block up to four rounds a warp; 8 warps at least, for the experts
-    const int rounds = (a.slots + 31) / 32;
+    const int64_t rounds = ((int64_t)a.slots + 31) / 32;
     const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : kMaxBlocks;
     const int warps = rounds <= 8 ? 8 : rounds <= 16 ? 16 : kMaxWarps;
     static_assert(8 * 32 * kPerThread >= AR_MAX_EXPERTS, "experts of a block of 8 warps");

@@ -392,8 +392,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int col = n0 + c * (kOutRow / D::bytes);
                     if (col >= a.cols)
                         break;
-                    if (lane == 0)
-                        tma_store_wait_read<kOutBufs - 1>();
+                    // the first of a tile waits for all: the tile before may have
+                    // ended after an odd number, in the same buffer
+                    if (lane == 0) {
+                        if (c == 0)
+                            tma_store_wait_read<0>();
+                        else
+                            tma_store_wait_read<kOutBufs - 1>();
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < kPer; ++g) {

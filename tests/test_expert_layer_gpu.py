@@ -388,7 +388,8 @@ def test_matmul(dt, rows, cols, depth):
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows,cols,depth", [
     (1100, 1288, 656), (2000, 1027, 784), (700, 4104, 1040), (5200, 2312, 400),
-    (2561, 3976, 128), (4095, 2049, 144), (1, 70000, 2064), (1024, 2048, 1152)])
+    (2561, 3976, 128), (4095, 2049, 144), (1, 70000, 2064), (1024, 2048, 1152),
+    (20000, 272, 128), (12000, 608, 64)])
 def test_matmul_many_rows(dt, rows, cols, depth):
     test_matmul(dt, rows, cols, depth)
 
