@@ -18,14 +18,29 @@ constexpr int kThreads = 256;
 constexpr int kElems = 16;      // per thread
 constexpr float kFp8Max = 448.0f;
 
-// Two of g / (1 + e^-g) * u.  e^-g = 2^t, t = -g log2 e as a product and its
-// rounding error, which moves the power by a factor of 1 + error ln 2; then
-// the quotient G / d with G = g / 4 and d = (1 + e^-g) / 4 (a quarter, so that
-// the reciprocal of no finite d is below the normal range), by the approximate
-// reciprocal (1 ulp) and one correction.  Where the correction is no number (an
-// infinite gate, or e^-g beyond the range) the first quotient is exact.  In
-// packed pairs: with expf and the divide instructions 32 a element, which bound
-// the kernel (38.5 us at 16384 x 2048).
+// the largest magnitude of three; NaN is passed over, or wins with `_nan`
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_abs3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two of g / (1 + e^-g) * u for |g| < kPlainGate, where everything stays finite.
+// e^-g = 2^t, t = -g log2 e as a product and its rounding error, which moves the
+// power by a factor of 1 + error ln 2; then the quotient G / d with G = g / 4 and
+// d = (1 + e^-g) / 4 (a quarter, so that the reciprocal is not below the normal
+// range), by the approximate reciprocal (1 ulp) and one correction.  In packed
+// pairs: with expf and the divide instructions 32 a element, which bound the
+// kernel (38.5 us at 16384 x 2048).
+constexpr float kPlainGate = 88.0f;
+
 __device__ __forceinline__ uint64_t silu_mul_pair(uint64_t g, uint64_t u)
 {
     const float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
@@ -38,9 +53,7 @@ __device__ __forceinline__ uint64_t silu_mul_pair(uint64_t g, uint64_t u)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(-tf.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(-tf.y));
     const uint64_t pp = pair_of(p.x, p.y);
-    const float2 ef = unpack_pair(fma3_pair(pp, mul_pair(err, pair_of(kLn2, kLn2)), pp));
-    // (an infinite power times a negative correction is no number)
-    const uint64_t e = pair_of(p.x < INFINITY ? ef.x : p.x, p.y < INFINITY ? ef.y : p.y);
+    const uint64_t e = fma3_pair(pp, mul_pair(err, pair_of(kLn2, kLn2)), pp);
     const uint64_t G = mul_pair(g, quarter);
     const uint64_t minus_d = fma3_pair(e, pair_of(-0.25f, -0.25f), pair_of(-0.25f, -0.25f));
     const float2 df = unpack_pair(minus_d);
@@ -49,8 +62,13 @@ __device__ __forceinline__ uint64_t silu_mul_pair(uint64_t g, uint64_t u)
     const uint64_t rr = pair_of(r.x, r.y);
     const uint64_t q = mul_pair(G, rr);
     const uint64_t rem = fma3_pair(q, minus_d, G);
-    const float2 q0 = unpack_pair(q), rf = unpack_pair(rem), q1 = unpack_pair(fma3_pair(rem, rr, q));
-    return mul_pair(pair_of(rf.x == rf.x ? q1.x : q0.x, rf.y == rf.y ? q1.y : q0.y), u);
+    return mul_pair(fma3_pair(rem, rr, q), u);
+}
+
+// the same of one pair of numbers, for any gate
+__device__ __noinline__ float silu_mul(float g, float u)
+{
+    return g / (1.0f + expf(-g)) * u;
 }
 
 template <class D, bool ACT>
@@ -92,12 +110,23 @@ __global__ void __launch_bounds__(kThreads) block_quant_kernel(BlockQuantArgs a,
             if constexpr (ACT) {
                 float g[8];
                 unpack8<D>(u[h], g);
+                float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float2 o = unpack_pair(silu_mul_pair(pair_of(f[i], f[i + 1]),
-                                                               pair_of(g[i], g[i + 1])));
-                    f[i] = o.x;
-                    f[i + 1] = o.y;
+                for (int i = 0; i < 8; i += 2)
+                    top = max_abs3_nan(top, f[i], f[i + 1]);
+                if (top < kPlainGate) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 o = unpack_pair(silu_mul_pair(pair_of(f[i], f[i + 1]),
+                                                                   pair_of(g[i], g[i + 1])));
+                        f[i] = o.x;
+                        f[i + 1] = o.y;
+                    }
+                } else {
+                    // a gate that is no number or far out
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = silu_mul(f[i], g[i]);
                 }
             }
 #pragma unroll
@@ -105,10 +134,10 @@ __global__ void __launch_bounds__(kThreads) block_quant_kernel(BlockQuantArgs a,
                 y[8 * h + i] = f[i];
         }
     }
-    float amax = 0x1p-100f;     // fmaxf passes over NaN
+    float amax = 0x1p-100f;     // NaN is passed over
 #pragma unroll
-    for (int i = 0; i < kElems; ++i)
-        amax = fmaxf(amax, fabsf(y[i]));
+    for (int i = 0; i < kElems; i += 2)
+        amax = max_abs3(amax, y[i], y[i + 1]);
 #pragma unroll
     for (int m = 4; m >= 1; m >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));

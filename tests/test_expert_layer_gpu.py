@@ -303,6 +303,18 @@ def test_quant_blocks_special_values():
     q, s = run_quant(y, 256, False)
     assert np.isinf(s[0, 0]) and (q[0, 9] & 0x7F) == 0x7F and np.isfinite(s[0, 1])
     assert ((np.delete(q[0, :128], 9) & 0x7F) == 0).all()
+    # gates up to and beyond where e^-g leaves the fp32 range, in both directions
+    far = torch.tensor([87.9, 88.0, 88.1, 88.72, 88.73, 89.0, 103.0, 104.0, 1e4, 3e38])
+    w = torch.randn(4, 256, generator=g)
+    w[0, :10], w[1, :10], w[2, 50:60] = -far, far, -far
+    w[3, :128] = -88.5                       # a whole block of gates all but closed
+    q, s = run_quant(w, 128, True)
+    check_quant_rows(q, s, w, 128, True)
+    w[1, 3], w[2, 4] = float("nan"), -float("inf")
+    w[0, 5] = float("inf")
+    q, s = run_quant(w, 128, True)
+    assert (q[1, 3] & 0x7F) == 0x7F and (q[2, 4] & 0x7F) == 0x7F and np.isinf(s[0, 0])
+    check_quant_rows(q[3:], s[3:], w[3:], 128, True)
     # a gate far below zero closes, without NaN
     z = torch.randn(2, 256, generator=g)
     z[:, :64] = -1000.0
