@@ -5,16 +5,16 @@
 // three shuffles, the codes leave as one 128-bit store.  Each input element is
 // read once, quantised once, and written `copies` times.  Without the activation
 // memory bounds it; with it its instructions and the latency of the loads do
-// (64% of the issue slots, 51% of DRAM).  Blocks that stay and load their next
-// item ahead measured 32.3 against 33.4 us there and 4.4 against 3.9 us at 128
-// rows in 8 copies, and were not kept.
+// (16384 x 2048: 28.7 us, 5.9 TB/s; 29.5 without the bound on registers, 30.6 in
+// blocks of 256).  Blocks that stay and load their next item ahead gained 3%
+// there and lost 13% at 128 rows in 8 copies, and were not kept.
 #include "expert_internal.h"
 #include "expert_vec.cuh"
 
 namespace arf {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kElems = 16;      // per thread
 constexpr float kFp8Max = 448.0f;
 
@@ -72,7 +72,8 @@ __device__ __noinline__ float silu_mul(float g, float u)
 }
 
 template <class D, bool ACT>
-__global__ void __launch_bounds__(kThreads) block_quant_kernel(BlockQuantArgs a, int chunks)
+__global__ void __launch_bounds__(kThreads, D::bytes == 4 ? 10 : 12)
+    block_quant_kernel(BlockQuantArgs a, int chunks)
 {
     // one item = 8 threads = one block of 128 of one row; `chunks` blocks per row
     // (32 bits: 2^31 items would be 275 GB of codes)
