@@ -8,6 +8,7 @@ there is no fallback: if the library is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -107,7 +108,10 @@ class State(ctypes.Structure):
     ]
 
 
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
+
 _lib = None
+_native = None      # _marshal, once the library is loaded and if it was built
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 
@@ -176,7 +180,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "ar_fusion_matmul_status"):
         getattr(L, name).restype = _i
     _lib = L
+    _load_native(L)
     return L
+
+
+def _load_native(L: ctypes.CDLL) -> None:
+    """The expert-layer calls' marshalling in C++ (csrc/marshal.cpp).  The calls
+    work without it, through ctypes, some microseconds slower each."""
+    global _native
+    if not os.path.exists(MARSHAL_PATH):
+        return
+    spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+    try:
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+    except ImportError:         # built against another PyTorch
+        return
+    m.bind(*(ctypes.cast(getattr(L, f), _vp).value
+             for f in ("ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",
+                       "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8",
+                       "ar_fusion_combine")))
+    _native = m
 
 
 def lib() -> ctypes.CDLL:
@@ -462,6 +486,11 @@ def _operand(t: torch.Tensor, dtypes, shape, dev: int):
     raise _Refused
 
 
+def _handle(stream):
+    """None for the current stream, else the stream's address."""
+    return None if stream is None else _stream(stream)
+
+
 def _call(name: str, args) -> None:
     rc = getattr(_lib or load(), name)(*args)
     if rc:
@@ -518,6 +547,13 @@ def ar_fusion_route(logits: torch.Tensor, bias: torch.Tensor | None, ids_out: to
                     renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
     """logits [tokens, experts]; bias [experts] fp32 or None; ids_out (int32)
     and weights_out (fp32) [tokens, topk]."""
+    if _native is not None:
+        rc = _native.route(logits, bias, ids_out, weights_out, score, groups, groups_kept,
+                           group_score, renormalize, scale, _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if logits.dim() != 2 or ids_out.dim() != 2:
         _shapes(("logits", logits, 2), ("ids_out", ids_out, 2))
     tokens, experts = logits.shape
@@ -542,6 +578,13 @@ def ar_fusion_expert_plan(ids: torch.Tensor, experts: int, offsets_out: torch.Te
                           stream=None) -> None:
     """ids [tokens, topk] int32; offsets_out [experts + 1] and position_out
     [tokens, topk] int32, for the experts first_expert .. first_expert + experts - 1."""
+    if _native is not None:
+        rc = _native.expert_plan(ids, experts, offsets_out, position_out, first_expert,
+                                 _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if ids.dim() != 2:
         _shapes(("ids", ids, 2))
     slots = ids.shape
@@ -564,6 +607,13 @@ def ar_fusion_quant_blocks(x: torch.Tensor, quant_out: torch.Tensor, scale_out: 
     [out_rows, hidden] (uint8 or float8_e4m3fn); scale_out [out_rows,
     ceil(hidden / 128)] fp32; position [rows, copies] int32 or None; row_count: a
     one-element int32 tensor or None (a view of the plan's last offset)."""
+    if _native is not None:
+        rc = _native.quant_blocks(x, quant_out, scale_out, position, activation, row_count,
+                                  _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if x.dim() != 2 or quant_out.dim() != 2:
         _shapes(("x", x, 2), ("quant_out", quant_out, 2))
     rows = x.shape[0]
@@ -594,6 +644,12 @@ def ar_fusion_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor
                          b_scale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """a [rows, depth], b [cols, depth] (uint8 or float8_e4m3fn); a_scale [rows,
     ceil(depth / 128)], b_scale [ceil(cols / 128), ceil(depth / 128)] fp32; out [rows, cols]."""
+    if _native is not None:
+        rc = _native.matmul_fp8(a, a_scale, b, b_scale, out, _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if a.dim() != 2 or b.dim() != 2:
         _shapes(("a", a, 2), ("b", b, 2))
     rows, depth = a.shape
@@ -619,6 +675,13 @@ def ar_fusion_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch
                                 stream=None) -> None:
     """ar_fusion_matmul_fp8 by experts: b [experts, cols, depth], b_scale
     [experts, ceil(cols / 128), ceil(depth / 128)], offsets [experts + 1] int32."""
+    if _native is not None:
+        rc = _native.expert_matmul_fp8(a, a_scale, b, b_scale, offsets, out,
+                                       _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if a.dim() != 2 or b.dim() != 3:
         _shapes(("a", a, 2), ("b", b, 3))
     rows, depth = a.shape
@@ -655,6 +718,12 @@ def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: to
                       out: torch.Tensor, add: torch.Tensor | None = None, stream=None) -> None:
     """rows_in [in_rows, hidden]; position (int32) and weights (fp32) [tokens,
     topk]; out and add [tokens, hidden], of rows_in's type."""
+    if _native is not None:
+        rc = _native.combine(rows_in, position, weights, out, add, _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if rows_in.dim() != 2 or position.dim() != 2:
         _shapes(("rows_in", rows_in, 2), ("position", position, 2))
     in_rows, hidden = rows_in.shape

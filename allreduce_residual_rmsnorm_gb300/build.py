@@ -1,7 +1,8 @@
 """Build libarfusion.so in-tree with nvcc for sm_103a (no cmake).
 
 Each translation unit compiles in parallel; the shared library links the
-CUDA runtime dynamically so it shares one runtime with PyTorch.
+CUDA runtime dynamically so it shares one runtime with PyTorch.  Beside it
+``_marshal.so``, the binding's argument marshalling against PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libarfusion.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -44,8 +47,46 @@ def deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_marshal() -> None:
+    """marshal.cpp against the installed PyTorch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    include = os.path.join(root, "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", include,
+           "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(cuda_lib_dir()), "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        os.replace(tmp, MARSHAL)
+        return
+    # the binding works without it, through ctypes; an older one must not stay
+    if os.path.exists(MARSHAL):
+        os.remove(MARSHAL)
+    sys.stderr.write(f"marshal.cpp not built (calls go through ctypes):\n{r.stderr}")
+
+
+def fresh(path: str) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= deps_mtime()
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= deps_mtime():
+    if force or not fresh(MARSHAL):
+        with ThreadPoolExecutor(1) as ex:
+            marshal = ex.submit(build_marshal)
+            build_library(force, verbose, extra_flags)
+            marshal.result()
+        return LIB
+    return build_library(force, verbose, extra_flags)
+
+
+def build_library(force: bool, verbose: bool, extra_flags) -> str:
+    if not force and fresh(LIB):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nv = nvcc()

@@ -694,6 +694,48 @@ def test_layers_on_two_streams_at_once():
         layer.check()
 
 
+@pytest.mark.parametrize("native", [True, False])
+def test_marshalling_in_c_and_through_ctypes(native, monkeypatch):
+    """The same calls with the C++ marshalling and without it; optional operands,
+    another stream, and refusals that both answer alike."""
+    if native and B._native is None:
+        pytest.skip("marshal.cpp was not built")
+    if not native:
+        monkeypatch.setattr(B, "_native", None)
+    layer = Layer(33, 512, 256, 32, 6, 8, 16, seed=50)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    layer.run(stream=s)
+    s.synchronize()
+    layer.check()
+    layer.run()
+    torch.cuda.synchronize()
+    layer.check()
+    add = layer.x.clone()
+    B.ar_fusion_combine(layer.y, layer.pos, layer.w, layer.out, add=add)
+    want, mags = R.combine(layer.y, layer.pos, layer.w, add)
+    tol = 8 * U * mags + R.half_step(torch.bfloat16) * np.abs(want)
+    assert (np.abs(layer.out.double().cpu().numpy() - want) <= tol).all()
+    a, sa = layer.q.view(torch.float8_e4m3fn), layer.qs
+    out = torch.empty(a.shape[0], 512, dtype=torch.float16, device="cuda")
+    B.ar_fusion_matmul_fp8(a, sa, layer.w1[0], layer.s1[0], out, stream=s.cuda_stream)
+    s.synchronize()
+    with pytest.raises(ValueError, match="b: shape"):
+        B.ar_fusion_matmul_fp8(a, sa, layer.w1[0][:, :64], layer.s1[0], out)
+    with pytest.raises(TypeError, match="out"):
+        B.ar_fusion_matmul_fp8(a, sa, layer.w1[0], layer.s1[0], out.double())
+    with pytest.raises(TypeError, match="offsets"):
+        B.ar_fusion_expert_matmul_fp8(a, sa, layer.w1, layer.s1, layer.off.long(), layer.h)
+    with pytest.raises(ValueError, match="ids: 1 dimensions"):
+        B.ar_fusion_expert_plan(layer.ids.view(-1), 16, layer.off, layer.pos)
+    with pytest.raises(B.ArFusionError, match="groups"):
+        B.ar_fusion_route(layer.logits, layer.bias, layer.ids, layer.w, groups=5)
+    with pytest.raises(B.ArFusionError, match="score"):
+        B.ar_fusion_route(layer.logits, layer.bias, layer.ids, layer.w, score=7, scale=1)
+    with pytest.raises(ValueError, match="row_count"):
+        B.ar_fusion_quant_blocks(layer.x, layer.q[:33], layer.qs[:33], row_count=layer.off)
+
+
 def test_same_inputs_give_the_same_bits():
     a, b = (Layer(150, 512, 256, 32, 6, 0, 32, seed=40) for _ in range(2))
     a.run()
