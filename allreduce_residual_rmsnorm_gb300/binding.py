@@ -492,7 +492,11 @@ def _handle(stream):
 
 
 def _call(name: str, args) -> None:
-    rc = getattr(_lib or load(), name)(*args)
+    f = getattr(_lib or load(), name)
+    for a, kind in zip(args, f.argtypes):       # ctypes would drop the upper bits
+        if kind is _i and not -1 << 31 <= a < 1 << 31:
+            raise ValueError(f"{name}: {a} does not fit a 32-bit integer")
+    rc = f(*args)
     if rc:
         _check(rc)
 

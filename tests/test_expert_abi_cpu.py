@@ -167,6 +167,13 @@ def test_binding_refuses_types_shapes_and_host_tensors():
         B.ar_fusion_combine(z(4, 16), z(2, 2, dtype=i32), z(2, 2), z(2, 16), add=z(1, 16))
 
 
+def test_binding_refuses_numbers_past_32_bits(L):
+    """ctypes alone would pass the lower 32 bits."""
+    for first in (1 << 32, 1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="32-bit"):
+            B._call("ar_fusion_expert_plan", (4096, 1, 1, first, 8, 4096, 4096, None))
+
+
 # ------------------------------------------- the 64-bit reference itself
 
 def test_reference_decodes_e4m3_as_torch_does():
