@@ -1,8 +1,8 @@
 // Routing to experts: scores, groups, top-k and weights of one token row per
 // warp.  Expert e = lane + 32 i starts in register i of its lane; each lane
 // sorts its own, and a pick is the largest of the 32 heads.  Bounded by its
-// instructions, about 900 a row at 256 experts and 8 chosen (8192 rows: 9 MB,
-// 1.4 us of memory time).
+// instructions, 1570 a row with 256 sigmoid scores, a bias, 8 groups and 8 chosen
+// (8192 rows: 15.1 us; their 9 MB are 1.4 us of memory time).
 //
 // The order of the choice values c = s + bias is that of the real numbers.
 // Without a bias, or with the same one everywhere, it is the order of the

@@ -11,9 +11,15 @@
 // is added, times sa * sb, to fp32 registers: a thread has one column of the
 // output, the rows' scales come through shared memory, made ahead by two warps.
 //
-// Shared memory is sized so that at most two blocks share an SM, which keeps
-// their tensor memory (256 columns each at most) within the SM's 512: no block
-// of a cluster can wait for tensor memory that waits for its cluster.
+// Shared memory is sized so that at most two blocks share an SM (three where a
+// block has 64 columns of tensor memory), which keeps their tensor memory (256
+// columns each at most) within the SM's 512: no block of a cluster can wait for
+// tensor memory that waits for its cluster.
+//
+// Weights that one block alone reads leave L2 first (16 rows: 28672 x 7168 33.3 ->
+// 32.0 us, 131072 x 2048 48.5 -> 42.8); with several row tiles of an expert that
+// cost 1%, and where all of them may stay in L2 for a next call it cost 13% of
+// that (1 x 7168 x 2048, 14.7 MB), so there they are left alone.
 //
 // Warps 0-3: add and store; warp 4: copies; warp 5: products; warps 6, 7: scales.
 #include "matmul_internal.h"
@@ -53,7 +59,7 @@ template <class D, int TOK>
 __global__ void __launch_bounds__(kThreads)
     matmul_narrow_kernel(const __grid_constant__ CUtensorMap map_a,
                          const __grid_constant__ CUtensorMap map_b, MatmulArgs a, int* status,
-                         int split, int stages)
+                         int split, int stages, int large)
 {
     constexpr uint32_t kCols = TOK * kBufs;
     constexpr int kStage = kBytesW + TOK * kK;
@@ -121,6 +127,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t m0 = row0 + (int64_t)blockIdx.y * TOK; m0 < row1; m0 += step) {
         if (warp == 4) {
             const int brow = e * a.cols + n0;
+            const uint64_t policy = large && row1 - row0 <= TOK ? evict_first() : evict_normal();
             for (int kb = kb0; kb < kb1 && ok; ++kb) {
                 ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * s, ph ^ 1, bail, 1));
                 if (!ok)
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kThreads)
                 if (elect_one()) {
                     const uint32_t at = stage0 + s * kStage;
                     bar_expect(full + 8 * s, kStage);
-                    tma_load_2d(at, &map_b, full + 8 * s, kb * kK, brow);
+                    tma_load_2d(at, &map_b, full + 8 * s, kb * kK, brow, policy);
                     tma_load_2d(at + kBytesW, &map_a, full + 8 * s, kb * kK, (int)m0);
                 }
                 __syncwarp();
@@ -318,22 +325,31 @@ cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaSt
         !byte_tensor_map(&map_b, a.b, (uint64_t)a.experts * a.cols, (uint64_t)a.depth, kN))
         return cudaErrorInvalidValue;
     constexpr int kStage = kBytesW + TOK * kK;
-    const int budget = 106 * 1024;  // two blocks per SM
+    const int64_t per = ((int64_t)a.rows + a.experts - 1) / a.experts;
+    const int64_t y = (per + TOK - 1) / TOK;
+    const int64_t x = (int64_t)((a.cols + kN - 1) / kN) * split;
+    // Two blocks per SM; three of 16 rows (their registers allow it) where there
+    // are six or more to an SM, so that more of a block's start and end passes
+    // behind the others' copies: 64 experts x 4096 x 2048, 128 rows, 68.5 -> 65.3
+    // us, x 2048 x 512 16.3 -> 13.2.  With fewer it is the stages that count: 512
+    // blocks of 65536 x 2048 25.9 against 26.3 us.
+    constexpr int kMost = 106 * 1024, kThird = 73 * 1024;
+    const bool third = TOK == 16 && (a.experts < a.rows ? a.experts : a.rows) * x * y >= 6 * d.sms;
+    const int smem = third ? kThird : kMost;    // the whole of it: never another block
     const int sums = split > 1 ? TOK * kN * 4 : 0;
-    int stages = (budget - sums - 1024) / kStage;
+    int stages = (smem - sums - 1024) / kStage;
     stages = stages > kMaxStages ? kMaxStages : stages;
-    const int smem = budget;        // the whole of it: never three blocks per SM
     const auto kernel = matmul_narrow_kernel<D, TOK>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = once_per_device(done, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     });
     if (e != cudaSuccess)
         return e;
-    const int per = (a.rows + a.experts - 1) / a.experts;
-    const int y = (per + TOK - 1) / TOK;
+    // half of L2: beside what else a step touches, more would not stay
+    const int large = (uint64_t)a.experts * a.cols * a.depth > 64ull << 20;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.cols + kN - 1) / kN) * split, y > 65535 ? 65535 : y, a.experts);
+    cfg.gridDim = dim3((unsigned)x, (unsigned)(y > 65535 ? 65535 : y), a.experts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -345,7 +361,7 @@ cudaError_t launch_t(const MatmulArgs& a, int split, const DeviceInfo& d, cudaSt
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, d.status, split, stages);
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, d.status, split, stages, large);
 }
 
 template <class D>

@@ -488,6 +488,15 @@ def test_expert_matmul_first_offset_above_zero_and_clamped_offsets():
     check_experts(300, 136, 144, [-30, 200, 250, 2 ** 31 - 1], torch.float32, 3)
 
 
+def test_expert_matmul_of_many_experts_and_columns():
+    """Weights past half of L2 in more blocks than six per SM; experts of none,
+    one and several tiles of rows."""
+    loads = [0, 1, 3, 16, 17, 40] + [1, 0, 2] * 9
+    bounds = np.concatenate([[0], np.cumsum(loads)]).tolist()
+    check_experts(bounds[-1] + 2, 4104, 528, bounds, torch.float32, 77)
+    check_experts(5, 32776, 2064, [0, 5], torch.bfloat16, 78)
+
+
 # ------------------------------------------------------------------ combine
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
@@ -734,6 +743,18 @@ def test_marshalling_in_c_and_through_ctypes(native, monkeypatch):
         B.ar_fusion_route(layer.logits, layer.bias, layer.ids, layer.w, score=7, scale=1)
     with pytest.raises(ValueError, match="row_count"):
         B.ar_fusion_quant_blocks(layer.x, layer.q[:33], layer.qs[:33], row_count=layer.off)
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_numbers_past_32_bits_are_refused(native, monkeypatch):
+    B.load()
+    if not native:
+        monkeypatch.setattr(B, "_native", None)
+    layer = Layer(3, 128, 128, 32, 6, 8, 16, seed=51)
+    with pytest.raises(ValueError, match="32-bit"):
+        B.ar_fusion_expert_plan(layer.ids, 16, layer.off, layer.pos, first_expert=1 << 32)
+    with pytest.raises(ValueError, match="32-bit"):
+        B.ar_fusion_route(layer.logits, layer.bias, layer.ids, layer.w, groups=(1 << 32) + 1)
 
 
 def test_same_inputs_give_the_same_bits():
