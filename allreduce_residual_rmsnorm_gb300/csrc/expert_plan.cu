@@ -16,7 +16,8 @@ namespace {
 constexpr int kMaxWarps = 32;
 constexpr int kRounds = 8;      // of 32 slots, loaded together
 constexpr int kPerThread = 4;   // experts of a thread at most: blocks have 256 threads or more
-constexpr int kMaxBlocks = 8;   // of the cluster
+constexpr int kBlocks = 8;      // of the cluster, or as many as one may have
+constexpr int kMaxBlocks = 16;
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* local, unsigned rank)
 {
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bi
                 uint32_t c[kMaxBlocks];         // every block's at once
 #pragma unroll
                 for (unsigned b = 0; b < kMaxBlocks; ++b)
-                    c[b] = ld_dsmem_u32(&total[x], b);
+                    c[b] = b < blocks ? ld_dsmem_u32(&total[x], b) : 0u;
 #pragma unroll
                 for (unsigned b = 0; b < kMaxBlocks; ++b) {
                     before[q] += b < me ? c[b] : 0u;
@@ -192,16 +193,46 @@ __global__ void __launch_bounds__(32 * kMaxWarps) plan_kernel(PlanArgs a, int bi
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s)
 {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)(sizeof(uint32_t) * (kMaxWarps + 1) * AR_MAX_EXPERTS));
-    });
+    // devices where a cluster of 16 blocks fits
+    static std::atomic<uint64_t> done{0}, sixteen{0};
+    const int most = (int)(sizeof(uint32_t) * (kMaxWarps + 1) * AR_MAX_EXPERTS);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = once_per_device(done, [&] {
+            const cudaError_t es = cudaFuncSetAttribute(
+                plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            if (es != cudaSuccess || dev >= 64)
+                return es;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kMaxBlocks);
+            cfg.blockDim = dim3(32 * kMaxWarps);
+            cfg.dynamicSmemBytes = most;
+            cudaLaunchAttribute at;
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = kMaxBlocks;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            int fit = 0;
+            if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                     1) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&fit, plan_kernel, &cfg) == cudaSuccess && fit > 0)
+                sixteen.fetch_or(1ull << dev);
+            else
+                (void)cudaGetLastError();       // 8 blocks then
+            return cudaSuccess;
+        });
     if (e != cudaSuccess)
         return e;
-    // one block up to four rounds a warp; 8 warps at least, for the experts
+    // One block up to four rounds a warp, 8 up to six, then 16 (8 against 16, with
+    // the routing before: 32768 slots 17.1 / 17.4 us, 65536 25.3 / 24.8, 131072,
+    // where 8 would load their rounds twice, 48.0 / 38.6).  8 warps at least, for
+    // the experts.
     const int64_t rounds = ((int64_t)a.slots + 31) / 32;
-    const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : kMaxBlocks;
+    const bool many = rounds > 6 * kBlocks * kMaxWarps && dev < 64 &&
+                      (sixteen.load(std::memory_order_acquire) >> dev & 1u);
+    const unsigned blocks = rounds <= 4 * kMaxWarps ? 1 : many ? kMaxBlocks : kBlocks;
     const int warps = rounds <= 8 ? 8 : rounds <= 16 ? 16 : kMaxWarps;
     static_assert(8 * 32 * kPerThread >= AR_MAX_EXPERTS, "experts of a block of 8 warps");
     cudaLaunchConfig_t cfg = {};

@@ -223,6 +223,13 @@ def test_plan(T, k, E, first, lo, hi):
     assert np.array_equal(pos.cpu().numpy(), r_pos)
 
 
+@pytest.mark.parametrize("T,k,E", [(6144, 8, 256), (6145, 8, 256), (8193, 8, 256), (6700, 10, 1024),
+                                   (16384, 8, 33), (16385, 8, 256), (100003, 5, 1000)])
+def test_plan_of_many_slots(T, k, E):
+    """Around the sizes where the cluster grows and where slots are loaded twice."""
+    test_plan(T, k, E, 0, -1, E + 3)
+
+
 def test_plan_of_no_tokens_writes_zero_offsets():
     off = torch.full((9,), -5, dtype=torch.int32, device="cuda")
     none = torch.empty(0, 4, dtype=torch.int32, device="cuda")
