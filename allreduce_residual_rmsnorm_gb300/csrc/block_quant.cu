@@ -5,8 +5,8 @@
 // three shuffles, the codes leave as one 128-bit store.  Each input element is
 // read once, quantised once, and written `copies` times.  Without the activation
 // memory bounds it; with it its instructions and the latency of the loads do
-// (16384 x 2048: 28.7 us, 5.9 TB/s; 29.5 without the bound on registers, 30.6 in
-// blocks of 256).  Blocks that stay and load their next item ahead gained 3%
+// (16384 x 2048: 29.9 us, 5.65 TB/s; with log2 e in one part 29.0, then 29.8
+// without the bound on registers and 30.9 in blocks of 256).  Blocks that stay and load their next item ahead gained 3%
 // there and lost 13% at 128 rows in 8 copies, and were not kept.
 #include "expert_internal.h"
 #include "expert_vec.cuh"
@@ -33,29 +33,39 @@ __device__ __forceinline__ float max_abs3_nan(float a, float b, float c)
 }
 
 // Two of g / (1 + e^-g) * u for |g| < kPlainGate, where everything stays finite.
-// e^-g = 2^t, t = -g log2 e as a product and its rounding error, which moves the
-// power by a factor of 1 + error ln 2; then the quotient G / d with G = g / 4 and
-// d = (1 + e^-g) / 4 (a quarter, so that the reciprocal is not below the normal
-// range), by the approximate reciprocal (1 ulp) and one correction.  In packed
-// pairs: with expf and the divide instructions 32 a element, which bound the
-// kernel (38.5 us at 16384 x 2048).
+// e^-g = 2^t, t = -g log2 e: log2 e in two parts (Cody and Waite, Software Manual
+// for the Elementary Functions, 1980), the rounding error of the product with
+// the high part recovered by a fused multiply-add, so that t = -(minus_t - err)
+// with err below 2^-17.  e^-g is then p + p err ln 2 with p = 2^-minus_t.  One
+// part alone is off by 1.9e-8 |g| in t, 22 u at g = -87 (u = 2^-24).
+// The quotient is G / d with G = g / 4 and d = (1 + e^-g) / 4 (a quarter, so that
+// the reciprocal is not below the normal range), by the approximate reciprocal (1
+// ulp) and one correction.  d is added up from its smaller parts, without
+// rounding e^-g by itself.
+// Off by at most: ex2 2.45 u (measured over every argument), the sum d, the
+// quotient and the product with u one u each: 5.5 u.  In packed pairs: with expf
+// and the divide instructions 32 a element, which bound the kernel (38.5 us at
+// 16384 x 2048).
 constexpr float kPlainGate = 88.0f;
 
 __device__ __forceinline__ uint64_t silu_mul_pair(uint64_t g, uint64_t u)
 {
-    const float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
-    const uint64_t quarter = pair_of(0.25f, 0.25f);
+    const float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const uint64_t quarter = pair_of(0.25f, 0.25f), minus_quarter = pair_of(-0.25f, -0.25f);
     const uint64_t minus_t = mul_pair(g, pair_of(kLog2e, kLog2e));
-    // t's rounding error: g * -log2 e - t
-    const uint64_t err = fma3_pair(g, pair_of(-kLog2e, -kLog2e), minus_t);
+    // minus_t - g log2 e, exact but for the low part's own rounding
+    const uint64_t err = fma3_pair(g, pair_of(-kLog2eLow, -kLog2eLow),
+                                   fma3_pair(g, pair_of(-kLog2e, -kLog2e), minus_t));
     const float2 tf = unpack_pair(minus_t);
     float2 p, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(-tf.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(-tf.y));
     const uint64_t pp = pair_of(p.x, p.y);
-    const uint64_t e = fma3_pair(pp, mul_pair(err, pair_of(kLn2, kLn2)), pp);
     const uint64_t G = mul_pair(g, quarter);
-    const uint64_t minus_d = fma3_pair(e, pair_of(-0.25f, -0.25f), pair_of(-0.25f, -0.25f));
+    // -d = -p / 4 + (-1 / 4 - p err ln 2 / 4)
+    const uint64_t low = fma3_pair(pp, mul_pair(err, pair_of(-0.25f * kLn2, -0.25f * kLn2)),
+                                   minus_quarter);
+    const uint64_t minus_d = fma3_pair(pp, minus_quarter, low);
     const float2 df = unpack_pair(minus_d);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-df.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-df.y));
