@@ -29,6 +29,9 @@ int launched(cudaError_t e, const char* what)
     return AR_OK;
 }
 
+// longest row in blocks of AR_QUANT_BLOCK: the end of its last block fits 32 bits
+constexpr int kMaxLength = INT_MAX - (AR_QUANT_BLOCK - 1);
+
 bool aligned(const void* p, unsigned to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
 
 int bad_dtype(int dtype)
@@ -44,6 +47,8 @@ int check_matmul(const MatmulArgs& m, int dtype)
         return efail(AR_ERR_INVALID, "rows %d < 0 or cols %d < 1", m.rows, m.cols);
     if (m.depth < 16 || m.depth % 16 != 0)
         return efail(AR_ERR_INVALID, "depth %d is not a positive multiple of 16", m.depth);
+    if (m.depth > kMaxLength)
+        return efail(AR_ERR_UNSUPPORTED, "depth %d > %d", m.depth, kMaxLength);
     if (m.experts < 1)
         return efail(AR_ERR_INVALID, "experts %d < 1", m.experts);
     if (m.experts > AR_MAX_EXPERTS)
@@ -132,6 +137,8 @@ int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int 
         return efail(AR_ERR_INVALID, "rows %d or out_rows %d < 0", rows, out_rows);
     if (hidden < 16 || hidden % 16 != 0)
         return efail(AR_ERR_INVALID, "hidden %d is not a positive multiple of 16", hidden);
+    if (hidden > kMaxLength)
+        return efail(AR_ERR_UNSUPPORTED, "hidden %d > %d", hidden, kMaxLength);
     if (activation != AR_ACT_NONE && activation != AR_ACT_SILU_MUL)
         return efail(AR_ERR_INVALID, "activation %d unknown", activation);
     if (copies < 1 || (!position && copies != 1))

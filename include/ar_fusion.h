@@ -554,7 +554,8 @@ int ar_fusion_expert_plan(const int32_t* ids, int tokens, int topk, int first_ex
  *   quant_out  [out_rows][hidden] E4M3 bytes
  *   scale_out  [out_rows][ceil(hidden / 128)] fp32
  * Rows that nothing is written to are left as they were.
- * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, hidden within 128 of 2^31),
+ * AR_ERR_CUDA. */
 int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int activation,
                            const int32_t* position, int copies, const int32_t* row_count,
                            int out_rows, void* quant_out, float* scale_out, void* stream);
