@@ -35,31 +35,6 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices] = {};
 
-cudaError_t device_info(DeviceInfo* out)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lk(g_mu);
-    DeviceInfo& d = g_info[dev];
-    if (!d.status) {
-        int sms = 0;
-        void* p = nullptr;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaGetSymbolAddress(&p, g_status);
-        if (e != cudaSuccess)
-            return e;
-        d.sms = sms;
-        d.status = static_cast<int*>(p);
-    }
-    *out = d;
-    return cudaSuccess;
-}
-
 // Which kernel, by the time that each would take, in microseconds of this device.
 // Both advance in steps of 128 of the depth that are bound by latency where the
 // blocks fit the device once, and in waves where they do not:
@@ -101,6 +76,31 @@ Choice choose(const MatmulArgs& a, int sms)
 }
 
 }  // namespace
+
+cudaError_t device_info(DeviceInfo* out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceInfo& d = g_info[dev];
+    if (!d.status) {
+        int sms = 0;
+        void* p = nullptr;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaGetSymbolAddress(&p, g_status);
+        if (e != cudaSuccess)
+            return e;
+        d.sms = sms;
+        d.status = static_cast<int*>(p);
+    }
+    *out = d;
+    return cudaSuccess;
+}
 
 bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t depth,
                      uint32_t box_rows)

@@ -21,6 +21,8 @@ struct DeviceInfo {
     int sms;
     int* status;                // device status words of the products: code, detail
 };
+// Of the current device.
+cudaError_t device_info(DeviceInfo* out);
 
 // Tokens on the lanes of tensor memory, 256 x 256 outputs per pair of blocks: many rows.
 cudaError_t launch_matmul_wide(int dtype, const MatmulArgs& a, const DeviceInfo& d,

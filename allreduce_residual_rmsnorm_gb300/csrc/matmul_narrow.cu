@@ -293,11 +293,14 @@ __global__ void __launch_bounds__(kThreads)
             cluster_barrier();
         }
     }
-    if (warp == 5)
-        ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // Without a wait that gave up every product has been added, so no copy and no
+    // product is left.  With one, whichever warp's it was, both end here before
+    // the block does.
+    if (*static_cast<volatile int*>(&dead)) {
         if (warp == 4) {
-            // a block that gave up waits for its copies in flight
             for (uint32_t i = 0; i < (uint32_t)stages && i < issued; ++i) {
                 ph ^= s == 0;
                 s = s == 0 ? stages - 1 : s - 1;
@@ -310,9 +313,6 @@ __global__ void __launch_bounds__(kThreads)
             bar_drain(done, 0);
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (warp == 5)
         tmem_free(tmem, kCols);
 }

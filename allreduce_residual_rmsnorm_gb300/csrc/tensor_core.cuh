@@ -15,6 +15,16 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
 
 // ------------------------------------------------------------- mbarriers
 
+// Limit of a wait, tries between two looks at the time, and how a try waits
+// (try_wait: some time in hardware).  Constants: as a kernel argument the limit
+// cost the product for many rows 1 to 2%.  The tests also build the kernels with
+// waits that give up at once.
+#ifndef ARF_WAIT_NS
+#define ARF_WAIT_NS 2000000000ull
+#define ARF_WAIT_TRIES 16u
+#define ARF_WAIT_TRY "try_wait"
+#endif
+
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -36,7 +46,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier." ARF_WAIT_TRY ".parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -44,11 +54,9 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Every wait ends: after kWaitNs, or as soon as another wait of the block gave
+// Every wait ends: after ARF_WAIT_NS, or as soon as another wait of the block gave
 // up (its flag is set), it returns false, and the first one to give up records
 // AR_ERR_TIMEOUT and `where` in the device's status words.
-constexpr uint64_t kWaitNs = 2000000000ull;
-
 struct Bail {
     uint32_t dead;              // shared-memory address of the block's flag
     int* status;                // device status words: code, detail
@@ -60,7 +68,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Ba
         return true;
     uint64_t t0 = 0;
     for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
-        if (n & 15u)
+        if (n % ARF_WAIT_TRIES)
             continue;
         uint32_t dead;
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(dead) : "r"(b.dead) : "memory");
@@ -68,7 +76,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Ba
             return false;
         const uint64_t t = globaltimer_ns();
         t0 = t0 ? t0 : t;
-        if (t - t0 > kWaitNs) {
+        if (t - t0 > ARF_WAIT_NS) {
             asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(b.dead) : "memory");
             if (atomicCAS(b.status, 0, AR_ERR_TIMEOUT) == 0)
                 atomicExch(b.status + 1, where);
