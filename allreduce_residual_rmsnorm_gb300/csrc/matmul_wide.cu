@@ -106,6 +106,42 @@ __device__ __forceinline__ void store16(uint8_t* p, const uint32_t (&w)[16 * D::
     }
 }
 
+// Waits for what a pair that gave up has in flight; one warp of each block, none
+// of which issues anything any more.  The copies of both blocks arrive at the
+// first one's `full`: a stage is filled again only after the products of its last
+// fill, so the blocks differ by one fill of a stage at most, of which the first
+// block armed the barrier for both or not at all.  The commits arrive at the
+// barriers of both.
+__device__ __noinline__ void end_pair(uint32_t rank, uint32_t full, uint32_t empty, uint32_t tfull,
+                                      const uint32_t* issued, const uint32_t* committed)
+{
+    const auto fills = [](uint32_t n, uint32_t s) { return n > s ? (n - s - 1) / kStages + 1 : 0u; };
+    const uint32_t lane = threadIdx.x & 31;
+    if (rank == 0) {
+        const uint32_t other = ld_cluster_u32(smem_u32(issued), 1);
+        for (uint32_t s = 0; s < kStages; ++s) {
+            const uint32_t mine = fills(*issued, s), theirs = fills(other, s), n = max(mine, theirs);
+            if (lane == 0 && mine > theirs)
+                bar_forgo(full + 8 * s, kStage);
+            if (lane == 0 && mine < theirs)
+                bar_expect(full + 8 * s, kStage);
+            __syncwarp();
+            if (n > 0)
+                bar_drain(full + 8 * s, (n - 1) & 1);
+        }
+    }
+    const uint32_t c0 = ld_cluster_u32(smem_u32(committed), 0),
+                   c1 = ld_cluster_u32(smem_u32(committed + 1), 0);
+    for (uint32_t s = 0; s < kStages; ++s)
+        if (const uint32_t n = fills(c1, s))
+            bar_drain(empty + 8 * s, (n - 1) & 1);
+    for (uint32_t b = 0; b < 4; ++b) {
+        const uint32_t c = b & 1 ? c1 : c0;
+        if (const uint32_t n = (c + 1 - (b >> 1)) / 2)      // sums of even or odd steps
+            bar_drain(tfull + 8 * b, (n - 1) & 1);
+    }
+}
+
 template <class D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_wide_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -119,6 +155,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bars[2 * kStages + 13];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
+    // for the end of a pair that gave up: whether each block did, copies issued here,
+    // products of each half of the columns that the first block committed
+    __shared__ uint32_t gave_up_sh[2], issued_sh, committed_sh[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const uint32_t stage0 = (smem_u32(dyn) + 1023u) & ~1023u, out0 = stage0 + kStages * kStage;
@@ -128,6 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         dead = 0;
+        gave_up_sh[0] = gave_up_sh[1] = 0;
         for (int s = 0; s < kStages; ++s) {
             bar_init(full + 8 * s, 1);      // used in the first block: both blocks' copies
             bar_init(empty + 8 * s, 1);
@@ -231,18 +271,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // until every stage is free again: no copy and no arrival is on its way
             // when the block ends
-            for (uint32_t i = 0; i < kStages && i < issued; ++i) {
+            for (uint32_t i = 0; i < kStages && i < issued && ok; ++i) {
                 const uint32_t back = issued < kStages ? i : (s + i) % kStages;
                 const uint32_t par = issued < kStages ? 0u : ((s + i) >= kStages ? ph : ph ^ 1);
-                if (!ok || !__all_sync(0xffffffffu, bar_wait(empty + 8 * back, par, bail, 1))) {
-                    // gave up: the copies of both blocks arrive at the first one's barrier
-                    ok = false;
-                    if (rank == 0)
-                        bar_drain(full + 8 * back, par);
-                    else
-                        __nanosleep(100000);
-                }
+                ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * back, par, bail, 1));
             }
+            if (lane == 0)
+                issued_sh = issued;
         } else if (warp == 9) {
             if (rank == 0 && elect_one()) {
                 constexpr uint32_t idesc = fp8_idesc(kM, kN / 2);
@@ -251,15 +286,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t steps = t0 < tiles ? ((tiles - 1 - t0) / pairs + 1) * nkb : 0;
                 uint32_t s = 0, ph = 0;
                 bool ok = true;
+                committed_sh[0] = committed_sh[1] = steps;
                 for (uint32_t it = 0; it < steps; ++it) {
-                    if (!(ok = bar_wait(full + 8 * s, ph, bail, 3)))
+                    if (!(ok = bar_wait(full + 8 * s, ph, bail, 3))) {
+                        committed_sh[0] = committed_sh[1] = it;
                         break;
+                    }
                     const uint32_t at = (uint32_t)desc0 + s * (kStage >> 4);
 #pragma unroll
                     for (uint32_t h = 0; h < 2; ++h) {
                         const uint32_t b = 2 * (it & 1) + h;
-                        if (!(ok = bar_wait(tempty + 8 * b, (it >> 1 & 1) ^ 1, bail, 2)))
+                        if (!(ok = bar_wait(tempty + 8 * b, (it >> 1 & 1) ^ 1, bail, 2))) {
+                            committed_sh[0] = it + h;
+                            committed_sh[1] = it;
                             break;
+                        }
                         tc_fence_after();
                         mma4_fp8_pair(tmem + b * (kN / 2), at, at + (kBytes >> 4) + h * (kBytes >> 5),
                                       hi, idesc);
@@ -273,10 +314,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         s = 0;
                         ph ^= 1;
                     }
-                }
-                if (!ok) {
-                    mma_commit_pair(done);
-                    bar_drain(done, 0);
                 }
             }
             __syncwarp();
@@ -441,10 +478,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_store_wait_read<0>();
         __syncwarp();
     }
+    __syncthreads();            // every wait that gives up has set the flag
+    if (tid == 0 && dead) {
+        gave_up_sh[rank] = 1;
+        st_cluster_u32(smem_u32(&gave_up_sh[rank]), rank ^ 1, 1);
+    }
     __syncwarp();
     tc_fence_before();
     cluster_barrier();
     tc_fence_after();
+    // Without a wait that gave up every product has been added and every stage is
+    // free again: nothing is on its way.  With one, both blocks know it here, and
+    // stay until the last has arrived.
+    if (gave_up_sh[0] | gave_up_sh[1]) {
+        if (warp == 8)
+            end_pair(rank, full, empty, tfull, &issued_sh, committed_sh);
+        else if (warp == 9 && rank == 0) {
+            if (elect_one())
+                mma_commit_pair_here(done);
+            __syncwarp();
+            bar_drain(done, 0);
+        }
+        __syncwarp();
+        cluster_barrier();
+    }
     if (warp == 9)
         tmem_free_pair(tmem, kCols);
 }

@@ -41,6 +41,12 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
         "r"(bytes)
         : "memory");
 }
+// `bytes` that no copy will bring count as arrived
+__device__ __forceinline__ void bar_forgo(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -149,6 +155,16 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(addr, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t rank, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(addr, rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ void bar_arrive_remote(uint32_t cluster_bar)
 {
@@ -299,6 +315,13 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
         : "memory");
 }
 
+// The same of a pair's products, at a barrier of the issuing block alone.
+__device__ __forceinline__ void mma_commit_pair_here(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
 // The commit arrives at the same barrier of both blocks.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
 {

@@ -85,7 +85,8 @@ class Product:
 
 @pytest.mark.parametrize("tokens,split,dims,loads", [
     (16, 1, (40, 300, 2064), None), (16, 8, (40, 300, 2064), None), (64, 4, (150, 520, 4112), None),
-    (32, 2, (300, 260, 656), [0, 1, 130, 40, 120])])
+    (32, 2, (300, 260, 656), [0, 1, 130, 40, 120]), (0, 0, (700, 1032, 2064), None),
+    (0, 0, (900, 1028, 400), [300, 0, 2, 129, 460])])
 def test_products_whose_waits_give_up_at_once(hasty, forms, tokens, split, dims, loads):
     p = Product(*dims, torch.bfloat16, loads)
     gave_up = 0
