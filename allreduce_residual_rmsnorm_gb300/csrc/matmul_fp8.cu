@@ -35,46 +35,6 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices] = {};
 
-// Which kernel, by the time that each would take, in microseconds of this device.
-// Both advance in steps of 128 of the depth that are bound by latency where the
-// blocks fit the device once, and in waves where they do not:
-//   wide     a step of a pair of blocks 0.40, a wave 1 more; 256 x 256 outputs
-//   narrow   a step 0.22, 0.31 or 0.55 with 16, 32 or 64 rows, a wave (two blocks
-//            per SM) 1.3 more, the sum over a split 0.04 a row; 128 columns
-// Measured against the model (rows x cols x depth: narrow best / wide):
-//   16 x 7168 x 2048: 5.3 / 10.1     128 x 7168 x 2048: 8.7 / 10.8
-//   256 x 7168 x 2048: 13.2 / 11.0   256 x 4096 x 4096: 14.2 / 17.0
-//   512 x 2048 x 7168: 21.4 / 25.8   1003 x 2048 x 7168: 33.2 / 26.4
-// Loads of experts differ: they are taken to reach twice the mean (64 experts,
-// 2048 rows x 4096 x 2048: 99 / 131; 32 experts: 74 / 65).
-struct Choice {
-    int tokens, split;          // split 0: the wide kernel
-};
-Choice choose(const MatmulArgs& a, int sms)
-{
-    const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-    const int64_t active = a.experts < a.rows ? a.experts : a.rows;
-    const int64_t per = up(a.rows, a.experts) * (a.experts > 1 ? 2 : 1);
-    const int steps = quant_blocks(a.depth);
-    Choice best{0, 0};
-    float us = 4.5f - 1.0f + (float)up(active * up(per, 256) * up(a.cols, 256), sms / 2) *
-                                 (0.40f * steps + 1.0f);
-    const int tokens[3] = {16, 32, 64};
-    const float step[3] = {0.22f, 0.31f, 0.55f};
-    for (int i = 0; i < 3; ++i) {
-        for (int split = 1; split <= 8 && split <= steps; split *= 2) {
-            const int64_t blocks = active * up(per, tokens[i]) * up(a.cols, 128) * split;
-            const float t = 2.5f + (float)up(blocks, 2 * sms) * (1.3f + step[i] * up(steps, split)) +
-                            (split > 1 ? 0.04f * tokens[i] : 0.0f);
-            if (t < us) {
-                us = t;
-                best = Choice{tokens[i], split};
-            }
-        }
-    }
-    return best;
-}
-
 }  // namespace
 
 cudaError_t device_info(DeviceInfo* out)
@@ -135,13 +95,50 @@ bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Which kernel, by the time that each would take, in microseconds of this device.
+// Both advance in steps of 128 of the depth that are bound by latency where the
+// blocks fit the device once, and in waves where they do not:
+//   wide     a step of a pair of blocks 0.40, a wave 1 more; 256 x 256 outputs
+//   narrow   a step 0.22, 0.31 or 0.55 with 16, 32 or 64 rows, a wave (two blocks
+//            per SM) 1.3 more, the sum over a split 0.04 a row; 128 columns
+// Measured against the model (rows x cols x depth: narrow best / wide):
+//   16 x 7168 x 2048: 5.3 / 10.1     128 x 7168 x 2048: 8.7 / 10.8
+//   256 x 7168 x 2048: 13.2 / 11.0   256 x 4096 x 4096: 14.2 / 17.0
+//   512 x 2048 x 7168: 21.4 / 25.8   1003 x 2048 x 7168: 33.2 / 26.4
+// Loads of experts differ: they are taken to reach twice the mean (64 experts,
+// 2048 rows x 4096 x 2048: 99 / 131; 32 experts: 74 / 65).
+Choice choose_matmul(const MatmulArgs& a, int sms)
+{
+    const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    const int64_t active = a.experts < a.rows ? a.experts : a.rows;
+    const int64_t per = up(a.rows, a.experts) * (a.experts > 1 ? 2 : 1);
+    const int steps = quant_blocks(a.depth);
+    Choice best{0, 0};
+    float us = 4.5f - 1.0f + (float)up(active * up(per, 256) * up(a.cols, 256), sms / 2) *
+                                 (0.40f * steps + 1.0f);
+    const int tokens[3] = {16, 32, 64};
+    const float step[3] = {0.22f, 0.31f, 0.55f};
+    for (int i = 0; i < 3; ++i) {
+        for (int split = 1; split <= 8 && split <= steps; split *= 2) {
+            const int64_t blocks = active * up(per, tokens[i]) * up(a.cols, 128) * split;
+            const float t = 2.5f + (float)up(blocks, 2 * sms) * (1.3f + step[i] * up(steps, split)) +
+                            (split > 1 ? 0.04f * tokens[i] : 0.0f);
+            if (t < us) {
+                us = t;
+                best = Choice{tokens[i], split};
+            }
+        }
+    }
+    return best;
+}
+
 cudaError_t launch_matmul(int dtype, const MatmulArgs& a, cudaStream_t s)
 {
     DeviceInfo d;
     const cudaError_t e = device_info(&d);
     if (e != cudaSuccess)
         return e;
-    const Choice c = choose(a, d.sms);
+    const Choice c = choose_matmul(a, d.sms);
     return c.split ? launch_matmul_narrow(dtype, a, c.tokens, c.split, d, s)
                    : launch_matmul_wide(dtype, a, d, s);
 }

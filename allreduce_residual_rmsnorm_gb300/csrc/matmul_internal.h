@@ -24,6 +24,13 @@ struct DeviceInfo {
 // Of the current device.
 cudaError_t device_info(DeviceInfo* out);
 
+// The kernel of a call: the one for few rows with `tokens` (16, 32 or 64) of them at
+// a time and the depth split over `split` blocks, or, split 0, the one for many.
+struct Choice {
+    int tokens, split;
+};
+Choice choose_matmul(const MatmulArgs& a, int sms);
+
 // Tokens on the lanes of tensor memory, 256 x 256 outputs per pair of blocks: many rows.
 cudaError_t launch_matmul_wide(int dtype, const MatmulArgs& a, const DeviceInfo& d,
                                cudaStream_t s);

@@ -51,6 +51,15 @@ extern "C" int product_form(const void* a, const float* sa, const void* b, const
                   : launch_matmul_wide(dtype, m, d, s);
 }
 
+extern "C" void product_choice(int experts, int rows, int cols, int depth, int sms, int* tokens,
+                               int* split)
+{
+    const MatmulArgs m{nullptr, nullptr, nullptr, nullptr, nullptr, experts, rows, cols, depth, nullptr};
+    const Choice c = choose_matmul(m, sms);
+    *tokens = c.tokens;
+    *split = c.split;
+}
+
 extern "C" int lone_wait(int where, int* out)
 {
     DeviceInfo d;

@@ -30,6 +30,8 @@ def load(out_dir, wait_ns, alone=False):
     p, i = ctypes.c_void_p, ctypes.c_int
     L.product_form.argtypes = [p, p, p, p, p, i, i, i, i, i, p, i, i, p]
     L.lone_wait.argtypes = [i, p]
+    L.product_choice.argtypes = [i, i, i, i, i, ctypes.POINTER(i), ctypes.POINTER(i)]
+    L.product_choice.restype = None
     L.ar_fusion_matmul_status.argtypes = [p, ctypes.POINTER(i)]
     return L
 
@@ -38,3 +40,11 @@ def status(L):
     """(status, detail) of the kernels behind L, cleared by the query."""
     d = ctypes.c_int(-1)
     return L.ar_fusion_matmul_status(None, ctypes.byref(d)), d.value
+
+
+def choice(L, rows, cols, depth, experts=1, sms=152):
+    """(tokens, split) of the form that a call of these sizes takes; (0, 0) is the
+    kernel for many rows."""
+    t, s = ctypes.c_int(-1), ctypes.c_int(-1)
+    L.product_choice(experts, rows, cols, depth, sms, ctypes.byref(t), ctypes.byref(s))
+    return t.value, s.value
