@@ -13,6 +13,8 @@ import os
 
 import torch
 
+from .build import marshal_path
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libarfusion.so")
 
@@ -108,8 +110,6 @@ class State(ctypes.Structure):
     ]
 
 
-MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
-
 _lib = None
 _native = None      # _marshal, once the library is loaded and if it was built
 _vp = ctypes.c_void_p
@@ -188,13 +188,14 @@ def _load_native(L: ctypes.CDLL) -> None:
     """The expert-layer calls' marshalling in C++ (csrc/marshal.cpp).  The calls
     work without it, through ctypes, some microseconds slower each."""
     global _native
-    if not os.path.exists(MARSHAL_PATH):
+    path = marshal_path()
+    if not os.path.exists(path):
         return
-    spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+    spec = importlib.util.spec_from_file_location("_marshal", path)
     try:
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-    except ImportError:         # built against another PyTorch
+    except ImportError:
         return
     m.bind(*(ctypes.cast(getattr(L, f), _vp).value
              for f in ("ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",

@@ -2,7 +2,8 @@
 
 Each translation unit compiles in parallel; the shared library links the
 CUDA runtime dynamically so it shares one runtime with PyTorch.  Beside it
-``_marshal.so``, the binding's argument marshalling against PyTorch's headers.
+``_marshal.<PyTorch and Python>.so``, the binding's argument marshalling against
+PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -19,7 +20,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libarfusion.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -47,28 +47,49 @@ def deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
-def build_marshal() -> None:
-    """marshal.cpp against the installed PyTorch."""
+def marshal_path() -> str:
+    """Where the marshalling module for this PyTorch and this Python lies.  It reads
+    tensors through PyTorch's inlined code: one built for another version may load,
+    its symbols resolved, and read the wrong bytes, so its name says which it is for."""
+    import torch
+    tag = (f"{torch.__version__}-{(torch.version.git_version or 'none')[:12]}"
+           f"-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}-{sysconfig.get_config_var('SOABI')}")
+    return os.path.join(HERE, f"_marshal.{tag}.so")
+
+
+def marshal_command(out: str) -> list[str]:
     import torch
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     include = os.path.join(root, "include")
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-I", include,
-           "-I", os.path.join(include, "torch", "csrc", "api", "include"),
-           "-I", os.path.join(os.path.dirname(cuda_lib_dir()), "include"),
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
-           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode == 0:
-        os.replace(tmp, MARSHAL)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-I", include,
+            "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-I", os.path.join(os.path.dirname(cuda_lib_dir()), "include"),
+            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", out,
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            f"-Wl,-rpath,{lib}"]
+
+
+def build_marshal(path: str) -> None:
+    """marshal.cpp against the installed PyTorch.  The binding works without it,
+    through ctypes: a failure is told and noted beside `path`, and not tried again
+    until a source changes."""
+    tmp = path + f".tmp{os.getpid()}"
+    try:
+        r = subprocess.run(marshal_command(tmp), capture_output=True, text=True)
+        why = r.stderr if r.returncode else None
+    except OSError as e:                        # no compiler
+        why = str(e)
+    if why is None:
+        os.replace(tmp, path)
         return
-    # the binding works without it, through ctypes; an older one must not stay
-    if os.path.exists(MARSHAL):
-        os.remove(MARSHAL)
-    sys.stderr.write(f"marshal.cpp not built (calls go through ctypes):\n{r.stderr}")
+    if os.path.exists(path):                    # an older one must not stay
+        os.remove(path)
+    with open(path + ".failed", "w") as f:
+        f.write(why)
+    sys.stderr.write(f"marshal.cpp not built (calls go through ctypes):\n{why}\n")
 
 
 def fresh(path: str) -> bool:
@@ -76,9 +97,14 @@ def fresh(path: str) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if force or not fresh(MARSHAL):
+    try:
+        path = marshal_path()
+    except ImportError as e:                    # no PyTorch: the library alone
+        sys.stderr.write(f"marshal.cpp not built: {e}\n")
+        return build_library(force, verbose, extra_flags)
+    if force or not (fresh(path) or fresh(path + ".failed")):
         with ThreadPoolExecutor(1) as ex:
-            marshal = ex.submit(build_marshal)
+            marshal = ex.submit(build_marshal, path)
             build_library(force, verbose, extra_flags)
             marshal.result()
         return LIB
