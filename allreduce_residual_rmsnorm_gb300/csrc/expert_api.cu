@@ -145,7 +145,7 @@ int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int 
         return efail(AR_ERR_INVALID, "copies %d < 1, or not 1 without position", copies);
     if (!position && out_rows < rows)
         return efail(AR_ERR_INVALID, "out_rows %d < rows %d", out_rows, rows);
-    if (rows == 0)
+    if (rows == 0 || out_rows == 0)     // out_rows 0: every position lies outside
         return AR_OK;
     if (!aligned(in, 16) || !aligned(quant_out, 16))
         return efail(AR_ERR_INVALID, "in or quant_out NULL or not 16-byte aligned");

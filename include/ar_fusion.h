@@ -550,7 +550,8 @@ int ar_fusion_expert_plan(const int32_t* ids, int tokens, int topk, int first_ex
  *              j; entries outside 0..out_rows - 1 are skipped; no two may be equal
  *   row_count  NULL, or a device int32: rows t >= *row_count are not read
  *              (offsets_out + experts of the plan, where not every slot is local)
- *   out_rows   rows of the outputs; at least `rows` without position
+ *   out_rows   rows of the outputs; at least `rows` without position (rows or
+ *              out_rows 0: nothing launched)
  *   quant_out  [out_rows][hidden] E4M3 bytes
  *   scale_out  [out_rows][ceil(hidden / 128)] fp32
  * Rows that nothing is written to are left as they were.

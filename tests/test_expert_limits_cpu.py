@@ -32,6 +32,13 @@ def test_depth_and_hidden_near_2_to_31_are_refused(L, n):
                     "hidden")
 
 
+def test_rows_for_no_place_are_taken(L):
+    """out_rows 0: every position lies outside, and an empty tensor has no address."""
+    assert L.ar_fusion_quant_blocks(P, 4, 128, 0, 0, P, 2, None, 0, None, None, None) == B.AR_OK
+    rc = L.ar_fusion_quant_blocks(P, 4, 128, 0, 0, P, 2, None, 1, None, None, None)
+    assert rc == B.AR_ERR_INVALID and "quant_out" in B.ar_fusion_last_error()
+
+
 def test_no_rows_of_such_a_depth_either(L):
     unsupported(L.ar_fusion_matmul_fp8(P, P, P, P, 0, 1, 2 ** 31 - 16, 0, P, None), "depth")
     assert L.ar_fusion_matmul_fp8(P, P, P, P, 0, 1, 2 ** 31 - 128, 0, P, None) == B.AR_OK
