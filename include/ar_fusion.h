@@ -456,9 +456,10 @@ int ar_fusion_noalloc_status(void* stream, int* detail);
  * (ar_fusion_quant_blocks), multiplied with 8-bit weights
  * (ar_fusion_expert_matmul_fp8, or ar_fusion_matmul_fp8 where there are no
  * experts), and combined back into token rows (ar_fusion_combine), which are
- * a rank's partial of the next fused call.  A dense product writes a partial
- * straight into the workspace through ar_fusion_workspace_partial_ptr in
- * AR_MODE_BUFFER (its outputs may hold -0.0, which a Lamport slot may not).
+ * a rank's partial of the next fused call.  A dense product
+ * or the combination writes a partial straight into the workspace through
+ * ar_fusion_workspace_partial_ptr in AR_MODE_BUFFER (their outputs may hold -0.0,
+ * which a Lamport slot may not; ar_fusion_workspace_stage writes it as +0.0).
  *
  * All of them are asynchronous on `stream`, run on the current device, take
  * no workspace and keep nothing between calls, so calls on several streams
@@ -565,7 +566,8 @@ int ar_fusion_quant_blocks(const void* in, int rows, int hidden, int dtype, int 
  *   out[m][n] = sum_b a_scale[m][b] * b_scale[n / 128][b]
  *                 * sum_{k in block b} a[m][k] * b[n][k]
  * (block b: k from 128 b to 128 b + 127 or the end), sums in fp32, rounded to
- * the output type once.  Device-side waits are bounded (2 s each); one that
+ * the output type once.  The product of the two scales comes first and has to lie
+ * in the range of fp32 itself.  Device-side waits are bounded (2 s each); one that
  * gives up leaves the outputs undefined and is reported by
  * ar_fusion_matmul_status.
  *   a          [rows][depth] E4M3;  a_scale [rows][ceil(depth / 128)] fp32
