@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libarfusion.so")
 AR_DT_BF16 = 0
 AR_DT_FP16 = 1
 AR_DT_FP32 = 2
+AR_DT_E4M3 = 3
 # enum ar_pattern
 AR_RESIDUAL_OUT = 1
 AR_NORM_OUT = 2
@@ -70,6 +71,11 @@ AR_MAX_EXPERTS = 1024
 AR_MAX_TOPK = 32
 AR_MAX_GROUPS = 32
 AR_QUANT_BLOCK = 128
+AR_MAX_SEQUENCES = 4096
+AR_MAX_HEAD_GROUP = 128
+AR_MAX_HEAD_DIM = 128
+AR_MAX_AXES = 4
+AR_ATTENTION_WORKSPACE_BYTES = 32 << 20
 
 PATTERNS = {
     "res_norm": AR_RESIDUAL_OUT | AR_NORM_OUT,
@@ -108,6 +114,18 @@ class State(ctypes.Structure):
         ("comm_size", ctypes.c_uint64), ("clear_size", ctypes.c_uint64),
         ("status", ctypes.c_int32), ("detail", ctypes.c_int32), ("calls", ctypes.c_uint64),
     ]
+
+
+class _HeadRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f"{x}_{s}", ctypes.c_int64) for x in "kv" for s in ("page", "row", "head")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "pages", "page_size", "heads", "head_dim",
+                                      "sequences", "max_pages")] + [
+        ("scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -164,6 +182,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                               _vp]
     L.ar_fusion_combine.argtypes = [_vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]
     L.ar_fusion_matmul_status.argtypes = [_vp, ctypes.POINTER(_i)]
+    cache, rows = ctypes.POINTER(_KvCache), ctypes.POINTER(_HeadRows)
+    L.ar_fusion_rope_append.argtypes = [cache, rows, rows, rows, rows, _i, _i, _i, _vp, _vp, _vp, _i,
+                                        ctypes.POINTER(_i), _i, _i, _vp]
+    L.ar_fusion_decode_attention.argtypes = [cache, rows, rows, _vp, _i, _i, ctypes.c_float, _i, _i,
+                                             _vp, ctypes.c_size_t, _vp]
+    L.ar_fusion_prompt_attention.argtypes = [cache, rows, rows, _vp, _vp, _i, _i, _i, ctypes.c_float,
+                                             _i, _i, _vp, ctypes.c_size_t, _vp]
+    L.ar_fusion_attention_status.argtypes = [_vp, ctypes.POINTER(_i)]
     for name in ("ar_fusion_workspace_bytes", "ar_fusion_workspace_create",
                  "ar_fusion_workspace_destroy", "ar_fusion_workspace_info",
                  "ar_fusion_workspace_copy_state", "ar_fusion_workspace_status",
@@ -177,7 +203,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "ar_fusion_sum", "ar_fusion_run_noalloc", "ar_fusion_noalloc_status",
                  "ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",
                  "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8", "ar_fusion_combine",
-                 "ar_fusion_matmul_status"):
+                 "ar_fusion_matmul_status", "ar_fusion_rope_append",
+                 "ar_fusion_decode_attention", "ar_fusion_prompt_attention",
+                 "ar_fusion_attention_status"):
         getattr(L, name).restype = _i
     _lib = L
     _load_native(L)
@@ -746,3 +774,190 @@ def ar_fusion_combine(rows_in: torch.Tensor, position: torch.Tensor, weights: to
                  ("weights", weights, _F32, slots), ("out", out, same, shape),
                  ("add", add, same, shape))
     _call("ar_fusion_combine", args)
+
+
+# -------------------------------------------------------- attention layers
+
+_CACHE = {torch.bfloat16: AR_DT_BF16, torch.float16: AR_DT_FP16, torch.float8_e4m3fn: AR_DT_E4M3}
+_ROWS = (torch.bfloat16, torch.float16)
+
+
+def _fits(name: str, value: int) -> int:
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name}: {value} does not fit a 32-bit integer")
+    return value
+
+
+def _head_rows(name: str, t: torch.Tensor, rows: int, dtype, dim: int, heads: int | None = None):
+    """A [rows, heads, dim] tensor whose last dimension is contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: type {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or heads not in (None, t.shape[1]):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"({rows}, {'heads' if heads is None else heads}, {dim})")
+    _placed(name, t)
+    if dim > 1 and t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name}: expected a contiguous last dimension")
+    return _HeadRows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _placed(name: str, t: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, and the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _array(name: str, t: torch.Tensor, dtype, shape) -> int:
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: type {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _placed(name, t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, page_table, lengths, kv_scale) -> _KvCache:
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in _CACHE:
+            raise TypeError(f"{name}: unsupported type {t.dtype}")
+        if t.dim() != 4:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected 4")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache: type {v_cache.dtype}, expected {k_cache.dtype}")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache: shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: {page_table.dim()} dimensions, expected 2")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _placed(name, t)
+        if t.shape[3] > 1 and t.stride(3) != 1 and t.numel():
+            raise ValueError(f"{name}: expected a contiguous last dimension")
+    pages, page_size, heads, dim = (_fits("k_cache", n) for n in k_cache.shape)
+    S, most = (_fits("page_table", n) for n in page_table.shape)
+    return _KvCache(
+        k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3], *v_cache.stride()[:3],
+        _CACHE[k_cache.dtype], pages, page_size, heads, dim, S, most,
+        None if kv_scale is None else _array("kv_scale", kv_scale, torch.float32, (2,)),
+        _array("page_table", page_table, torch.int32, (S, most)),
+        _array("lengths", lengths, torch.int32, (S,)))
+
+
+def ar_fusion_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                          k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          page_table: torch.Tensor, lengths: torch.Tensor,
+                          inv_freq: torch.Tensor | None, q_out: torch.Tensor | None = None,
+                          starts: torch.Tensor | None = None,
+                          positions: torch.Tensor | None = None, sections=None,
+                          interleaved: bool = False, kv_scale: torch.Tensor | None = None,
+                          stream=None) -> None:
+    """Rotates q [tokens, q_heads, dim] into q_out (q itself if None) and k [tokens, heads, dim],
+    and writes k and v into the caches [pages, page_size, heads, dim] (bf16 / fp16 as the
+    rows, or float8_e4m3fn with kv_scale [2] fp32 or None).  Any strides with a
+    contiguous last dimension.  page_table [sequences, max_pages], lengths [sequences] (the
+    new tokens included), starts [sequences + 1] (None: a row for each sequence),
+    positions [tokens] or [axes, tokens] (None: the index in the sequence) int32; inv_freq
+    [rot / 2] fp32 (None: no rotation); sections: pairs of each axis."""
+    if k.dim() != 3:
+        raise ValueError(f"k: {k.dim()} dimensions, expected 3")
+    if k.dtype not in _ROWS:
+        raise TypeError(f"k: unsupported type {k.dtype}")
+    cache = _kv_cache(k_cache, v_cache, page_table, lengths, kv_scale)
+    tokens, dt, dim, heads = _fits("k", k.shape[0]), k.dtype, cache.head_dim, cache.heads
+    if cache.dtype != AR_DT_E4M3 and k_cache.dtype != dt:
+        raise TypeError(f"k_cache: type {k_cache.dtype}, expected {dt} or {torch.float8_e4m3fn}")
+    kr, vr = _head_rows("k", k, tokens, dt, dim, heads), _head_rows("v", v, tokens, dt, dim, heads)
+    qr = qo = None
+    q_heads = 0
+    if q is not None:
+        qr = _head_rows("q", q, tokens, dt, dim)
+        q_heads = _fits("q", q.shape[1])
+        qo = qr if q_out is None else _head_rows("q_out", q_out, tokens, dt, dim, q_heads)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0 if inv_freq is None else _fits("inv_freq", 2 * inv_freq.numel())
+    axes = 1 if sections is None else len(sections)
+    shape = (axes, tokens) if positions is not None and positions.dim() == 2 else (tokens,)
+    if sections is not None and axes > 1:
+        shape = (axes, tokens)
+    table = None if sections is None else (_i * max(axes, 1))(*(_fits("sections", n) for n in sections))
+    rc = lib().ar_fusion_rope_append(
+        ctypes.byref(cache), None if qr is None else ctypes.byref(qr),
+        None if qo is None else ctypes.byref(qo), ctypes.byref(kr), ctypes.byref(vr), tokens,
+        q_heads, _ELEM[dt],
+        None if starts is None else _array("starts", starts, torch.int32, (cache.sequences + 1,)),
+        None if positions is None else _array("positions", positions, torch.int32, shape),
+        None if inv_freq is None else _array("inv_freq", inv_freq, torch.float32, (rot // 2,)),
+        rot, table, axes, 1 if interleaved else 0, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def _attention(name, q, k_cache, v_cache, page_table, lengths, out, workspace, scale, window,
+               sinks, lse, kv_scale, starts, stream):
+    if q.dim() != 3:
+        raise ValueError(f"q: {q.dim()} dimensions, expected 3")
+    if q.dtype not in _ROWS:
+        raise TypeError(f"q: unsupported type {q.dtype}")
+    cache = _kv_cache(k_cache, v_cache, page_table, lengths, kv_scale)
+    tokens, q_heads = (_fits("q", n) for n in q.shape[:2])
+    if cache.dtype != AR_DT_E4M3 and k_cache.dtype != q.dtype:
+        raise TypeError(f"k_cache: type {k_cache.dtype}, expected {q.dtype} or {torch.float8_e4m3fn}")
+    if name == "ar_fusion_decode_attention" and tokens != cache.sequences:
+        raise ValueError(f"q: {tokens} rows for {cache.sequences} sequences")
+    qr = _head_rows("q", q, tokens, q.dtype, cache.head_dim)
+    to = _head_rows("out", out, tokens, q.dtype, cache.head_dim, q_heads)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    work, size = None, 0
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+        work = _array("workspace", workspace, workspace.dtype, workspace.shape)
+    args = [ctypes.byref(cache), ctypes.byref(qr), ctypes.byref(to),
+            None if lse is None else _array("lse", lse, torch.float32, (tokens, q_heads))]
+    if name == "ar_fusion_prompt_attention":
+        args += [_array("starts", starts, torch.int32, (cache.sequences + 1,)), tokens]
+    args += [q_heads, _ELEM[q.dtype], scale, _fits("window", window), _fits("sinks", sinks), work,
+             size, _stream(stream)]
+    rc = getattr(lib(), name)(*args)
+    if rc:
+        _check(rc)
+
+
+def ar_fusion_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               page_table: torch.Tensor, lengths: torch.Tensor,
+                               out: torch.Tensor, workspace: torch.Tensor | None = None,
+                               scale: float | None = None, window: int = 0, sinks: int = 0,
+                               lse: torch.Tensor | None = None,
+                               kv_scale: torch.Tensor | None = None, stream=None) -> None:
+    """One new token per sequence: q and out [sequences, q_heads, dim], lse [sequences, q_heads]
+    fp32; caches and sequences as ar_fusion_rope_append takes them.  scale None:
+    1 / sqrt(dim).  workspace: AR_ATTENTION_WORKSPACE_BYTES of one call at a time (None: a
+    sequence's keys are not split over the GPU)."""
+    _attention("ar_fusion_decode_attention", q, k_cache, v_cache, page_table, lengths, out,
+               workspace, scale, window, sinks, lse, kv_scale, None, stream)
+
+
+def ar_fusion_prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               page_table: torch.Tensor, lengths: torch.Tensor,
+                               starts: torch.Tensor, out: torch.Tensor,
+                               workspace: torch.Tensor | None = None,
+                               scale: float | None = None, window: int = 0, sinks: int = 0,
+                               lse: torch.Tensor | None = None,
+                               kv_scale: torch.Tensor | None = None, stream=None) -> None:
+    """Any number of new tokens per sequence: q and out [tokens, q_heads, dim], lse [tokens,
+    q_heads] fp32, starts [sequences + 1] int32; the rest as ar_fusion_decode_attention."""
+    _attention("ar_fusion_prompt_attention", q, k_cache, v_cache, page_table, lengths, out,
+               workspace, scale, window, sinks, lse, kv_scale, starts, stream)
+
+
+def ar_fusion_attention_status(stream=None):
+    """ar_fusion_matmul_status of ar_fusion_prompt_attention."""
+    d = ctypes.c_int(-1)
+    rc = lib().ar_fusion_attention_status(_stream(stream), ctypes.byref(d))
+    if rc not in (AR_OK, AR_ERR_TIMEOUT):
+        _check(rc)
+    return rc, d.value

@@ -1,0 +1,227 @@
+// Rotation of the new queries and keys by position, and the keys and values into
+// the paged cache.
+//
+// A block has one row (token).  Its pairs' cosines and sines are computed once, in
+// shared memory, and serve all of its heads; a thread turns 16 elements at a time,
+// so that both halves of 8 pairs are in its registers.  Every element is read once
+// and written once.  The row's place (its sequence, length and page) is a chain of
+// three loads, and the elements do not wait for it: the first kAhead pieces of
+// every thread are loaded before it.
+#include "ar_internal.h"
+#include "attention_internal.h"
+#include "expert_vec.cuh"
+
+namespace arf {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAhead = 3;       // pieces of 16 elements in flight per thread
+
+// position * f / pi modulo 2, with f / pi = hi + lo: the product's high part loses
+// whole turns exactly (the remainder of two floats by a power of two is exact), its
+// rounding error comes back from the fused multiply-add.  |p| < 2^24: exact as a float.
+__device__ __forceinline__ float half_turns(float p, float hi, float lo)
+{
+    const float u = p * hi;
+    const float err = fmaf(p, hi, -u);
+    return (u - 2.0f * rintf(0.5f * u)) + fmaf(p, lo, err);
+}
+
+// cos and sin of position * f.  1 / pi in two floats; positions in two parts below
+// 2^24.  Off by a few 2^-24 at any position, where the product in 32 bits is off by
+// position * 2^-24.
+__device__ __forceinline__ float2 turn(int position, float f)
+{
+    const float kInvPi = 0.318309873f, kInvPiLow = 1.28412765e-8f;
+    const float hi = f * kInvPi;
+    const float lo = fmaf(f, kInvPi, -hi) + f * kInvPiLow;
+    const int low = position & 0xfff;
+    float t = half_turns((float)low, hi, lo);
+    if (position != low)
+        t += half_turns((float)(position >> 12), 4096.0f * hi, 4096.0f * lo);
+    float2 r;
+    sincospif(t, &r.y, &r.x);
+    return r;
+}
+
+struct Piece {
+    const uint8_t* from;        // NULL: none
+    int kind, head, first, second;      // kind 0: q, 1: k, 2: v; vectors of 8, second -1: none
+    int pair;                   // first pair of the half form, -1: neighbours or a copy
+};
+
+template <class D, bool F8>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a)
+{
+    __shared__ float2 cs[AR_MAX_HEAD_DIM / 2];
+    const int row = blockIdx.x, tid = threadIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    // pieces of a rotated head (the pairs of the half form, then the rest) and of a copied one
+    const int half = a.interleaved ? 0 : a.rot / 16;
+    const int rest = half * 2;
+    const unsigned vecs = a.c.D / 8, per = half + (vecs - rest + 1) / 2, per_v = (vecs + 1) / 2;
+    const unsigned turned = (a.Hq + a.c.heads) * per, total = turned + a.c.heads * per_v;
+
+    const auto piece = [&](unsigned i) {
+        Piece p;
+        p.pair = -1;
+        unsigned in;
+        if (i < turned) {
+            const unsigned h = i / per;
+            in = i - h * per;
+            p.kind = h < (unsigned)a.Hq ? 0 : 1;
+            p.head = p.kind ? h - a.Hq : h;
+            if (in < (unsigned)half) {
+                p.pair = 8 * in;
+                p.first = in;
+                p.second = in + half;
+            } else {
+                p.first = rest + 2 * (in - half);
+            }
+        } else {
+            const unsigned h = (i - turned) / per_v;
+            in = i - turned - h * per_v;
+            p.kind = 2;
+            p.head = h;
+            p.first = 2 * in;
+        }
+        if (p.pair < 0)
+            p.second = p.first + 1 < (int)vecs ? p.first + 1 : -1;
+        const Rows& r = p.kind == 0 ? a.q : p.kind == 1 ? a.k : a.v;
+        p.from = i < total ? r.p + row * r.row + p.head * r.head : nullptr;
+        return p;
+    };
+
+    // which sequence: the number of starts at or before the row
+    int seq = row, before = 0;
+    uint4 x[kAhead][2];
+    if (a.starts) {
+        for (int s0 = 0; s0 <= a.c.S; s0 += kThreads)
+            before += s0 + tid <= a.c.S && a.starts[s0 + tid] <= row;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const Piece p = piece(tid + j * kThreads);
+        if (p.from) {
+            x[j][0] = ld_stream(p.from + 16 * p.first);
+            if (p.second >= 0)
+                x[j][1] = ld_stream(p.from + 16 * p.second);
+        }
+    }
+    int end = row + 1;
+    if (a.starts) {
+        __shared__ int count[kThreads / 32];
+        before = __reduce_add_sync(0xffffffffu, before);
+        if ((tid & 31) == 0)
+            count[tid >> 5] = before;
+        __syncthreads();
+        seq = -1;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w)
+            seq += count[w];
+        if (seq < 0 || seq >= a.c.S)
+            return;
+        end = a.starts[seq + 1];
+        if (a.starts[seq] < 0 || row >= end || end > a.T)
+            return;
+    }
+    const int index = clamp_length(a.c, a.c.lengths[seq]) - (end - row);
+    int page = -1;
+    if (index >= 0)
+        page = a.c.table[(int64_t)seq * a.c.max_pages + (index >> a.c.page_shift)];
+    const bool placed = page >= 0 && page < a.c.pages;
+    const int in_page = index & ((1 << a.c.page_shift) - 1);
+    if (tid < a.rot / 2) {
+        int axis = 0;
+        while (tid >= a.ends[axis])     // ends[axes - 1] is rot / 2
+            ++axis;
+        const int at = a.positions ? a.positions[(int64_t)axis * a.T + row] : index;
+        cs[tid] = turn(at, a.inv_freq[tid]);
+    }
+    float inverse[2] = {1.0f, 1.0f};
+    if (F8 && a.c.scale) {
+        inverse[0] = 1.0f / a.c.scale[0];
+        inverse[1] = 1.0f / a.c.scale[1];
+    }
+    __syncthreads();
+
+    const auto finish = [&](const Piece& p, const uint4& x0, const uint4& x1) {
+        if (p.kind && !placed)
+            return;
+        float f[2][8];
+        unpack8<D>(x0, f[0]);
+        if (p.second >= 0)
+            unpack8<D>(x1, f[1]);
+        if (p.pair >= 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 c = cs[p.pair + e];
+                const float u = f[0][e], w = f[1][e];
+                f[0][e] = fmaf(u, c.x, -(w * c.y));
+                f[1][e] = fmaf(w, c.x, u * c.y);
+            }
+        } else if (a.interleaved && p.kind < 2) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int first = (p.first + v) * 8;
+                if (first < a.rot) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 c = cs[first / 2 + e];
+                        const float u = f[v][2 * e], w = f[v][2 * e + 1];
+                        f[v][2 * e] = fmaf(u, c.x, -(w * c.y));
+                        f[v][2 * e + 1] = fmaf(w, c.x, u * c.y);
+                    }
+                }
+            }
+        }
+        uint8_t* to;
+        if (p.kind == 0)
+            to = a.q_out.p + row * a.q_out.row + p.head * a.q_out.head;
+        else if (p.kind == 1)
+            to = a.c.k + page * a.c.k_page + in_page * a.c.k_row + p.head * a.c.k_head;
+        else
+            to = a.c.v + page * a.c.v_page + in_page * a.c.v_row + p.head * a.c.v_head;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const int at = v ? p.second : p.first;
+            if (at < 0)
+                continue;
+            if (F8 && p.kind) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[v][e] *= inverse[p.kind - 1];
+                *reinterpret_cast<uint2*>(to + 8 * at) = e4m3x8(f[v]);
+            } else {
+                *reinterpret_cast<uint4*>(to + 16 * at) = pack8<D>(f[v]);
+            }
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const Piece p = piece(tid + j * kThreads);
+        if (p.from)
+            finish(p, x[j][0], x[j][1]);
+    }
+    for (unsigned i = tid + kAhead * kThreads; i < total; i += kThreads) {
+        const Piece p = piece(i);
+        uint4 x0 = ld_stream(p.from + 16 * p.first), x1 = x0;
+        if (p.second >= 0)
+            x1 = ld_stream(p.from + 16 * p.second);
+        finish(p, x0, x1);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(int dtype, bool e4m3, const RopeArgs& a, cudaStream_t s)
+{
+    if (dtype == AR_DT_BF16)
+        return e4m3 ? launch_after(rope_append_kernel<Bf16, true>, a.T, kThreads, 0, s, a)
+                    : launch_after(rope_append_kernel<Bf16, false>, a.T, kThreads, 0, s, a);
+    return e4m3 ? launch_after(rope_append_kernel<Fp16, true>, a.T, kThreads, 0, s, a)
+                : launch_after(rope_append_kernel<Fp16, false>, a.T, kThreads, 0, s, a);
+}
+
+}  // namespace arf

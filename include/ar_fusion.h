@@ -74,7 +74,8 @@ extern "C" {
 enum ar_dtype {
     AR_DT_BF16 = 0,
     AR_DT_FP16 = 1,
-    AR_DT_FP32 = 2
+    AR_DT_FP32 = 2,
+    AR_DT_E4M3 = 3            /* of caches of keys and values only (ar_kv_cache) */
 };
 
 /* Output pattern bits.  Valid patterns are the four of allreduce_fusion_op
@@ -613,6 +614,160 @@ int ar_fusion_matmul_status(void* stream, int* detail);
 int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
                       const float* weights, int tokens, int topk, int hidden, int dtype,
                       const void* add, void* out, void* stream);
+
+/* ------------------------------------------------ attention layers -- */
+
+/* The work between two fused epilogues of an attention layer (no counterpart on
+ * the pages either): the normed rows are quantised and multiplied with the
+ * projection's weights (ar_fusion_quant_blocks, ar_fusion_matmul_fp8), queries and
+ * keys are rotated by their positions and keys and values appended to a paged
+ * cache (ar_fusion_rope_append), the new tokens attend to what their sequences
+ * hold there (ar_fusion_decode_attention where each sequence has one new token,
+ * ar_fusion_prompt_attention for any number), and the next projection makes a
+ * rank's partial of the next fused call.
+ *
+ * All of them are asynchronous on `stream`, run on the current device and keep
+ * nothing between calls.  The two attention calls use a workspace of the caller:
+ * its contents mean nothing before or after a call, so calls that follow one
+ * another (on one stream, or ordered by events; captured or not) share one,
+ * and calls that may run at the same time each need their own.  Outputs must not
+ * overlap inputs, but for q_out of ar_fusion_rope_append, which may be q itself.
+ *
+ * Sequences.  `sequences` of them, with lengths[b] tokens each, the new ones
+ * included.  The new tokens of sequence b are rows starts[b] .. starts[b + 1] - 1
+ * of the call's row arrays (where there is no `starts`: row b alone), and row
+ * starts[b] + j is the token of index lengths[b] - n + j of its sequence, n the
+ * number of its rows.  A row whose index is negative (more rows than lengths[b])
+ * has no place in the cache and sees no key.  Rows outside starts[0] ..
+ * starts[sequences] - 1 are not read and what belongs to them is left as it was.
+ * starts may not decrease nor leave 0 .. tokens: where it does, rows are left as
+ * they were, nothing else is touched.
+ *
+ * Pages.  The token of index i of sequence b lies in page
+ * page_table[b][i / page_size], row i % page_size.  Entries behind a sequence's
+ * last token are not used.  An entry outside 0 .. pages - 1 is of no page:
+ * nothing is written there, and its keys and values read as zeros.  lengths[b]
+ * is taken as at most max_pages * page_size, and as 0 where it is negative.
+ * Two sequences may share pages that they read.  Two new tokens must not have
+ * the same place. */
+
+/* Sequences of one call, and query heads that share a key's head. */
+#define AR_MAX_SEQUENCES 4096
+#define AR_MAX_HEAD_GROUP 128
+/* Elements of a head; axes of a position. */
+#define AR_MAX_HEAD_DIM 128
+#define AR_MAX_AXES 4
+/* Bytes of workspace with which the attention calls split as far as they can. */
+#define AR_ATTENTION_WORKSPACE_BYTES (32 << 20)
+
+/* Rows of heads: element d of head h of row t is data[t * row + h * head + d].
+ * The strides are in elements, of either sign or order, and 16-byte multiples; data
+ * is 16-byte aligned (a slice of a projection's output [tokens][all heads][dim]
+ * is as good as an array of its own).  A stride along an extent of one is not
+ * looked at. */
+typedef struct ar_head_rows {
+    void* data;
+    int64_t row, head;
+} ar_head_rows;
+
+/* A paged cache of keys and values, and the sequences in it.
+ *   k, v         element d of head h of row r of page p at p * page + r * row +
+ *                h * head + d (strides in elements, positive 16-byte multiples below
+ *                2^40 bytes; data 16-byte aligned; page, row and head may stand in
+ *                any order: [pages][rows][heads][dim] or [pages][heads][rows][dim])
+ *   dtype        AR_DT_BF16 or AR_DT_FP16 (that of the call's rows), or AR_DT_E4M3
+ *   pages        >= 1;  page_size a power of two, 8 .. 65536
+ *   heads        >= 1;  head_dim a multiple of 8 (E4M3: 16), 8 .. AR_MAX_HEAD_DIM
+ *   scale        device fp32 [2]: a key is its code times scale[0], a value its code times
+ *                scale[1].  NULL: 1.  With AR_DT_E4M3 only
+ *   page_table   device int32 [sequences][max_pages]
+ *   lengths      device int32 [sequences]
+ *   sequences    0 .. AR_MAX_SEQUENCES (0: nothing launched);  max_pages >= 1,
+ *                max_pages * page_size < 2^31 */
+typedef struct ar_kv_cache {
+    void *k, *v;
+    int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+    int32_t dtype, pages, page_size, heads, head_dim;
+    int32_t sequences, max_pages;
+    const float* scale;
+    const int32_t* page_table;
+    const int32_t* lengths;
+} ar_kv_cache;
+
+/* Rotation by position of the new rows' queries and keys, and the keys and values
+ * into the cache.  With f_m = inv_freq[m] (fp32, as given) and p the row's position
+ * on the axis of pair m, the angle is a = p * f_m (taken modulo 2 pi before any
+ * rounding to 32 bits), and for the pairs m < rot / 2 of every head
+ *   (x0, x1) -> (x0 cos a - x1 sin a, x1 cos a + x0 sin a)
+ * where x0, x1 are elements m and m + rot / 2, or 2m and 2m + 1 if `interleaved`;
+ * the head's elements from rot on stay as they are.  In fp32, rounded to the
+ * element type once (to E4M3: the fp32 value times 1 / scale, nearest even,
+ * saturating).
+ *   q, q_out   [tokens][q_heads], of `dtype`; q NULL: keys and values alone
+ *   k, v       [tokens][cache->heads]
+ *   dtype      AR_DT_BF16 or AR_DT_FP16
+ *   starts     device int32 [sequences + 1], or NULL: tokens == sequences, a row each
+ *   positions  device int32 [axes][tokens], or NULL: the token's index in its
+ *              sequence on every axis
+ *   inv_freq   device fp32 [rot / 2];  rot a multiple of 16, 0 .. head_dim (0: no
+ *              rotation, inv_freq is not read)
+ *   sections   host int [axes]: pairs of each axis, in order, rot / 2 in all
+ *              (NULL with axes 1);  axes 1 .. AR_MAX_AXES
+ *   interleaved  0 or 1
+ * A row without a place in the cache still gets its q_out.
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */
+int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,
+                          const ar_head_rows* q_out, const ar_head_rows* k,
+                          const ar_head_rows* v, int tokens, int q_heads, int dtype,
+                          const int32_t* starts, const int32_t* positions,
+                          const float* inv_freq, int rot, const int* sections, int axes,
+                          int interleaved, void* stream);
+
+/* Attention of one new token per sequence (row b is the last token of sequence b)
+ * over the cache.  Query head h reads the keys and values of head
+ * h / (q_heads / heads).  With i the token's index, it sees the keys j <= i, of which
+ * with window > 0 only those with j > i - window or j < sinks:
+ *   s_j = scale * q . k_j,  out = sum_j e^{s_j} v_j / sum_j e^{s_j},
+ *   lse = log sum_j e^{s_j}
+ * in fp32 (the products of the matrix instructions; e^{s_j - max} is rounded to the
+ * 16-bit type of the values' product), rounded to the element type once.  A token that
+ * sees nothing gets zeros and -inf.  What keys and values hold that no token of the
+ * call sees, NaN and infinities among it, changes nothing.
+ *   q, out     [sequences][q_heads] of `dtype` (AR_DT_BF16 or AR_DT_FP16)
+ *   lse        device fp32 [sequences][q_heads] or NULL
+ *   q_heads    a multiple of cache->heads, at most AR_MAX_HEAD_GROUP times it
+ *   scale      positive and finite
+ *   window     0 (all keys) or the number of last keys, the token's own among them;
+ *              sinks >= 0: first keys that stay visible (0 without a window)
+ *   workspace  device memory, 16-byte aligned, written by this call alone while it
+ *              runs; the long axis is split as far as workspace_bytes allow (NULL with
+ *              0: not at all; AR_ATTENTION_WORKSPACE_BYTES are always enough)
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */
+int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
+                               const ar_head_rows* out, float* lse, int q_heads, int dtype,
+                               float scale, int window, int sinks, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The same of any number of new tokens per sequence, each seeing the keys up to its
+ * own index.
+ *   q, out     [tokens][q_heads];  lse [tokens][q_heads] or NULL
+ *   starts     device int32 [sequences + 1]
+ * AR_DT_E4M3 caches are refused.  An infinite or NaN value of a key that one token of a
+ * sequence sees also reaches tokens next to it that do not see that key.
+ * Device-side waits are bounded (2 s each); one that gives up leaves the outputs undefined
+ * and is reported by ar_fusion_attention_status.
+ * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */
+int ar_fusion_prompt_attention(const ar_kv_cache* cache, const ar_head_rows* q,
+                               const ar_head_rows* out, float* lse, const int32_t* starts,
+                               int tokens, int q_heads, int dtype, float scale, int window,
+                               int sinks, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Device-side status of ar_fusion_prompt_attention on the current device, as
+ * ar_fusion_matmul_status.  *detail: 1 the copies for a free stage, 2 for free
+ * queries, 3 the products for queries, 4 for keys or values, 5 for weights, 6 the
+ * softmax for scores, 7 for sums, 8 the clearing of unseen values, or -1. */
+int ar_fusion_attention_status(void* stream, int* detail);
 
 /* ---------------------------------------------------------- utilities -- */
 
