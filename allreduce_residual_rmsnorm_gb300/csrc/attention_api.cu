@@ -76,8 +76,9 @@ int take_cache(const ar_kv_cache* cache, int dtype, bool runs, CacheArgs* a, boo
         return afail(AR_ERR_UNSUPPORTED, "page_size %d outside 8..65536", c.page_size);
     if (c.sequences > AR_MAX_SEQUENCES)
         return afail(AR_ERR_UNSUPPORTED, "sequences %d > %d", c.sequences, AR_MAX_SEQUENCES);
-    if ((int64_t)c.max_pages * c.page_size > INT_MAX)
-        return afail(AR_ERR_UNSUPPORTED, "max_pages %d x page_size %d beyond 2^31 - 1", c.max_pages,
+    // ends of tiles of keys stay within 32 bits
+    if ((int64_t)c.max_pages * c.page_size > INT_MAX - 1023)
+        return afail(AR_ERR_UNSUPPORTED, "max_pages %d x page_size %d beyond 2^31 - 1024", c.max_pages,
                      c.page_size);
     const int unit = *e4m3 ? 16 : 8;
     if (c.head_dim < unit || c.head_dim % unit != 0)
@@ -113,12 +114,13 @@ int take_rows(const char* name, const ar_head_rows* r, int rows, int heads, Rows
 {
     if (!r || !aligned(r->data, 16))
         return afail(AR_ERR_INVALID, "%s NULL or not 16-byte aligned", name);
-    const int64_t most = (int64_t)1 << 40;
-    const int64_t row = rows > 1 ? r->row : 0, head = heads > 1 ? r->head : 0;
-    if (row % 8 != 0 || head % 8 != 0 || row >= most || row <= -most || head >= most || head <= -most)
-        return afail(AR_ERR_INVALID, "%s: strides %lld, %lld are not multiples of 16 bytes below 2^40",
+    const auto bad = [](int64_t stride, int extent) {
+        return extent > 1 && (stride < 1 || stride % 8 != 0 || stride >= (int64_t)1 << 39);
+    };
+    if (bad(r->row, rows) || bad(r->head, heads))
+        return afail(AR_ERR_INVALID, "%s: strides %lld, %lld are not positive multiples of 16 bytes below 2^40",
                      name, (long long)r->row, (long long)r->head);
-    *out = Rows{static_cast<uint8_t*>(r->data), 2 * row, 2 * head};
+    *out = Rows{static_cast<uint8_t*>(r->data), rows > 1 ? 2 * r->row : 0, heads > 1 ? 2 * r->head : 0};
     return AR_OK;
 }
 
@@ -160,8 +162,10 @@ int take_attention(const ar_kv_cache* cache, const ar_head_rows* q, const ar_hea
     a->lse = lse;
     a->starts = nullptr;
     a->scale_log2 = (float)((double)scale * 1.4426950408889634);
-    a->window = window;
-    a->sinks = sinks;
+    // a window of all that the table holds is none
+    const bool windowed = window > 0 && window < (int64_t)cache->max_pages * cache->page_size;
+    a->window = windowed ? window : 0;
+    a->sinks = windowed ? sinks : 0;
     a->work = static_cast<uint8_t*>(workspace);
     a->work_bytes = workspace_bytes;
     if (!runs)

@@ -8,8 +8,9 @@
 namespace arf {
 namespace {
 
-// code and detail of the first wait that gave up, per device
-__device__ int g_status[2];
+// code and detail of the first wait that gave up, per device: of the products, and
+// of the attention of prompts
+__device__ int g_status[2 * kStatusWords];
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -143,11 +144,25 @@ cudaError_t launch_matmul(int dtype, const MatmulArgs& a, cudaStream_t s)
                    : launch_matmul_wide(dtype, a, d, s);
 }
 
-}  // namespace arf
-
-extern "C" int ar_fusion_matmul_status(void* stream, int* detail)
+bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4])
 {
-    using namespace arf;
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return false;
+    const CUtensorMapDataType type = dtype == AR_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t s[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return fn(map, type, 4, const_cast<void*>(base), d, s, b, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int read_status(int which, void* stream, int* detail, const char* message)
+{
     if (detail)
         *detail = -1;
     DeviceInfo d;
@@ -155,12 +170,13 @@ extern "C" int ar_fusion_matmul_status(void* stream, int* detail)
     int st[2] = {0, 0};
     const int clear[2] = {0, 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int* words = e == cudaSuccess ? d.status + kStatusWords * which : nullptr;
     if (e == cudaSuccess)
-        e = cudaMemcpyAsync(st, d.status, sizeof st, cudaMemcpyDeviceToHost, s);
+        e = cudaMemcpyAsync(st, words, sizeof st, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(s);
     if (e == cudaSuccess && st[0] != 0) {
-        e = cudaMemcpyAsync(d.status, clear, sizeof clear, cudaMemcpyHostToDevice, s);
+        e = cudaMemcpyAsync(words, clear, sizeof clear, cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess)
             e = cudaStreamSynchronize(s);
     }
@@ -170,5 +186,17 @@ extern "C" int ar_fusion_matmul_status(void* stream, int* detail)
         return AR_OK;
     if (detail)
         *detail = st[1];
-    return set_last_error(st[0], "a product's device-side wait gave up");
+    return set_last_error(st[0], message);
+}
+
+}  // namespace arf
+
+extern "C" int ar_fusion_matmul_status(void* stream, int* detail)
+{
+    return arf::read_status(0, stream, detail, "a product's device-side wait gave up");
+}
+
+extern "C" int ar_fusion_attention_status(void* stream, int* detail)
+{
+    return arf::read_status(1, stream, detail, "a prompt's device-side wait gave up");
 }

@@ -17,10 +17,18 @@ bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
 bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, int dtype,
                     uint32_t box_rows, uint32_t box_cols);
 
+// Rows of 16-bit heads as boxes of 64 elements, 128-byte swizzle, zeros outside.
+// Strides in bytes, of dimensions 1 to 3.
+bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+
+constexpr int kStatusWords = 2;     // code, detail
 struct DeviceInfo {
     int sms;
-    int* status;                // device status words of the products: code, detail
+    int* status;                // device status words: of the products, then of attention
 };
+// The answer of the status calls; `which` 0: products, 1: attention.
+int read_status(int which, void* stream, int* detail, const char* message);
 // Of the current device.
 cudaError_t device_info(DeviceInfo* out);
 

@@ -1,89 +1,779 @@
 // Attention of prompts (any number of new tokens per sequence) over the paged cache.
 //
-// A warp has one row and query head, a lane four elements of the head; keys one
-// after the other with a running maximum and sum.  The simplest form that is right.
+// Scores S = Q K^T and sums O += P V on the tensor cores, both in tensor memory.  The rows
+// of a tile are the query heads that share a head of the cache, of consecutive tokens
+// (128 / G tokens x G heads, so that a tile's rows see nearly the same keys); a block has
+// two tiles, which read the same keys and values from shared memory, 128 keys at a
+// time.  While the tensor cores work for one tile the four warps of the other turn its
+// scores into weights: a thread has a row, so its maximum and sum need no exchange,
+// and writes the weights back where the scores were, as the first operand of the
+// second product.  The sums are rescaled only where a row's maximum grew by more than
+// 2^8 (weights stay below 2^8 then, and are as exact).
+//
+//   tensor memory: scores of tile 0, of tile 1, sums of tile 0, of tile 1, 128 columns each
+//   warps 0-3, 4-7: softmax and output of tile 0, 1;  warp 8: copies;  warp 9: products;
+//   warp 10: clears values that no row sees (what lies there need not be finite)
+//
+// Items (a pair of tiles and a head) are worked off by one block per SM: where there
+// are many, whole ones, the longest first; where there are few, the key tiles of all items
+// are one list and a block takes an equal share of it.  Items that several blocks
+// share are added up by join_kernel from sums, maxima and totals in the workspace.
 #include "ar_internal.h"
 #include "attention_internal.h"
-#include "expert_vec.cuh"
 #include "matmul_internal.h"
+#include "tensor_core.cuh"
 
 namespace arf {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kRows = 128, kKeys = 128;             // of a tile, of a step
+constexpr int kRegsLaunch = 168, kRegsFew = 88, kRegsMany = 208;
+static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * kRegsLaunch, "register shares");
+constexpr float kLn2 = 0.693147181f;
+constexpr float kGrowth = 8.0f;                     // of a maximum before the sums are rescaled
+enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
+       kWaitCleared };
 
-template <class D>
-__global__ void __launch_bounds__(kThreads) prompt_attention_kernel(AttentionArgs a)
+template <int DP>
+struct Shape {
+    static constexpr int half = kRows * 128;        // bytes of 128 rows of 64 elements
+    static constexpr int tile = half * (DP / 64);
+    static constexpr int stages = DP == 64 ? 8 : 4;
+    static constexpr int smem = 2 * tile + stages * tile + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
+    static constexpr int part = 2 * kRows * (DP + 2) * 4;
+};
+// More than half of an SM's shared memory for every shape: no second block of this kernel
+// and no block of the products, which would wait for tensor memory, beside one.
+constexpr int kLeastSmem = 200 * 1024;
+
+struct Plan {
+    int tok;                    // tokens of a tile
+    int whole;                  // 1: items are not split
+    int4* desc;                 // [blocks]: parts, first row, tokens, head
+    uint8_t* parts;             // [blocks][2]
+};
+
+// A pair of tiles: tokens from row0 on, `tokens` of them; the first has index i0.
+struct Pair {
+    int seq, row0, tokens, i0;
+    int end, low, sinks;        // keys that any row sees: below end, from low on or below sinks
+    int first, gap, n;          // key tiles: x of n is tile x, or x + gap behind `first`
+};
+
+// whether a key tile holds keys that no row of the pair sees
+__device__ __forceinline__ bool has_unseen(const Pair& p, int key0)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    return key0 + kKeys > p.end || (key0 < p.low && key0 + kKeys > p.sinks);
+}
+__device__ __forceinline__ int tile_of(const Pair& p, int x) { return x < p.first ? x : x + p.gap; }
+
+__device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
+{
+    const int r0 = a.starts[s], r1 = a.starts[s + 1];
+    *row0 = r0;
+    return r0 >= 0 && r1 <= a.T && r1 > r0 ? r1 - r0 : 0;
+}
+
+// pair f of all: sequences in order, in each the last tokens first
+__device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const int* first_pair, int f)
+{
+    int lo = 0, hi = a.c.S;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_pair[mid] <= f)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Pair p;
+    p.seq = lo;
+    const int n = rows_of(a, lo, &p.row0);
+    const int length = clamp_length(a.c, a.c.lengths[lo]);
+    const int t0 = (first_pair[lo + 1] - 1 - f) * 2 * tok;
+    p.row0 += t0;
+    p.tokens = min(2 * tok, n - t0);
+    p.i0 = length - n + t0;
+    p.end = max(p.i0 + p.tokens, 0);
+    p.low = a.window ? (int)max((long long)p.i0 - a.window + 1, 0ll) : 0;
+    p.sinks = a.window ? min(a.sinks, p.end) : 0;
+    p.first = (p.sinks + kKeys - 1) / kKeys;
+    p.gap = max(0, min(p.low, p.end) / kKeys - p.first);
+    p.n = (p.end + kKeys - 1) / kKeys - p.gap;
+    return p;
+}
+
+// The items of a block, one after the other: key tiles x0 .. x1 - 1 of a pair for a head.
+struct Walk {
+    int item, items, x, step;   // whole items: `step` counts them
+    long long left;             // of a share: units left
+    Pair p;
+    int head, x0, x1;
+
+    __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const int* first_pair)
+    {
+        for (;;) {
+            if (plan.whole) {
+                // back and forth over the blocks, so that the first does not get the
+                // longest of every round
+                const long long base = (long long)step * gridDim.x;
+                const int at = step & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+                if (base >= items)
+                    return false;
+                ++step;
+                if (base + at >= items)
+                    continue;
+                item = (int)(base + at);
+            } else {
+                if (left <= 0)
+                    return false;
+            }
+            const int f = item / a.c.heads;
+            head = item - f * a.c.heads;
+            p = pair_at(a, plan.tok, first_pair, f);
+            x0 = x;
+            x1 = plan.whole ? p.n : (int)min((long long)p.n, x0 + left);
+            if (!plan.whole) {
+                left -= x1 - x0;
+                ++item;
+                x = 0;
+            }
+            if (x1 > x0)
+                return true;
+        }
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <class D, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v, AttentionArgs a, Plan plan,
+                            int* status)
+{
+    using F = Shape<DP>;
+    constexpr uint32_t kStages = F::stages;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 5 + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead, begin_sh[2];
+    __shared__ long long scan_sh[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t q_at = (smem_u32(dyn) + 1023u) & ~1023u, ring = q_at + 2 * F::tile;
+    int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
+                   wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
+                   pfull = sfull + 16, ofull = pfull + 16, done = ofull + 16;
+    const Bail bail{smem_u32(&dead), status};
+
+    if (tid == 0) {
+        dead = 0;
+        for (uint32_t s = 0; s < kStages; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+            bar_init(cleared + 8 * s, 1);
+            bar_init(wanted + 8 * s, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            bar_init(qfull + 8 * t, 1);
+            bar_init(qempty + 8 * t, 1);
+            bar_init(sfull + 8 * t, 1);
+            bar_init(pfull + 8 * t, 4);
+            bar_init(ofull + 8 * t, 1);
+        }
+        bar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
+    }
+    if (warp == 9)
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // not before this block has its tensor memory: the next kernel may want some
     pdl_trigger();
     pdl_wait();
-    const int row = (int)(item / a.Hq), h = (int)(item - (int64_t)row * a.Hq);
-    if (row >= a.T)
-        return;
-    int seq = -1;
-    for (int s0 = 0; s0 <= a.c.S; s0 += 32)
-        seq += __reduce_add_sync(0xffffffffu, s0 + lane <= a.c.S && a.starts[s0 + lane] <= row);
-    if (seq < 0 || seq >= a.c.S || a.starts[seq] < 0 || a.starts[seq + 1] <= row || a.starts[seq + 1] > a.T)
-        return;
-    const int i = clamp_length(a.c, a.c.lengths[seq]) - (a.starts[seq + 1] - row);
-    const int low = a.window ? i - a.window + 1 : 0, hk = h / a.G;
-    float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    for (int e = 0; e < 4; ++e)
-        q[e] = 4 * lane + e < a.c.D
-                   ? load1<D>(a.q.p + row * a.q.row + h * a.q.head, 4 * lane + e) * a.scale_log2
-                   : 0.0f;
-    for (int j = 0; j <= i; ++j) {
-        if (j < low && j >= a.sinks) {
-            j = low - 1;
-            continue;
+    const uint32_t tmem = tmem_slot;
+
+    // pairs before each sequence
+    if (warp == 0) {
+        int before = 0;
+        for (int s0 = 0; s0 < a.c.S; s0 += 32) {
+            int row0, n = 0;
+            if (s0 + lane < a.c.S)
+                n = (rows_of(a, s0 + lane, &row0) + 2 * plan.tok - 1) / (2 * plan.tok);
+            int upto = n;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, m);
+                upto += lane >= m ? v : 0;
+            }
+            if (s0 + lane < a.c.S)
+                first_pair[s0 + lane] = before + upto - n;
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        const int page = a.c.table[(int64_t)seq * a.c.max_pages + (j >> a.c.page_shift)];
-        const int in = j & ((1 << a.c.page_shift) - 1);
-        const bool there = page >= 0 && page < a.c.pages;
-        float s = 0.0f;
-        for (int e = 0; e < 4; ++e)
-            if (there && 4 * lane + e < a.c.D)
-                s = fmaf(q[e], load1<D>(a.c.k + page * a.c.k_page + in * a.c.k_row + hk * a.c.k_head,
-                                        4 * lane + e), s);
-        for (int k = 1; k < 32; k <<= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, k);
-        const float top = fmaxf(m, s), base = top == -INFINITY ? 0.0f : top;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        l = fmaf(l, f, p);
-        for (int e = 0; e < 4; ++e) {
-            o[e] *= f;
-            if (there && 4 * lane + e < a.c.D)
-                o[e] = fmaf(p, load1<D>(a.c.v + page * a.c.v_page + in * a.c.v_row + hk * a.c.v_head,
-                                        4 * lane + e), o[e]);
-        }
-        m = top;
+        if (lane == 0)
+            first_pair[a.c.S] = before;
     }
-    for (int e = 0; e < 4; ++e)
-        if (4 * lane + e < a.c.D)
-            reinterpret_cast<uint16_t*>(a.out.p + row * a.out.row + h * a.out.head)[4 * lane + e] =
-                (uint16_t)pack2<D>(l == 0.0f ? 0.0f : o[e] / l, 0.0f);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)row * a.Hq + h] = (m + log2f(l)) * 0.693147181f;
+    __syncthreads();
+    const int pairs = first_pair[a.c.S];
+
+    Walk start{0, pairs * a.c.heads, 0, 0, 0, {}, 0, 0, 0};
+    long long total = 0, u0 = 0;
+    int blocks = gridDim.x;
+    if (!plan.whole) {
+        // this block's share of the list of key tiles, and where it begins
+        const int per = (pairs + kThreads - 1) / kThreads;
+        const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
+        long long mine = 0;
+        for (int f = f0; f < f1; ++f)
+            mine += (long long)pair_at(a, plan.tok, first_pair, f).n * a.c.heads;
+        long long upto = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, m);
+            upto += lane >= m ? v : 0;
+        }
+        if (lane == 31)
+            scan_sh[warp] = upto;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            upto += w < warp ? scan_sh[w] : 0;
+            total += scan_sh[w];
+        }
+        // no more blocks than units: an item's blocks are then consecutive ones
+        blocks = (int)min((long long)blocks, max(total, 1ll));
+        if ((int)blockIdx.x < blocks) {
+            u0 = total * blockIdx.x / blocks;
+            start.left = total * (blockIdx.x + 1) / blocks - u0;
+        }
+        long long at = upto - mine;
+        if (start.left && u0 >= at && u0 < upto) {
+            for (int f = f0; f < f1; ++f) {
+                const int n = pair_at(a, plan.tok, first_pair, f).n;
+                const long long end = at + (long long)n * a.c.heads;
+                if (u0 < end) {
+                    const int in = (int)(u0 - at);
+                    begin_sh[0] = f * a.c.heads + in / n;
+                    begin_sh[1] = in % n;
+                    break;
+                }
+                at = end;
+            }
+        }
+        if (tid == 0)
+            plan.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        start.item = begin_sh[0];
+        start.x = begin_sh[1];
+    }
+    // rows that see nothing, where that holds for a whole pair
+    for (int f = blockIdx.x; f < pairs; f += (int)gridDim.x) {
+        const Pair p = pair_at(a, plan.tok, first_pair, f);
+        if (p.n > 0)
+            continue;
+        for (int i = tid; i < p.tokens * a.Hq; i += kThreads) {
+            const int row = p.row0 + i / a.Hq, h = i % a.Hq;
+            uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
+            for (int c = 0; c < a.c.D / 8; ++c)
+                *reinterpret_cast<uint4*>(to + 16 * c) = make_uint4(0, 0, 0, 0);
+            if (a.lse)
+                a.lse[(int64_t)row * a.Hq + h] = -INFINITY;
+        }
+    }
+
+    Walk w = start;
+    if (warp >= 8) {
+        regs_fewer<kRegsFew>();
+        if (warp == 8) {
+            // copies: per item the queries, then keys and values of a tile in turn
+            uint32_t it = 0, uses[2] = {0, 0};
+            bool ok = true;
+            const int page_rows = min(1 << a.c.page_shift, kKeys), boxes = kKeys / page_rows;
+            const int box = lane % boxes, part = lane / boxes;      // part: which 64 elements
+            while (ok && w.next(a, plan, first_pair)) {
+                for (int t = 0; t < 2 && t * plan.tok < w.p.tokens && ok; ++t) {
+                    ok = bar_wait(qempty + 8 * t, (uses[t] & 1) ^ 1, bail, kWaitQueryFree);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
+                        bar_expect(qfull + 8 * t, DP / 64 * 128 * plan.tok * a.G);
+                        for (int h = 0; h < DP / 64; ++h)
+                            tma_load_4d(q_at + t * F::tile + h * F::half, &map_q, qfull + 8 * t, 64 * h,
+                                        0, w.head, w.p.row0 + t * plan.tok);
+                    }
+                    __syncwarp();
+                    ++uses[t];
+                }
+                for (int x = w.x0; x < w.x1 && ok; ++x) {
+                    const int key = tile_of(w.p, x) * kKeys + box * page_rows;
+                    int page = -1;
+                    if (key < w.p.end)
+                        page = a.c.table[(int64_t)w.p.seq * a.c.max_pages + (key >> a.c.page_shift)];
+                    // outside the map: zeros
+                    if (page < 0 || page >= a.c.pages)
+                        page = a.c.pages;
+                    const int row = key & ((1 << a.c.page_shift) - 1);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const uint32_t s = it % kStages;
+                        ok = bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            bar_expect(full + 8 * s, F::tile);
+                        __syncwarp();
+                        // a lane's box: at most 16 a half of the tile
+                        const uint32_t to = ring + s * F::tile + box * page_rows * 128;
+                        for (int h = part; h < DP / 64; h += 32 / boxes)
+                            tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
+                                        row, w.head, page);
+                        __syncwarp();
+                        if (kv && lane == 0 && has_unseen(w.p, tile_of(w.p, x) * kKeys))
+                            bar_arrive(wanted + 8 * s);
+                    }
+                }
+            }
+            // until every stage and the queries' places are free again: no copy and no arrival is
+            // on its way when the block ends
+            for (uint32_t i = it < kStages ? 0 : it - kStages; i < it && ok; ++i)
+                ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % kStages), i / kStages & 1, bail,
+                                                      kWaitStage));
+            for (int t = 0; t < 2 && ok; ++t)
+                if (uses[t])
+                    ok = __all_sync(0xffffffffu, bar_wait(qempty + 8 * t, (uses[t] - 1) & 1, bail,
+                                                          kWaitQueryFree));
+            __syncwarp();
+            if (!ok) {
+                // what this warp sent for has to land
+                for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i)
+                    bar_drain(full + 8 * (i % kStages), i / kStages & 1);
+                for (int t = 0; t < 2; ++t)
+                    if (uses[t])
+                        bar_drain(qfull + 8 * t, (uses[t] - 1) & 1);
+            }
+        } else if (warp == 9) {
+            if (elect_one()) {
+                constexpr bool bf16 = D::id == AR_DT_BF16;
+                constexpr uint32_t id_s = half_idesc(kRows, kKeys, bf16, false);
+                constexpr uint32_t id_o = half_idesc(kRows, DP, bf16, true);
+                uint32_t it = 0, uses[2] = {0, 0}, weights[2] = {0, 0}, clears = 0;
+                bool ok = true;
+                const auto scores = [&](int t, uint32_t s) {
+                    const uint64_t q = smem_desc(q_at + t * F::tile), k = smem_desc(ring + s * F::tile);
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i) {
+                        const uint32_t off = (i / 4) * (F::half >> 4) + (i % 4) * 2;
+                        mma_half(tmem + t * 128, q + off, k + off, id_s, i > 0);
+                    }
+                    mma_commit(sfull + 8 * t);
+                };
+                while (ok && w.next(a, plan, first_pair)) {
+                    const int tiles = w.p.tokens > plan.tok ? 2 : 1;
+                    if (!(ok = bar_wait(full + 8 * (it % kStages), it / kStages & 1, bail, kWaitKeys)))
+                        break;
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        if (!(ok = bar_wait(qfull + 8 * t, uses[t] & 1, bail, kWaitQuery)))
+                            break;
+                        ++uses[t];
+                        tc_fence_after();
+                        scores(t, it % kStages);
+                        if (w.x0 + 1 == w.x1)
+                            mma_commit(qempty + 8 * t);
+                    }
+                    if (!ok)
+                        break;
+                    mma_commit(empty + 8 * (it % kStages));
+                    ++it;
+                    for (int x = w.x0; x < w.x1 && ok; ++x) {
+                        const uint32_t sv = it % kStages, sk = (it + 1) % kStages;
+                        const bool last = x + 1 == w.x1;
+                        if (!(ok = bar_wait(full + 8 * sv, it / kStages & 1, bail, kWaitKeys)))
+                            break;
+                        if (has_unseen(w.p, tile_of(w.p, x) * kKeys)) {
+                            if (!(ok = bar_wait(cleared + 8 * sv, clears >> sv & 1, bail, kWaitCleared)))
+                                break;
+                            clears ^= 1u << sv;
+                        }
+                        for (int t = 0; t < tiles && ok; ++t) {
+                            if (!(ok = bar_wait(pfull + 8 * t, weights[t] & 1, bail, kWaitWeights)))
+                                break;
+                            ++weights[t];
+                            tc_fence_after();
+                            const uint64_t v = smem_desc_mn(ring + sv * F::tile, F::half);
+#pragma unroll
+                            for (int i = 0; i < kKeys / 16; ++i)
+                                mma_half_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i,
+                                            v + i * (2048 >> 4), id_o, x > w.x0 || i > 0);
+                            if (t + 1 == tiles)
+                                mma_commit(empty + 8 * sv);
+                            if (last) {
+                                mma_commit(ofull + 8 * t);
+                                continue;
+                            }
+                            if (t == 0 && !(ok = bar_wait(full + 8 * sk, (it + 1) / kStages & 1, bail,
+                                                          kWaitKeys)))
+                                break;
+                            tc_fence_after();
+                            scores(t, sk);
+                            if (x + 2 == w.x1)
+                                mma_commit(qempty + 8 * t);
+                            if (t + 1 == tiles)
+                                mma_commit(empty + 8 * sk);
+                        }
+                        it += last ? 1 : 2;
+                    }
+                }
+                if (!ok) {
+                    mma_commit(done);
+                    bar_drain(done, 0);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 10) {
+            // Values of keys that no row of the pair sees.  The copies say which stage it is: by
+            // then the stage's fill before this one is over, so that the wait for the fill is not
+            // answered by an older one.
+            uint32_t it = 0, asked = 0;
+            bool ok = true;
+            while (ok && w.next(a, plan, first_pair)) {
+                for (int x = w.x0; x < w.x1 && ok; ++x, it += 2) {
+                    const int key0 = tile_of(w.p, x) * kKeys;
+                    if (!has_unseen(w.p, key0))
+                        continue;
+                    const uint32_t s = (it + 1) % kStages;
+                    ok = bar_wait(wanted + 8 * s, asked >> s & 1, bail, kWaitCleared) &&
+                         bar_wait(full + 8 * s, (it + 1) / kStages & 1, bail, kWaitKeys);
+                    asked ^= 1u << s;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    for (int i = lane; i < kKeys * 8; i += 32) {
+                        const int key = key0 + i / 8;
+                        if (key < w.p.end && (key >= w.p.low || key < w.p.sinks))
+                            continue;
+#pragma unroll
+                        for (int h = 0; h < DP / 64; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             ring + s * F::tile + h * F::half + i * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(cleared + 8 * s);
+                }
+            }
+        }
+    } else {
+        regs_more<kRegsMany>();
+        // A wait that gives up is not looked at here: what is stored is then undefined, within the
+        // output, and every later wait returns at once.
+        const int t = warp >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
+        const int in = r / a.G, g = r - in * a.G;       // token of the tile, head of the group
+        uint32_t seen = 0, items = 0;
+        while (w.next(a, plan, first_pair)) {
+            const int tok0 = t * plan.tok;
+            if (tok0 >= w.p.tokens)
+                continue;
+            const bool live = in < plan.tok && tok0 + in < w.p.tokens;
+            const int i = live ? w.p.i0 + tok0 + in : -1;
+            const int ia = w.p.i0 + tok0, ib = w.p.i0 + min(tok0 + plan.tok, w.p.tokens) - 1;
+            float top = -INFINITY;
+            uint64_t sum[2] = {0, 0};
+            for (int x = w.x0; x < w.x1; ++x, ++seen) {
+                const int key0 = tile_of(w.p, x) * kKeys;
+                bar_wait(sfull + 8 * t, seen & 1, bail, kWaitScores);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t s[kKeys];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(s_at + 32 * c, s + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_wait32(s + 32 * c);
+                // every row sees every key?
+                if (!(key0 + kKeys - 1 <= ia &&
+                      (a.window == 0 || key0 > ib - a.window || key0 + kKeys <= a.sinks))) {
+                    const int hi = i + 1 - key0, lo = a.window ? i - a.window + 1 - key0 : -key0,
+                              first = a.sinks - key0;
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c >= hi || (c < lo && c >= first))
+                            s[c] = 0xff800000u;
+                }
+                float m[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    m[c] = max3(__uint_as_float(s[3 * c]), __uint_as_float(s[3 * c + 1]),
+                                __uint_as_float(s[3 * c + 2]));
+#pragma unroll
+                for (int c = 12; c < kKeys; c += 2)
+                    m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale_log2;
+                if (x == w.x0) {
+                    top = best;
+                } else if (__any_sync(0xffffffffu, best > top + kGrowth)) {
+                    const float now = best > top + kGrowth ? best : top;
+                    const float f = now == top ? 1.0f : exp2_fast(top - now);
+                    top = now;
+                    const uint64_t ff = pair_of(f, f);
+                    sum[0] = mul_pair(sum[0], ff);
+                    sum[1] = mul_pair(sum[1], ff);
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + c, o);
+                        tmem_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(o_at + c, o);
+                    }
+                }
+                const float used = top == -INFINITY ? 0.0f : top;
+                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2), minus = pair_of(-used, -used);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int k = 64 * c + 2 * e;
+                        const float2 z = unpack_pair(fma3_pair(pack_pair(s[k], s[k + 1]), scale, minus));
+                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                        sum[e & 1] = add_pair(sum[e & 1], pair_of(e0, e1));
+                        p[e] = pack2<D>(e0, e1);
+                    }
+                    tmem_st32(s_at + 32 * c, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(pfull + 8 * t);
+            }
+            const float2 two = unpack_pair(add_pair(sum[0], sum[1]));
+            const float total_w = two.x + two.y;
+            bar_wait(ofull + 8 * t, items & 1, bail, kWaitSums);
+            ++items;
+            __syncwarp();
+            tc_fence_after();
+            const int row = w.p.row0 + tok0 + in, h = w.head * a.G + g;
+            const bool split = w.x0 > 0 || w.x1 < w.p.n;
+            if (!split) {
+                const float inv = total_w > 0.0f || total_w != total_w ? 1.0f / total_w : 0.0f;
+                uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
+#pragma unroll
+                for (int c = 0; c < DP; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
+                    tmem_wait(o);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        uint4 v;
+                        v.x = pack2<D>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        v.y = pack2<D>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        v.z = pack2<D>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        v.w = pack2<D>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                        if (live && c + e < a.c.D)
+                            *reinterpret_cast<uint4*>(to + 2 * (c + e)) = v;
+                    }
+                }
+                if (live && a.lse)
+                    a.lse[(int64_t)row * a.Hq + h] = (top + log2f(total_w)) * kLn2;
+            } else {
+                // a piece that begins here is part 1, one that began before part 0
+                const int which = w.x0 == 0 ? 1 : 0;
+                float* to = reinterpret_cast<float*>(plan.parts +
+                                                     (int64_t)(2 * blockIdx.x + which) * F::part) +
+                            t * kRows + r;
+                to[0] = top;
+                to[2 * kRows] = total_w;
+                to += 4 * kRows;
+#pragma unroll
+                for (int c = 0; c < DP; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
+                    tmem_wait(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        to[(c + e) * 2 * kRows] = __uint_as_float(o[e]);
+                }
+                if (which && tid == 0) {
+                    // the block that has the item's last unit
+                    const long long used_units = total * (blockIdx.x + 1) / blocks;
+                    const long long lastu = used_units + (w.p.n - w.x1) - 1;
+                    const int end = (int)(((lastu + 1) * blocks - 1) / total);
+                    plan.desc[blockIdx.x] =
+                        make_int4(end - (int)blockIdx.x + 1, w.p.row0, w.p.tokens, w.head);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9)
+        tmem_free(tmem, 512);
+}
+
+// Items that several blocks share.  Block (b, y): the item that begins in block b, 16 of its
+// elements; a thread has a row.
+template <class D, int DP>
+__global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan plan)
+{
+    constexpr int kEach = 16;
+    pdl_trigger();
+    pdl_wait();
+    const int4 d = plan.desc[blockIdx.x];
+    const int r = threadIdx.x, in = r % kRows / a.G, g = r % kRows - in * a.G;
+    const int token = r / kRows * plan.tok + in;
+    if (d.x == 0 || in >= plan.tok || token >= d.z)
+        return;
+    const auto part = [&](int p) {
+        const int slot = p == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + p);
+        return reinterpret_cast<const float*>(plan.parts + (int64_t)slot * Shape<DP>::part) + r;
+    };
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int p = 0; p < d.x; ++p)
+        top = fmaxf(top, part(p)[0]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+        acc[e] = 0.0f;
+    const int d0 = blockIdx.y * kEach;
+#pragma unroll 2
+    for (int p = 0; p < d.x; ++p) {
+        const float* s = part(p);
+        const float f = exp2_fast(s[0] - base);
+        sum = fmaf(s[2 * kRows], f, sum);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            acc[e] = fmaf(s[(2 + d0 + e) * 2 * kRows], f, acc[e]);
+    }
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int row = d.y + token, h = d.w * a.G + g;
+    uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
+#pragma unroll
+    for (int e = 0; e < kEach; e += 8) {
+        if (d0 + e >= a.c.D)
+            continue;
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f[k] = acc[e + k] * inv;
+        *reinterpret_cast<uint4*>(to + 2 * (d0 + e)) = pack8<D>(f);
+    }
+    if (a.lse && blockIdx.y == 0)
+        a.lse[(int64_t)row * a.Hq + h] = (top + log2f(sum)) * kLn2;
+}
+
+// the stride of an extent of one: any multiple of 16
+uint64_t stride_of(int64_t stride) { return stride ? (uint64_t)stride : 16u; }
+
+template <class D, int DP>
+cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
+{
+    constexpr int smem = Shape<DP>::smem > kLeastSmem ? Shape<DP>::smem : kLeastSmem;
+    static_assert(smem <= 227 * 1024 - 2048, "shared memory");
+    Plan plan{};
+    plan.tok = kRows / a.G;
+    const uint64_t D_ = (uint64_t)a.c.D;
+    const uint32_t page = 1u << a.c.page_shift, box = page < (uint32_t)kKeys ? page : kKeys;
+    CUtensorMap map_q, map_k, map_v;
+    if (!rows_tensor_map(&map_q, D::id, a.q.p, {D_, (uint64_t)a.G, (uint64_t)a.c.heads, (uint64_t)a.T},
+                         {stride_of(a.q.head), stride_of(a.q.head * a.G), stride_of(a.q.row)},
+                         {64, (uint32_t)a.G, 1, (uint32_t)plan.tok}) ||
+        !rows_tensor_map(&map_k, D::id, a.c.k, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
+                         {stride_of(a.c.k_row), stride_of(a.c.k_head), stride_of(a.c.k_page)},
+                         {64, box, 1, 1}) ||
+        !rows_tensor_map(&map_v, D::id, a.c.v, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
+                         {stride_of(a.c.v_row), stride_of(a.c.v_head), stride_of(a.c.v_page)},
+                         {64, box, 1, 1}))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        // fewer registers at launch than the shares add up to would wait for ever
+        cudaFuncAttributes attr;
+        const cudaError_t ea = cudaFuncGetAttributes(&attr, prompt_attention_kernel<D, DP>);
+        if (ea != cudaSuccess)
+            return ea;
+        if (attr.numRegs < kRegsLaunch)
+            return cudaErrorLaunchOutOfResources;
+        return cudaFuncSetAttribute(prompt_attention_kernel<D, DP>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess)
+        return e;
+    // at most so many items: every sequence may end in a part of a pair
+    const int64_t items = ((int64_t)a.T / (2 * plan.tok) + (a.c.S < a.T ? a.c.S : a.T)) * a.c.heads;
+    if (items > 0x7fffffffll - d.sms)
+        return cudaErrorInvalidValue;
+    int blocks = d.sms;
+    const int64_t fit = (int64_t)(a.work_bytes / (16 + 2 * Shape<DP>::part));
+    plan.whole = items >= 4ll * d.sms || fit < 2;
+    if (plan.whole) {
+        if (items < blocks)
+            blocks = (int)items;
+    } else {
+        const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
+        const int64_t most = items * ((keys + kKeys - 1) / kKeys);
+        if (most < blocks)
+            blocks = (int)most;
+        if (fit < blocks)
+            blocks = (int)fit;
+        plan.desc = reinterpret_cast<int4*>(a.work);
+        plan.parts = a.work + 16 * (int64_t)blocks;
+    }
+    e = launch_after(prompt_attention_kernel<D, DP>, blocks, kThreads, smem, s, map_q, map_k, map_v, a,
+                     plan, d.status + kStatusWords);
+    if (e != cudaSuccess || plan.whole || blocks == 1)
+        return e;
+    return launch_after(join_kernel<D, DP>, dim3(blocks, DP / 16), 2 * kRows, 0, s, a, plan);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(int dtype, const AttentionArgs& a, cudaStream_t s)
 {
-    const int64_t blocks = ((int64_t)a.T * a.Hq + kThreads / 32 - 1) / (kThreads / 32);
-    return dtype == AR_DT_BF16
-               ? launch_after(prompt_attention_kernel<Bf16>, (unsigned)blocks, kThreads, 0, s, a)
-               : launch_after(prompt_attention_kernel<Fp16>, (unsigned)blocks, kThreads, 0, s, a);
+    DeviceInfo d;
+    const cudaError_t e = device_info(&d);
+    if (e != cudaSuccess)
+        return e;
+    if (dtype == AR_DT_BF16)
+        return a.c.D <= 64 ? launch_t<Bf16, 64>(a, d, s) : launch_t<Bf16, 128>(a, d, s);
+    return a.c.D <= 64 ? launch_t<Fp16, 64>(a, d, s) : launch_t<Fp16, 128>(a, d, s);
 }
 
 }  // namespace arf
-
-extern "C" int ar_fusion_attention_status(void* stream, int* detail)
-{
-    (void)stream;
-    if (detail)
-        *detail = -1;
-    return AR_OK;
-}

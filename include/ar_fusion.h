@@ -661,10 +661,10 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
 #define AR_ATTENTION_WORKSPACE_BYTES (32 << 20)
 
 /* Rows of heads: element d of head h of row t is data[t * row + h * head + d].
- * The strides are in elements, of either sign or order, and 16-byte multiples; data
- * is 16-byte aligned (a slice of a projection's output [tokens][all heads][dim]
- * is as good as an array of its own).  A stride along an extent of one is not
- * looked at. */
+ * The strides are in elements, positive 16-byte multiples below 2^40 bytes in either
+ * order; data is 16-byte aligned (a slice of a projection's output [tokens][all
+ * heads][dim] is as good as an array of its own).  A stride along an extent of one is
+ * not looked at. */
 typedef struct ar_head_rows {
     void* data;
     int64_t row, head;
@@ -683,7 +683,7 @@ typedef struct ar_head_rows {
  *   page_table   device int32 [sequences][max_pages]
  *   lengths      device int32 [sequences]
  *   sequences    0 .. AR_MAX_SEQUENCES (0: nothing launched);  max_pages >= 1,
- *                max_pages * page_size < 2^31 */
+ *                max_pages * page_size at most 2^31 - 1024 */
 typedef struct ar_kv_cache {
     void *k, *v;
     int64_t k_page, k_row, k_head, v_page, v_row, v_head;
