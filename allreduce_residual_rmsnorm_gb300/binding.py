@@ -71,7 +71,7 @@ AR_MAX_EXPERTS = 1024
 AR_MAX_TOPK = 32
 AR_MAX_GROUPS = 32
 AR_QUANT_BLOCK = 128
-AR_MAX_SEQUENCES = 4096
+AR_MAX_SEQUENCES = 2048
 AR_MAX_HEAD_GROUP = 128
 AR_MAX_HEAD_DIM = 128
 AR_MAX_AXES = 4

@@ -40,7 +40,7 @@ struct Shape {
     static constexpr int half = kRows * 128;        // bytes of 128 rows of 64 elements
     static constexpr int tile = half * (DP / 64);
     static constexpr int stages = DP == 64 ? 8 : 4;
-    static constexpr int smem = 2 * tile + stages * tile + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
+    static constexpr int smem = (2 + stages) * tile + 3 * (AR_MAX_SEQUENCES + 1) * 4 + 1024;
     static constexpr int part = 2 * kRows * (DP + 2) * 4;
 };
 // More than half of an SM's shared memory for every shape: no second block of this kernel
@@ -68,30 +68,33 @@ __device__ __forceinline__ bool has_unseen(const Pair& p, int key0)
 }
 __device__ __forceinline__ int tile_of(const Pair& p, int x) { return x < p.first ? x : x + p.gap; }
 
-__device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
+// In shared memory, [sequences (+ 1)]: pairs before each sequence, starts, lengths.
+struct Table {
+    int *first_pair, *starts, *lengths;
+};
+
+__device__ __forceinline__ int rows_of(const AttentionArgs& a, const Table& tab, int s)
 {
-    const int r0 = a.starts[s], r1 = a.starts[s + 1];
-    *row0 = r0;
+    const int r0 = tab.starts[s], r1 = tab.starts[s + 1];
     return r0 >= 0 && r1 <= a.T && r1 > r0 ? r1 - r0 : 0;
 }
 
 // pair f of all: sequences in order, in each the last tokens first
-__device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const int* first_pair, int f)
+__device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const Table& tab, int f)
 {
     int lo = 0, hi = a.c.S;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first_pair[mid] <= f)
+        if (tab.first_pair[mid] <= f)
             lo = mid;
         else
             hi = mid;
     }
     Pair p;
     p.seq = lo;
-    const int n = rows_of(a, lo, &p.row0);
-    const int length = clamp_length(a.c, a.c.lengths[lo]);
-    const int t0 = (first_pair[lo + 1] - 1 - f) * 2 * tok;
-    p.row0 += t0;
+    const int n = rows_of(a, tab, lo), length = tab.lengths[lo];
+    const int t0 = (tab.first_pair[lo + 1] - 1 - f) * 2 * tok;
+    p.row0 = tab.starts[lo] + t0;
     p.tokens = min(2 * tok, n - t0);
     p.i0 = length - n + t0;
     p.end = max(p.i0 + p.tokens, 0);
@@ -110,7 +113,7 @@ struct Walk {
     Pair p;
     int head, x0, x1;
 
-    __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const int* first_pair)
+    __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const Table& tab)
     {
         for (;;) {
             if (plan.whole) {
@@ -130,7 +133,7 @@ struct Walk {
             }
             const int f = item / a.c.heads;
             head = item - f * a.c.heads;
-            p = pair_at(a, plan.tok, first_pair, f);
+            p = pair_at(a, plan.tok, tab, f);
             x0 = x;
             x1 = plan.whole ? p.n : (int)min((long long)p.n, x0 + left);
             if (!plan.whole) {
@@ -163,6 +166,12 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
     return r;
 }
 
+// the lowest n of 32 bits
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
+
 template <class D, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -173,16 +182,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     using F = Shape<DP>;
     constexpr uint32_t kStages = F::stages;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 5 + 1];
+    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 6 + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, begin_sh[2];
     __shared__ long long scan_sh[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t q_at = (smem_u32(dyn) + 1023u) & ~1023u, ring = q_at + 2 * F::tile;
-    int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
+    Table tab;
+    tab.first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
+    tab.starts = tab.first_pair + AR_MAX_SEQUENCES + 1;
+    tab.lengths = tab.starts + AR_MAX_SEQUENCES + 1;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
                    wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
-                   pfull = sfull + 16, ofull = pfull + 16, done = ofull + 16;
+                   pfull = sfull + 16, ofull = pfull + 32, done = ofull + 16;
     const Bail bail{smem_u32(&dead), status};
 
     if (tid == 0) {
@@ -197,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(qfull + 8 * t, 1);
             bar_init(qempty + 8 * t, 1);
             bar_init(sfull + 8 * t, 1);
-            bar_init(pfull + 8 * t, 4);
+            bar_init(pfull + 16 * t, 4);        // weights of the first 64 keys, of the others
+            bar_init(pfull + 16 * t + 8, 4);
             bar_init(ofull + 8 * t, 1);
         }
         bar_init(done, 1);
@@ -217,12 +230,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
 
     // pairs before each sequence
+    for (int s = tid; s <= a.c.S; s += kThreads) {
+        tab.starts[s] = a.starts[s];
+        if (s < a.c.S)
+            tab.lengths[s] = clamp_length(a.c, a.c.lengths[s]);
+    }
+    __syncthreads();
     if (warp == 0) {
         int before = 0;
         for (int s0 = 0; s0 < a.c.S; s0 += 32) {
-            int row0, n = 0;
+            int n = 0;
             if (s0 + lane < a.c.S)
-                n = (rows_of(a, s0 + lane, &row0) + 2 * plan.tok - 1) / (2 * plan.tok);
+                n = (rows_of(a, tab, s0 + lane) + 2 * plan.tok - 1) / (2 * plan.tok);
             int upto = n;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -230,14 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 upto += lane >= m ? v : 0;
             }
             if (s0 + lane < a.c.S)
-                first_pair[s0 + lane] = before + upto - n;
+                tab.first_pair[s0 + lane] = before + upto - n;
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (lane == 0)
-            first_pair[a.c.S] = before;
+            tab.first_pair[a.c.S] = before;
     }
     __syncthreads();
-    const int pairs = first_pair[a.c.S];
+    const int pairs = tab.first_pair[a.c.S];
 
     Walk start{0, pairs * a.c.heads, 0, 0, 0, {}, 0, 0, 0};
     long long total = 0, u0 = 0;
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
         long long mine = 0;
         for (int f = f0; f < f1; ++f)
-            mine += (long long)pair_at(a, plan.tok, first_pair, f).n * a.c.heads;
+            mine += (long long)pair_at(a, plan.tok, tab, f).n * a.c.heads;
         long long upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -272,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long at = upto - mine;
         if (start.left && u0 >= at && u0 < upto) {
             for (int f = f0; f < f1; ++f) {
-                const int n = pair_at(a, plan.tok, first_pair, f).n;
+                const int n = pair_at(a, plan.tok, tab, f).n;
                 const long long end = at + (long long)n * a.c.heads;
                 if (u0 < end) {
                     const int in = (int)(u0 - at);
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // rows that see nothing, where that holds for a whole pair
     for (int f = blockIdx.x; f < pairs; f += (int)gridDim.x) {
-        const Pair p = pair_at(a, plan.tok, first_pair, f);
+        const Pair p = pair_at(a, plan.tok, tab, f);
         if (p.n > 0)
             continue;
         for (int i = tid; i < p.tokens * a.Hq; i += kThreads) {
@@ -313,21 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const int page_rows = min(1 << a.c.page_shift, kKeys), boxes = kKeys / page_rows;
             const int box = lane % boxes, part = lane / boxes;      // part: which 64 elements
-            while (ok && w.next(a, plan, first_pair)) {
-                for (int t = 0; t < 2 && t * plan.tok < w.p.tokens && ok; ++t) {
-                    ok = bar_wait(qempty + 8 * t, (uses[t] & 1) ^ 1, bail, kWaitQueryFree);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
-                        break;
-                    if (elect_one()) {
-                        bar_expect(qfull + 8 * t, DP / 64 * 128 * plan.tok * a.G);
-                        for (int h = 0; h < DP / 64; ++h)
-                            tma_load_4d(q_at + t * F::tile + h * F::half, &map_q, qfull + 8 * t, 64 * h,
-                                        0, w.head, w.p.row0 + t * plan.tok);
-                    }
-                    __syncwarp();
-                    ++uses[t];
-                }
+            while (ok && w.next(a, plan, tab)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x) {
                     const int key = tile_of(w.p, x) * kKeys + box * page_rows;
                     int page = -1;
@@ -353,6 +358,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
                                         row, w.head, page);
                         __syncwarp();
+                        // the queries behind the first keys: their place is free later
+                        if (x == w.x0 && kv == 0) {
+                            for (int t = 0; t < 2 && t * plan.tok < w.p.tokens && ok; ++t) {
+                                ok = bar_wait(qempty + 8 * t, (uses[t] & 1) ^ 1, bail, kWaitQueryFree);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok)
+                                    break;
+                                if (elect_one()) {
+                                    bar_expect(qfull + 8 * t, DP / 64 * 128 * plan.tok * a.G);
+                                    for (int h = 0; h < DP / 64; ++h)
+                                        tma_load_4d(q_at + t * F::tile + h * F::half, &map_q, qfull + 8 * t, 64 * h,
+                                                    0, w.head, w.p.row0 + t * plan.tok);
+                                }
+                                __syncwarp();
+                                ++uses[t];
+                            }
+                            if (!ok) {
+                                ++it;           // the keys are on their way
+                                break;
+                            }
+                        }
                         if (kv && lane == 0 && has_unseen(w.p, tile_of(w.p, x) * kKeys))
                             bar_arrive(wanted + 8 * s);
                     }
@@ -392,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(sfull + 8 * t);
                 };
-                while (ok && w.next(a, plan, first_pair)) {
+                while (ok && w.next(a, plan, tab)) {
                     const int tiles = w.p.tokens > plan.tok ? 2 : 1;
                     if (!(ok = bar_wait(full + 8 * (it % kStages), it / kStages & 1, bail, kWaitKeys)))
                         break;
@@ -420,15 +446,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             clears ^= 1u << sv;
                         }
                         for (int t = 0; t < tiles && ok; ++t) {
-                            if (!(ok = bar_wait(pfull + 8 * t, weights[t] & 1, bail, kWaitWeights)))
+                            const uint64_t v = smem_desc_mn(ring + sv * F::tile, F::half);
+                            for (int h = 0; h < 2 && ok; ++h) {
+                                if (!(ok = bar_wait(pfull + 16 * t + 8 * h, weights[t] & 1, bail,
+                                                    kWaitWeights)))
+                                    break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int i = 0; i < kKeys / 32; ++i)
+                                    mma_half_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * h + 8 * i,
+                                                v + (4 * h + i) * (2048 >> 4), id_o,
+                                                x > w.x0 || h > 0 || i > 0);
+                            }
+                            if (!ok)
                                 break;
                             ++weights[t];
-                            tc_fence_after();
-                            const uint64_t v = smem_desc_mn(ring + sv * F::tile, F::half);
-#pragma unroll
-                            for (int i = 0; i < kKeys / 16; ++i)
-                                mma_half_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i,
-                                            v + i * (2048 >> 4), id_o, x > w.x0 || i > 0);
                             if (t + 1 == tiles)
                                 mma_commit(empty + 8 * sv);
                             if (last) {
@@ -460,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // answered by an older one.
             uint32_t it = 0, asked = 0;
             bool ok = true;
-            while (ok && w.next(a, plan, first_pair)) {
+            while (ok && w.next(a, plan, tab)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x, it += 2) {
                     const int key0 = tile_of(w.p, x) * kKeys;
                     if (!has_unseen(w.p, key0))
@@ -499,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
         const int in = r / a.G, g = r - in * a.G;       // token of the tile, head of the group
         uint32_t seen = 0, items = 0;
-        while (w.next(a, plan, first_pair)) {
+        while (w.next(a, plan, tab)) {
             const int tok0 = t * plan.tok;
             if (tok0 >= w.p.tokens)
                 continue;
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = live ? w.p.i0 + tok0 + in : -1;
             const int ia = w.p.i0 + tok0, ib = w.p.i0 + min(tok0 + plan.tok, w.p.tokens) - 1;
             float top = -INFINITY;
-            uint64_t sum[2] = {0, 0};
+            uint64_t sum = 0;
             for (int x = w.x0; x < w.x1; ++x, ++seen) {
                 const int key0 = tile_of(w.p, x) * kKeys;
                 bar_wait(sfull + 8 * t, seen & 1, bail, kWaitScores);
@@ -523,13 +555,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every row sees every key?
                 if (!(key0 + kKeys - 1 <= ia &&
                       (a.window == 0 || key0 > ib - a.window || key0 + kKeys <= a.sinks))) {
-                    const int hi = i + 1 - key0, lo = a.window ? i - a.window + 1 - key0 : -key0,
+                    const int hi = i + 1 - key0, lo = a.window ? i - a.window + 1 - key0 : 0,
                               first = a.sinks - key0;
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (c >= hi || (c < lo && c >= first))
-                            s[c] = 0xff800000u;
+                    for (int c = 0; c < kKeys; c += 32) {
+                        const uint32_t seen_bits =
+                            below(hi - c) & (~below(lo - c) | below(first - c));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[c + e] = seen_bits >> e & 1 ? s[c + e] : 0xff800000u;
+                    }
                 }
+                // The weights of the first half by the maximum so far, while that of these scores
+                // is found; nearly always it is near enough.
+                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2);
+                uint32_t p[32];
+                uint64_t part[4] = {0, 0, 0, 0};
+                const auto weigh = [&](int c) {
+                    const float used = top == -INFINITY ? 0.0f : top;
+                    const uint64_t minus = pair_of(-used, -used);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int k = 64 * c + 2 * e;
+                        const float2 z = unpack_pair(fma3_pair(pack_pair(s[k], s[k + 1]), scale, minus));
+                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                        part[e & 3] = add_pair(part[e & 3], pair_of(e0, e1));
+                        p[e] = pack2<D>(e0, e1);
+                    }
+                };
+                weigh(0);
                 float m[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -539,48 +593,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 12; c < kKeys; c += 2)
                     m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale_log2;
-                if (x == w.x0) {
-                    top = best;
-                } else if (__any_sync(0xffffffffu, best > top + kGrowth)) {
+                if (__any_sync(0xffffffffu, best > top + kGrowth)) {
                     const float now = best > top + kGrowth ? best : top;
                     const float f = now == top ? 1.0f : exp2_fast(top - now);
                     top = now;
-                    const uint64_t ff = pair_of(f, f);
-                    sum[0] = mul_pair(sum[0], ff);
-                    sum[1] = mul_pair(sum[1], ff);
-#pragma unroll 1
-                    for (int c = 0; c < DP; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_at + c, o);
-                        tmem_wait(o);
+                    sum = mul_pair(sum, pair_of(f, f));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st16(o_at + c, o);
+                    for (int e = 0; e < 4; ++e)
+                        part[e] = 0;
+                    weigh(0);
+                    if (x > w.x0) {
+#pragma unroll 1
+                        for (int c = 0; c < DP; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + c, o);
+                            tmem_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_at + c, o);
+                        }
                     }
                 }
-                const float used = top == -INFINITY ? 0.0f : top;
-                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2), minus = pair_of(-used, -used);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int k = 64 * c + 2 * e;
-                        const float2 z = unpack_pair(fma3_pair(pack_pair(s[k], s[k + 1]), scale, minus));
-                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                        sum[e & 1] = add_pair(sum[e & 1], pair_of(e0, e1));
-                        p[e] = pack2<D>(e0, e1);
-                    }
+                    if (c == 1)
+                        weigh(1);
                     tmem_st32(s_at + 32 * c, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(pfull + 16 * t + 8 * c);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(pfull + 8 * t);
+                sum = add_pair(sum, add_pair(add_pair(part[0], part[1]), add_pair(part[2], part[3])));
             }
-            const float2 two = unpack_pair(add_pair(sum[0], sum[1]));
+            const float2 two = unpack_pair(sum);
             const float total_w = two.x + two.y;
             bar_wait(ofull + 8 * t, items & 1, bail, kWaitSums);
             ++items;
@@ -665,7 +713,7 @@ __global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan p
     };
     float top = -INFINITY;
 #pragma unroll 8
-    for (int p = 0; p < d.x; ++p)
+    for (int p = 0; p < d.x; ++p)       // all of their loads in flight
         top = fmaxf(top, part(p)[0]);
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, acc[kEach];
@@ -673,7 +721,7 @@ __global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan p
     for (int e = 0; e < kEach; ++e)
         acc[e] = 0.0f;
     const int d0 = blockIdx.y * kEach;
-#pragma unroll 2
+#pragma unroll 4
     for (int p = 0; p < d.x; ++p) {
         const float* s = part(p);
         const float f = exp2_fast(s[0] - base);

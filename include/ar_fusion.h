@@ -652,7 +652,7 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
  * the same place. */
 
 /* Sequences of one call, and query heads that share a key's head. */
-#define AR_MAX_SEQUENCES 4096
+#define AR_MAX_SEQUENCES 2048
 #define AR_MAX_HEAD_GROUP 128
 /* Elements of a head; axes of a position. */
 #define AR_MAX_HEAD_DIM 128

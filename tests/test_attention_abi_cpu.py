@@ -60,7 +60,7 @@ I, N = B.AR_ERR_INVALID, B.AR_ERR_UNSUPPORTED
 CACHES = [
     (dict(dtype=2), N, "cache dtype"), (dict(dtype=4), N, "cache dtype"), (dict(dtype=1), I, "cache dtype"),
     (dict(pages=0), I, "pages"), (dict(heads=0), I, "heads"), (dict(max_pages=0), I, "max_pages"),
-    (dict(sequences=-1), I, "sequences"), (dict(sequences=4097), N, "sequences"),
+    (dict(sequences=-1), I, "sequences"), (dict(sequences=2049), N, "sequences"),
     (dict(page_size=24), I, "page_size"), (dict(page_size=0), I, "page_size"),
     (dict(page_size=4), N, "page_size"), (dict(page_size=1 << 17), N, "page_size"),
     (dict(max_pages=1 << 28), N, "max_pages"), (dict(head_dim=0), I, "head_dim"),

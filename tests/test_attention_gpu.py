@@ -147,7 +147,7 @@ def test_append_many_sequences(cuda_lib):
     g = gen(9)
     new = torch.randint(0, 3, (700,), generator=g).tolist()
     check_append(new, [n + 3 for n in new], 8, 2, 1, 64, 64, BF16, BF16)
-    check_append([1] * 4096, [1 + b % 9 for b in range(4096)], 16, 1, 1, 16, 16, BF16, BF16)
+    check_append([1] * 2048, [1 + b % 9 for b in range(2048)], 16, 1, 1, 16, 16, BF16, BF16)
 
 
 # --------------------------------------------------- one token per sequence
@@ -220,7 +220,7 @@ def test_decode_many_sequences(workspace):
     for S in (129, 600):
         lengths = torch.randint(0, 90, (S,), generator=g).tolist()
         check_decode(lengths, 16, 4, 2, 64, BF16, BF16, workspace)
-    check_decode([1 + b % 3 for b in range(4096)], 8, 1, 1, 16, BF16, BF16, workspace)
+    check_decode([1 + b % 3 for b in range(2048)], 8, 1, 1, 16, BF16, BF16, workspace)
     check_decode([0] * 50, 8, 2, 1, 64, BF16, BF16, workspace)
 
 
@@ -348,7 +348,7 @@ def test_prompt_many_sequences(workspace):
     g = gen(8)
     new = torch.randint(0, 4, (700,), generator=g).tolist()
     check_prompt(new, [n + b % 40 for b, n in enumerate(new)], 16, 2, 1, 64, BF16, workspace)
-    check_prompt([b % 2 for b in range(4096)], [1 + b % 3 for b in range(4096)], 8, 1, 1, 16, BF16,
+    check_prompt([b % 2 for b in range(2048)], [1 + b % 3 for b in range(2048)], 8, 1, 1, 16, BF16,
                  workspace)
 
 
