@@ -7,8 +7,7 @@
 // time.  While the tensor cores work for one tile the four warps of the other turn its
 // scores into weights: a thread has a row, so its maximum and sum need no exchange,
 // and writes the weights back where the scores were, as the first operand of the
-// second product.  The sums are rescaled only where a row's maximum grew by more than
-// 2^8 (weights stay below 2^8 then, and are as exact).
+// second product.  The sums are rescaled only where a row's maximum grew far (growth()).
 //
 //   tensor memory: scores of tile 0, of tile 1, sums of tile 0, of tile 1, 128 columns each
 //   warps 0-3, 4-7: softmax and output of tile 0, 1;  warp 8: copies;  warp 9: products;
@@ -31,7 +30,13 @@ constexpr int kRows = 128, kKeys = 128;             // of a tile, of a step
 constexpr int kRegsLaunch = 168, kRegsFew = 88, kRegsMany = 208;
 static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * kRegsLaunch, "register shares");
 constexpr float kLn2 = 0.693147181f;
-constexpr float kGrowth = 8.0f;                     // of a maximum before the sums are rescaled
+// How far (in powers of two) a row's maximum may grow before its sums are rescaled: weights
+// are then up to 2^growth, as exact as below 1.  fp16 weights end at 2^16; with bf16 ones the
+// sums of n keys stay finite for values below 2^96 / n.  At 2^8 some row of 32 was rescaled
+// in two of three tiles of a windowed prompt, whose first tile has 4 keys (399 us, now
+// see below), at 0.4 us each.
+template <class D>
+__device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16 ? 32.0f : 14.0f; }
 enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
        kWaitCleared };
 
@@ -50,6 +55,7 @@ constexpr int kLeastSmem = 200 * 1024;
 struct Plan {
     int tok;                    // tokens of a tile
     int whole;                  // 1: items are not split
+    int wide;                   // 1: rows of the output are 32-byte aligned
     int4* desc;                 // [blocks]: parts, first row, tokens, head
     uint8_t* parts;             // [blocks][2]
 };
@@ -593,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 12; c < kKeys; c += 2)
                     m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale_log2;
-                if (__any_sync(0xffffffffu, best > top + kGrowth)) {
-                    const float now = best > top + kGrowth ? best : top;
+                if (__any_sync(0xffffffffu, best > top + growth<D>())) {
+                    const float now = best > top + growth<D>() ? best : top;
                     const float f = now == top ? 1.0f : exp2_fast(top - now);
                     top = now;
                     sum = mul_pair(sum, pair_of(f, f));
@@ -639,20 +645,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!split) {
                 const float inv = total_w > 0.0f || total_w != total_w ? 1.0f / total_w : 0.0f;
                 uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
+                uint32_t o[DP];
+#pragma unroll
+                for (int c = 0; c < DP; c += 32)
+                    tmem_ld32(o_at + c, o + c);
+#pragma unroll
+                for (int c = 0; c < DP; c += 32)
+                    tmem_wait32(o + c);
 #pragma unroll
                 for (int c = 0; c < DP; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_at + c, o);
-                    tmem_wait(o);
+                    uint32_t v[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        uint4 v;
-                        v.x = pack2<D>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                        v.y = pack2<D>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                        v.z = pack2<D>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                        v.w = pack2<D>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                        if (live && c + e < a.c.D)
-                            *reinterpret_cast<uint4*>(to + 2 * (c + e)) = v;
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = pack2<D>(__uint_as_float(o[c + 2 * e]) * inv,
+                                        __uint_as_float(o[c + 2 * e + 1]) * inv);
+                    // whole sectors where the output allows it
+                    if (plan.wide && c + 16 <= a.c.D) {
+                        if (live)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + 2 * c),
+                                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                                         "r"(v[6]), "r"(v[7])
+                                         : "memory");
+                    } else {
+                        if (live && c < a.c.D)
+                            *reinterpret_cast<uint4*>(to + 2 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (live && c + 8 < a.c.D)
+                            *reinterpret_cast<uint4*>(to + 2 * c + 16) = make_uint4(v[4], v[5], v[6], v[7]);
                     }
                 }
                 if (live && a.lse)
@@ -757,6 +775,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     static_assert(smem <= 227 * 1024 - 2048, "shared memory");
     Plan plan{};
     plan.tok = kRows / a.G;
+    plan.wide = ((uintptr_t)a.out.p | (uint64_t)a.out.row | (uint64_t)a.out.head) % 32 == 0;
     const uint64_t D_ = (uint64_t)a.c.D;
     const uint32_t page = 1u << a.c.page_shift, box = page < (uint32_t)kKeys ? page : kKeys;
     CUtensorMap map_q, map_k, map_v;
