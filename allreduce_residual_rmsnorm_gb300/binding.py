@@ -213,7 +213,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _load_native(L: ctypes.CDLL) -> None:
-    """The expert-layer calls' marshalling in C++ (csrc/marshal.cpp).  The calls
+    """The expert-layer and attention-layer calls' marshalling in C++ (csrc/marshal.cpp).  The calls
     work without it, through ctypes, some microseconds slower each."""
     global _native
     path = marshal_path()
@@ -228,7 +228,8 @@ def _load_native(L: ctypes.CDLL) -> None:
     m.bind(*(ctypes.cast(getattr(L, f), _vp).value
              for f in ("ar_fusion_route", "ar_fusion_expert_plan", "ar_fusion_quant_blocks",
                        "ar_fusion_matmul_fp8", "ar_fusion_expert_matmul_fp8",
-                       "ar_fusion_combine")))
+                       "ar_fusion_combine", "ar_fusion_rope_append",
+                       "ar_fusion_decode_attention", "ar_fusion_prompt_attention")))
     _native = m
 
 
@@ -860,7 +861,17 @@ def ar_fusion_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tens
     contiguous last dimension.  page_table [sequences, max_pages], lengths [sequences] (the
     new tokens included), starts [sequences + 1] (None: a row for each sequence),
     positions [tokens] or [axes, tokens] (None: the index in the sequence) int32; inv_freq
-    [rot / 2] fp32 (None: no rotation); sections: pairs of each axis."""
+    [rot / 2] fp32 (None: no rotation); sections: pairs of each axis (None: one axis)."""
+    if sections is not None:
+        sections = tuple(sections)
+    if _native is not None:
+        rc = _native.rope_append(q, k, v, k_cache, v_cache, page_table, lengths, inv_freq, q_out,
+                                 starts, positions, sections, interleaved, kv_scale,
+                                 _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if k.dim() != 3:
         raise ValueError(f"k: {k.dim()} dimensions, expected 3")
     if k.dtype not in _ROWS:
@@ -898,6 +909,15 @@ def ar_fusion_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tens
 
 def _attention(name, q, k_cache, v_cache, page_table, lengths, out, workspace, scale, window,
                sinks, lse, kv_scale, starts, stream):
+    if scale is None:
+        scale = max(1, k_cache.shape[-1] if k_cache.dim() else 1) ** -0.5
+    if _native is not None:
+        rc = _native.attention(q, k_cache, v_cache, page_table, lengths, starts, out, workspace,
+                               float(scale), window, sinks, lse, kv_scale, _handle(stream))
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return
     if q.dim() != 3:
         raise ValueError(f"q: {q.dim()} dimensions, expected 3")
     if q.dtype not in _ROWS:
@@ -910,8 +930,6 @@ def _attention(name, q, k_cache, v_cache, page_table, lengths, out, workspace, s
         raise ValueError(f"q: {tokens} rows for {cache.sequences} sequences")
     qr = _head_rows("q", q, tokens, q.dtype, cache.head_dim)
     to = _head_rows("out", out, tokens, q.dtype, cache.head_dim, q_heads)
-    if scale is None:
-        scale = cache.head_dim ** -0.5
     work, size = None, 0
     if workspace is not None:
         size = workspace.numel() * workspace.element_size()
@@ -950,6 +968,8 @@ def ar_fusion_prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                kv_scale: torch.Tensor | None = None, stream=None) -> None:
     """Any number of new tokens per sequence: q and out [tokens, q_heads, dim], lse [tokens,
     q_heads] fp32, starts [sequences + 1] int32; the rest as ar_fusion_decode_attention."""
+    if starts is None:
+        raise ValueError("starts: expected a tensor")
     _attention("ar_fusion_prompt_attention", q, k_cache, v_cache, page_table, lengths, out,
                workspace, scale, window, sinks, lse, kv_scale, starts, stream)
 

@@ -1,9 +1,11 @@
 // Attention of one new token per sequence over the paged cache.
 //
 // Memory bounds it: every key and value is read once, for all the query heads that
-// share it.  Those are the rows of m16n8k16 products (up to 16; scores = Q K^T, sums =
-// P V), so the scores leave the products in the layout in which the next ones take
-// their weights, and no value of theirs passes through shared memory.  At 8 heads per
+// share it.  Those are the 8 columns of m16n8k16 products (two of them for 9 to 16 heads):
+// S^T = K Q^T, O^T = V^T P^T, keys and values straight from shared memory as first operands, the
+// weights turned by movmatrix from one product's result to the next one's operand.
+// With the heads as the 16 rows, half of them empty at 8, the products of an E4M3 cache
+// took longer than its bytes (128 x 2048-4096 tokens x 64 / 8 heads 180 us).  At 8 heads per
 // key the arithmetic is 8 operations a byte, 54 T a second at the memory's rate: more
 // than the fp32 pipes have left beside the conversions, little for these products;
 // the instructions on 128 rows of tensor memory would waste seven eighths of them and
@@ -69,6 +71,13 @@ __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t at)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(at)
                  : "memory");
+}
+// the 8 x 8 matrix of 16-bit elements that a warp holds, turned over
+__device__ __forceinline__ uint32_t turned(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
 __device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t at)
 {
@@ -200,25 +209,38 @@ __device__ __forceinline__ void load_slice(const AttentionArgs& a, const Cursor<
     copies_commit();
 }
 
-// Element of the head that register (tile j, e) of a thread's sums belongs to.
+// Register (tile j of 16 elements, n of 8 heads, e) of a thread's sums: which element of
+// the head, and which head.
 template <bool F8>
-__device__ __forceinline__ int dim_of(int j, int e, int t)
+__device__ __forceinline__ int dim_of(int j, int e, int g)
 {
-    return F8 ? 16 * (j >> 1) + 4 * t + 2 * (e & 1) + (j & 1) : 8 * j + 2 * t + (e & 1);
+    return 16 * j + (F8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+}
+__device__ __forceinline__ int head_of(int n, int e, int t) { return 8 * n + 2 * t + (e & 1); }
+
+// a thread's two elements of tile j of a head
+template <class D, bool F8>
+__device__ __forceinline__ void store_dims(uint8_t* to, int dims, int j, int g, float f0, float f1)
+{
+    const uint32_t v = pack2<D>(f0, f1);
+    const int d0 = dim_of<F8>(j, 0, g), d1 = dim_of<F8>(j, 2, g);
+    if constexpr (F8) {
+        if (d0 < dims)          // even: the next one is in, too
+            *reinterpret_cast<uint32_t*>(to + 2 * d0) = v;
+    } else {
+        if (d0 < dims)
+            *reinterpret_cast<uint16_t*>(to + 2 * d0) = (uint16_t)v;
+        if (d1 < dims)
+            *reinterpret_cast<uint16_t*>(to + 2 * d1) = (uint16_t)(v >> 16);
+    }
 }
 
-template <class D>
-__device__ __forceinline__ void store_element(uint8_t* p, float f)
-{
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack2<D>(f, 0.0f);
-}
-
-template <class D, int DP, bool F8>
+template <class D, int DP, bool F8, int NB>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     decode_attention_kernel(AttentionArgs a, Split sp, int tiles)
 {
     using F = Form<D, DP, F8>;
-    constexpr int SL = F::SL, NT = SL / 8, KS = DP / 16, NO = DP / 8;
+    constexpr int SL = F::SL, NK = SL / 16, KS = DP / 16;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ float max_sh[kWarps][kRows], sum_sh[kWarps][kRows];
     __shared__ long long scan_sh[kWarps], where_sh[2];
@@ -342,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         }
     }
 
-    uint32_t q[KS][4];
-    float o[NO][4];
-    float top[2], total_w[2], factor[2];
+    uint32_t q[KS][NB][2];
+    float o[KS][NB][4];
+    float top[NB][2], total_w[NB][2], factor[NB][2];
     bool fresh = true, whole_start = c.unit == 0;
     int stage = 0;
     for (long long u = 0; u < count; ++u) {
@@ -354,34 +376,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (fresh) {
             fresh = false;
             const uint8_t* qp = a.q.p + c.seq * a.q.row + q_head * a.q.head;
-            const uint8_t* q0 = qp + g * a.q.head;
-            const uint8_t* q1 = qp + (g + 8) * a.q.head;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+            for (int n = 0; n < NB; ++n) {
+                const uint8_t* qh = qp + (8 * n + g) * a.q.head;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int d = F8 ? 16 * ks + 4 * t + 2 * half : 16 * ks + 8 * half + 2 * t;
-                    const bool in = (F8 ? 16 * ks : 16 * ks + 8 * half) < a.c.D;
-                    q[ks][2 * half] =
-                        in && g < rows ? *reinterpret_cast<const uint32_t*>(q0 + 2 * d) : 0u;
-                    q[ks][2 * half + 1] =
-                        in && g + 8 < rows ? *reinterpret_cast<const uint32_t*>(q1 + 2 * d) : 0u;
-                }
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = F8 ? 16 * ks + 4 * t + 2 * half : 16 * ks + 8 * half + 2 * t;
+                        const bool in = (F8 ? 16 * ks : 16 * ks + 8 * half) < a.c.D;
+                        q[ks][n][half] = in && 8 * n + g < rows
+                                             ? *reinterpret_cast<const uint32_t*>(qh + 2 * d)
+                                             : 0u;
+                    }
             }
-            factor[0] = factor[1] = a.scale_log2 * k_scale;
-            if constexpr (F8 && D::id == AR_DT_BF16) {
-                // The codes are exact in fp16; bf16 queries are once each row is taken
-                // times a power of two that brings its largest element to 2^14 .. 2^15:
-                // what is below 2^-24 then is 2^-38 of the largest.
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+            for (int n = 0; n < NB; ++n) {
+                float f = a.scale_log2 * k_scale;
+                if constexpr (F8 && D::id == AR_DT_BF16) {
+                    // The codes are exact in fp16; bf16 queries are once each head is taken
+                    // times a power of two that brings its largest element to 2^14 .. 2^15:
+                    // what is below 2^-24 then is 2^-38 of the largest.
                     float big = 0.0f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const float2 f = unpack2<Bf16>(q[ks][2 * half + r]);
-                            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            const float2 x = unpack2<Bf16>(q[ks][n][half]);
+                            big = fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y)));
                         }
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -389,23 +411,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                     const int e = (int)(__float_as_uint(big) >> 23);
                     const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
                     const float by = __uint_as_float((uint32_t)(127 + up) << 23);
-                    factor[r] *= __uint_as_float((uint32_t)(127 - up) << 23);
+                    f *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const float2 f = unpack2<Bf16>(q[ks][2 * half + r]);
-                            q[ks][2 * half + r] = pack2<Fp16>(f.x * by, f.y * by);
+                            const float2 x = unpack2<Bf16>(q[ks][n][half]);
+                            q[ks][n][half] = pack2<Fp16>(x.x * by, x.y * by);
                         }
                 }
+                // of the thread's two columns: head 8 n + 2 t + e is that of lane 4 (2 t + e)
+                factor[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+                factor[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
             }
 #pragma unroll
-            for (int j = 0; j < NO; ++j)
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[j][e] = 0.0f;
-            top[0] = top[1] = -INFINITY;
-            total_w[0] = total_w[1] = 0.0f;
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[j][n][e] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                top[n][0] = top[n][1] = -INFINITY;
+                total_w[n][0] = total_w[n][1] = 0.0f;
+            }
         }
         // the next copies go where the slice before this one was
         copies_wait<kStages - 2>();
@@ -423,122 +453,146 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (x < c.seen.n) {
             const uint32_t kb = ring + stage * 2 * kTile, vb = kb + kTile;
             const int key0 = (x < c.seen.first ? x : x + c.seen.gap) * SL;
-            float s[NT][4];
+            float s[NK][NB][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < NK; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] = 0.0f;
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[k][n][e] = 0.0f;
             if constexpr (F8) {
+                // a 16-byte chunk is 16 elements: 4t and 4t + 1 stand for the product's 2t and 2t + 1, the
+                // next two for 2t + 8 and 2t + 9, in the queries as here
 #pragma unroll
-                for (int ks = 0; ks < KS; ks += 4)
+                for (int ks = 0; ks < KS; ks += 2)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
+                    for (int k = 0; k < NK; ++k) {
                         uint32_t b[4];
-                        ldm4(b, kb + F::at(8 * n + (lane & 7), ks + (lane >> 3)));
+                        ldm4(b, kb + F::at(16 * k + 8 * (lane >> 3 & 1) + (lane & 7), ks + (lane >> 4)));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<false>(s[n], q[ks + i], e4m3_half2(b[i]), e4m3_half2(b[i] >> 16));
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t f[4] = {
+                                e4m3_half2(b[2 * i]), e4m3_half2(b[2 * i + 1]),
+                                e4m3_half2(b[2 * i] >> 16), e4m3_half2(b[2 * i + 1] >> 16)};
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                mma<false>(s[k][n], f, q[ks + i][n][0], q[ks + i][n][1]);
+                        }
                     }
             } else {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t b[4];
-                        ldm4(b, kb + F::at(8 * n + 8 * (lane >> 4) + (lane & 7),
-                                           2 * ks + (lane >> 3 & 1)));
-                        mma<F::bf16>(s[n], q[ks], b[0], b[1]);
-                        mma<F::bf16>(s[n + 1], q[ks], b[2], b[3]);
+                    for (int k = 0; k < NK; ++k) {
+                        uint32_t f[4];
+                        ldm4(f, kb + F::at(16 * k + 8 * (lane >> 3 & 1) + (lane & 7),
+                                           2 * ks + (lane >> 4)));
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma<F::bf16>(s[k][n], f, q[ks][n][0], q[ks][n][1]);
                     }
             }
             // all of the slice's keys seen?
+            const auto sees = [&](int j) {
+                return j < c.seen.length && (j >= c.seen.low || j < c.seen.sinks);
+            };
             const bool all = key0 + SL <= c.seen.length &&
                              (key0 >= c.seen.low || key0 + SL <= c.seen.sinks);
-            uint32_t keep[NT];          // of a pair of keys: which half of a register
+            uint32_t keep[2 * NK];      // of a pair of keys: which half of a register
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                keep[n] = 0xffffffffu;
+            for (int k = 0; k < 2 * NK; ++k) {
+                keep[k] = 0xffffffffu;
+                const bool mine = all || sees(key0 + 8 * k + g);
+                if (!all)
+                    keep[k] = (sees(key0 + 8 * k + 2 * t) ? 0xffffu : 0u) |
+                              (sees(key0 + 8 * k + 2 * t + 1) ? 0xffff0000u : 0u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] *= factor[e >> 1];
-                if (!all) {
-                    const int j = key0 + 8 * n + 2 * t;
-                    const bool k0 = j < c.seen.length && (j >= c.seen.low || j < c.seen.sinks);
-                    const bool k1 = j + 1 < c.seen.length &&
-                                    (j + 1 >= c.seen.low || j + 1 < c.seen.sinks);
-                    keep[n] = (k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u);
-                    if (!k0)
-                        s[n][0] = s[n][2] = -INFINITY;
-                    if (!k1)
-                        s[n][1] = s[n][3] = -INFINITY;
-                }
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float& z = s[k >> 1][n][2 * (k & 1) + e];
+                        z = mine ? z * factor[n][e] : -INFINITY;
+                    }
             }
-            float used[2], now[2];
+            float used[NB][2], now[NB][2];
             bool moved = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float m = top[r];
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    m = fmaxf(m, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                now[r] = m;
-                used[r] = m == -INFINITY ? 0.0f : m;    // a row that has seen nothing yet
-                moved |= m != top[r];
-            }
+                for (int e = 0; e < 2; ++e) {
+                    float m = top[n][e];
+#pragma unroll
+                    for (int k = 0; k < NK; ++k)
+                        m = fmaxf(m, fmaxf(s[k][n][e], s[k][n][2 + e]));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    now[n][e] = m;
+                    used[n][e] = m == -INFINITY ? 0.0f : m;     // a head that has seen nothing yet
+                    moved |= m != top[n][e];
+                }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float f = exp2_fast(top[r] - used[r]);
-                    total_w[r] *= f;
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int j = 0; j < NO; ++j) {
-                        o[j][2 * r] *= f;
-                        o[j][2 * r + 1] *= f;
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = exp2_fast(top[n][e] - used[n][e]);
+                        total_w[n][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < KS; ++j) {
+                            o[j][n][e] *= f;
+                            o[j][n][2 + e] *= f;
+                        }
+                        top[n][e] = now[n][e];
                     }
-                    top[r] = now[r];
-                }
             }
+            uint32_t p[NK][NB][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < NK; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[n][e] = exp2_fast(s[n][e] - used[e >> 1]);
-                    total_w[e >> 1] += s[n][e];
+                for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[k][n][e] = exp2_fast(s[k][n][e] - used[n][e & 1]);
+                        total_w[n][e & 1] += s[k][n][e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        p[k][n][i] = turned(F::bf16 ? pack2<Bf16>(s[k][n][2 * i], s[k][n][2 * i + 1])
+                                                    : pack2<Fp16>(s[k][n][2 * i], s[k][n][2 * i + 1]));
                 }
 #pragma unroll
-            for (int kk = 0; kk < NT; kk += 2) {
-                uint32_t p[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float* f = &s[kk + (i >> 1)][2 * (i & 1)];
-                    p[i] = F::bf16 ? pack2<Bf16>(f[0], f[1]) : pack2<Fp16>(f[0], f[1]);
-                }
+            for (int k = 0; k < NK; ++k) {
+                const uint32_t keep0 = keep[2 * k], keep1 = keep[2 * k + 1];
                 if constexpr (F8) {
 #pragma unroll
-                    for (int j = 0; j < DP / 16; j += 2) {
+                    for (int j = 0; j < KS; j += 2) {
                         uint32_t b[4];
-                        ldm4_trans(b, vb + F::at(8 * kk + 8 * (lane >> 3 & 1) + (lane & 7),
+                        ldm4_trans(b, vb + F::at(16 * k + 8 * (lane >> 3 & 1) + (lane & 7),
                                                  j + (lane >> 4)));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t b0 = b[2 * i] & keep[kk], b1 = b[2 * i + 1] & keep[kk + 1];
-                            mma<false>(o[2 * (j + i)], p, e4m3_half2(__byte_perm(b0, 0, 0x4420)),
-                                       e4m3_half2(__byte_perm(b1, 0, 0x4420)));
-                            mma<false>(o[2 * (j + i) + 1], p, e4m3_half2(__byte_perm(b0, 0, 0x4431)),
-                                       e4m3_half2(__byte_perm(b1, 0, 0x4431)));
+                            const uint32_t b0 = b[2 * i] & keep0, b1 = b[2 * i + 1] & keep1;
+                            const uint32_t f[4] = {e4m3_half2(__byte_perm(b0, 0, 0x4420)),
+                                                   e4m3_half2(__byte_perm(b0, 0, 0x4431)),
+                                                   e4m3_half2(__byte_perm(b1, 0, 0x4420)),
+                                                   e4m3_half2(__byte_perm(b1, 0, 0x4431))};
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                mma<false>(o[j + i][n], f, p[k][n][0], p[k][n][1]);
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < NO; j += 2) {
+                    for (int j = 0; j < KS; ++j) {
                         uint32_t b[4];
-                        ldm4_trans(b, vb + F::at(8 * kk + 8 * (lane >> 3 & 1) + (lane & 7),
-                                                 j + (lane >> 4)));
-                        mma<F::bf16>(o[j], p, b[0] & keep[kk], b[1] & keep[kk + 1]);
-                        mma<F::bf16>(o[j + 1], p, b[2] & keep[kk], b[3] & keep[kk + 1]);
+                        ldm4_trans(b, vb + F::at(16 * k + 8 * (lane >> 4) + (lane & 7),
+                                                 2 * j + (lane >> 3 & 1)));
+                        const uint32_t f[4] = {b[0] & keep0, b[1] & keep0, b[2] & keep1, b[3] & keep1};
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma<F::bf16>(o[j][n], f, p[k][n][0], p[k][n][1]);
                     }
                 }
             }
@@ -549,49 +603,61 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (item_ends || u + 1 == count) {
             // the four warps' sums together
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                total_w[r] += __shfl_xor_sync(0xffffffffu, total_w[r], 1);
-                total_w[r] += __shfl_xor_sync(0xffffffffu, total_w[r], 2);
-                if (t == 0) {
-                    max_sh[warp][g + 8 * r] = top[r];
-                    sum_sh[warp][g + 8 * r] = total_w[r];
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float& l = total_w[n][e];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    if (g == 0) {
+                        max_sh[warp][head_of(n, e, t)] = top[n][e];
+                        sum_sh[warp][head_of(n, e, t)] = l;
+                    }
                 }
-            }
             __syncthreads();
-            float best[2], sum[2];
+            float best[NB][2], sum[NB][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                best[r] = -INFINITY;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    best[r] = fmaxf(best[r], max_sh[w][g + 8 * r]);
-                const float base = best[r] == -INFINITY ? 0.0f : best[r];
-                sum[r] = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    const int h = head_of(n, e, t);
+                    float m = -INFINITY, l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    sum[r] += sum_sh[w][g + 8 * r] * exp2_fast(max_sh[w][g + 8 * r] - base);
-                const float f = exp2_fast(top[r] - base);
+                    for (int w = 0; w < kWarps; ++w)
+                        m = fmaxf(m, max_sh[w][h]);
+                    const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    o[j][2 * r] *= f;
-                    o[j][2 * r + 1] *= f;
+                    for (int w = 0; w < kWarps; ++w)
+                        l += sum_sh[w][h] * exp2_fast(max_sh[w][h] - base);
+                    best[n][e] = m;
+                    sum[n][e] = l;
+                    const float f = exp2_fast(top[n][e] - base);
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        o[j][n][e] *= f;
+                        o[j][n][2 + e] *= f;
+                    }
                 }
-            }
             const auto put = [&](float* to) {
 #pragma unroll
-                for (int j = 0; j < NO; ++j)
+                for (int j = 0; j < KS; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        to[(4 * j + e) * 32 + lane] = o[j][e];
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            to[((j * NB + n) * 4 + e) * 32 + lane] = o[j][n][e];
             };
             const auto add = [&](const float* from) {
 #pragma unroll
-                for (int j = 0; j < NO; ++j)
+                for (int j = 0; j < KS; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[j][e] += from[(4 * j + e) * 32 + lane];
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[j][n][e] += from[((j * NB + n) * 4 + e) * 32 + lane];
             };
-            constexpr int kBuf = kRows * DP;
+            constexpr int kBuf = 8 * NB * DP;
             if (warp >= 2)
                 put(sums + (warp - 2) * kBuf);
             __syncthreads();
@@ -604,39 +670,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 add(sums + kBuf);
                 if (item_ends && whole_start) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int row = g + 8 * r;
-                        if (row >= rows)
-                            continue;
-                        const float inv = sum[r] > 0.0f || sum[r] != sum[r] ? v_scale / sum[r] : 0.0f;
-                        uint8_t* to = a.out.p + c.seq * a.out.row + (q_head + row) * a.out.head;
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int j = 0; j < NO; ++j) {
-                            const int d0 = dim_of<F8>(j, 0, t), d1 = dim_of<F8>(j, 1, t);
-                            if (d0 >= a.c.D)
+                        for (int e = 0; e < 2; ++e) {
+                            const int h = head_of(n, e, t);
+                            if (h >= rows)
                                 continue;
-                            const float f0 = o[j][2 * r] * inv, f1 = o[j][2 * r + 1] * inv;
-                            if constexpr (F8) {
-                                store_element<D>(to + 2 * d0, f0);
-                                store_element<D>(to + 2 * d1, f1);
-                            } else {
-                                *reinterpret_cast<uint32_t*>(to + 2 * d0) = pack2<D>(f0, f1);
-                            }
+                            const float l = sum[n][e], inv = l > 0.0f || l != l ? v_scale / l : 0.0f;
+                            uint8_t* to = a.out.p + c.seq * a.out.row + (q_head + h) * a.out.head;
+#pragma unroll
+                            for (int j = 0; j < KS; ++j)
+                                store_dims<D, F8>(to, a.c.D, j, g, o[j][n][e] * inv, o[j][n][2 + e] * inv);
+                            if (a.lse && g == 0)
+                                a.lse[(int64_t)c.seq * a.Hq + q_head + h] = (best[n][e] + log2f(l)) * kLn2;
                         }
-                        if (a.lse && t == 0)
-                            a.lse[(int64_t)c.seq * a.Hq + q_head + row] =
-                                (best[r] + log2f(sum[r])) * kLn2;
-                    }
                 } else {
                     // a piece that begins here is part 1, one that began before part 0
                     uint8_t* to = sp.parts + (int64_t)(2 * block + (whole_start ? 1 : 0)) * part_bytes<DP>();
                     float* stats = reinterpret_cast<float*>(to);
-                    if (t == 0) {
+                    if (g == 0) {
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            stats[g + 8 * r] = best[r];
-                            stats[kRows + g + 8 * r] = sum[r];
-                        }
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                stats[head_of(n, e, t)] = best[n][e];
+                                stats[kRows + head_of(n, e, t)] = sum[n][e];
+                            }
                     }
                     put(stats + 2 * kRows);
                     if (whole_start && lane == 0) {
@@ -654,96 +713,73 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
 }
 
-// Items that several blocks share.  Block (b, y): the item that begins in block b and
-// ends in a later one, a quarter of its elements; a warp has a few registers of the
-// fragments, each lane one row of them.
-constexpr int kJoinThreads = 256, kJoinY = 4, kJoinParts = 32;
+// Items that several blocks share.  Block (b, y): the item that begins in block b and ends in a
+// later one, a part of its elements; a thread has two elements of a head, and all of its loads
+// of kJoinAhead parts in flight.
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
 
-template <class D, int DP, bool F8>
+template <class D, int DP, bool F8, int NB>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Split sp, int tiles)
 {
-    constexpr int kEach = DP / 2 / (kJoinY * kJoinThreads / 32);      // registers of a warp: 2 or 1
-    __shared__ float weight[kJoinParts][kRows], max_sh[kRows], sum_sh[kRows];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_trigger();
     pdl_wait();
     const int4 d = sp.desc[blockIdx.x];
     if (d.x == 0)
         return;
-    const auto part = [&](int p) {
-        const int slot = p == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + p);
-        return reinterpret_cast<const float*>(sp.parts + (int64_t)slot * part_bytes<DP>());
-    };
-    // maximum and total of each row, 16 threads a row
-    {
-        const int row = tid >> 4, i = tid & 15;
-        float m = -INFINITY, l = 0.0f;
-        for (int p = i; p < d.x; p += 16) {
-            const float* s = part(p);
-            const float pm = s[row], pl = s[kRows + row];
-            const float top = fmaxf(m, pm), base = top == -INFINITY ? 0.0f : top;
-            l = l * exp2_fast(m - base) + pl * exp2_fast(pm - base);
-            m = top;
-        }
+    // registers (j, n, e) and (j, n, e + 2)
+    const int which = blockIdx.y * (kJoinThreads / 32) + (tid >> 5);
+    const int e = which & 1, n = (which >> 1) % NB, j = (which >> 1) / NB;
+    const int h = head_of(n, e, t), at = ((j * NB + n) * 4 + e) * 32 + lane;
+    float m = -INFINITY, l = 0.0f, f0 = 0.0f, f1 = 0.0f;
+    for (int p0 = 0; p0 < d.x; p0 += kJoinAhead) {
+        float pm[kJoinAhead], pl[kJoinAhead], v0[kJoinAhead], v1[kJoinAhead];
 #pragma unroll
-        for (int k = 1; k < 16; k <<= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, k), ol = __shfl_xor_sync(0xffffffffu, l, k);
-            const float top = fmaxf(m, om), base = top == -INFINITY ? 0.0f : top;
-            l = l * exp2_fast(m - base) + ol * exp2_fast(om - base);
-            m = top;
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const int p = p0 + i;
+            const int slot = p == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + p);
+            const float* s = reinterpret_cast<const float*>(sp.parts + (int64_t)slot * part_bytes<DP>());
+            pm[i] = p < d.x ? s[h] : -INFINITY;
+            pl[i] = p < d.x ? s[kRows + h] : 0.0f;
+            v0[i] = p < d.x ? s[2 * kRows + at] : 0.0f;
+            v1[i] = p < d.x ? s[2 * kRows + at + 64] : 0.0f;
         }
-        if (i == 0) {
-            max_sh[row] = m;
-            sum_sh[row] = l;
-        }
-    }
-    const int first = (blockIdx.y * (kJoinThreads / 32) + warp) * kEach;     // register 4 j + e
-    const int row = (lane >> 2) + 8 * (first >> 1 & 1), t = lane & 3;
-    float acc[kEach];
+        float top = m;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-        acc[i] = 0.0f;
-    for (int p0 = 0; p0 < d.x; p0 += kJoinParts) {
-        __syncthreads();
-        for (int i = tid; i < kJoinParts * kRows; i += kJoinThreads) {
-            const int p = p0 + i / kRows, r = i % kRows;
-            const float base = max_sh[r] == -INFINITY ? 0.0f : max_sh[r];
-            weight[i / kRows][r] = p < d.x ? exp2_fast(part(p)[r] - base) : 0.0f;
-        }
-        __syncthreads();
-        const int n = min(kJoinParts, d.x - p0);
-#pragma unroll 8
-        for (int p = 0; p < n; ++p) {
-            const float* s = part(p0 + p) + 2 * kRows + first * 32 + lane;
+        for (int i = 0; i < kJoinAhead; ++i)
+            top = fmaxf(top, pm[i]);
+        const float base = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - base);
+        l *= f;
+        f0 *= f;
+        f1 *= f;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                acc[i] = fmaf(s[32 * i], weight[p][row], acc[i]);
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const float w = exp2_fast(pm[i] - base);
+            l = fmaf(pl[i], w, l);
+            f0 = fmaf(v0[i], w, f0);
+            f1 = fmaf(v1[i], w, f1);
         }
+        m = top;
     }
     const int head = d.z / tiles, tile = d.z - head * tiles;
-    if (row >= min(kRows, a.G - tile * kRows))
+    if (h >= min(kRows, a.G - tile * kRows))
         return;
-    const int q_head = head * a.G + tile * kRows + row;
-    const float sum = sum_sh[row], v_scale = F8 && a.c.scale ? a.c.scale[1] : 1.0f;
-    const float inv = sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;
+    const int q_head = head * a.G + tile * kRows + h;
+    const float v_scale = F8 && a.c.scale ? a.c.scale[1] : 1.0f;
+    const float inv = l > 0.0f || l != l ? v_scale / l : 0.0f;
     uint8_t* to = a.out.p + d.y * a.out.row + q_head * a.out.head;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int at = dim_of<F8>((first + i) >> 2, (first + i) & 3, t);
-        if (at < a.c.D)
-            store_element<D>(to + 2 * at, acc[i] * inv);
-    }
-    if (a.lse && t == 0 && (first & ~3) == 0 && (first & 1) == 0)
-        a.lse[(int64_t)d.y * a.Hq + q_head] = (max_sh[row] + log2f(sum)) * kLn2;
+    store_dims<D, F8>(to, a.c.D, j, g, f0 * inv, f1 * inv);
+    if (a.lse && g == 0 && j == 0)
+        a.lse[(int64_t)d.y * a.Hq + q_head] = (m + log2f(l)) * kLn2;
 }
 
-template <class D, int DP, bool F8>
+template <class D, int DP, bool F8, int NB>
 cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
     constexpr int kSmem = kWarps * kStages * 2 * kTile + 2 * kRows * DP * 4;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(decode_attention_kernel<D, DP, F8>,
+        return cudaFuncSetAttribute(decode_attention_kernel<D, DP, F8, NB>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e != cudaSuccess)
@@ -766,16 +802,19 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         sp.desc = reinterpret_cast<int4*>(a.work);
         sp.parts = a.work + 16 * (int64_t)blocks;
     }
-    e = launch_after(decode_attention_kernel<D, DP, F8>, blocks, kThreads, kSmem, s, a, sp, tiles);
+    e = launch_after(decode_attention_kernel<D, DP, F8, NB>, blocks, kThreads, kSmem, s, a, sp, tiles);
     if (e != cudaSuccess || sp.whole || blocks == 1)
         return e;
-    return launch_after(join_kernel<D, DP, F8>, dim3(blocks, kJoinY), kJoinThreads, 0, s, a, sp, tiles);
+    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)), kJoinThreads, 0, s, a, sp, tiles);
 }
 
 template <class D, bool F8>
 cudaError_t launch_d(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
-    return a.c.D <= 64 ? launch_t<D, 64, F8>(a, d, s) : launch_t<D, 128, F8>(a, d, s);
+    // heads in one or two groups of 8 columns
+    if (a.c.D <= 64)
+        return a.G <= 8 ? launch_t<D, 64, F8, 1>(a, d, s) : launch_t<D, 64, F8, 2>(a, d, s);
+    return a.G <= 8 ? launch_t<D, 128, F8, 1>(a, d, s) : launch_t<D, 128, F8, 2>(a, d, s);
 }
 
 }  // namespace
