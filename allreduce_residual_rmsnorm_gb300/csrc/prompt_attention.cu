@@ -11,7 +11,8 @@
 //
 //   tensor memory: scores of tile 0, of tile 1, sums of tile 0, of tile 1, 128 columns each
 //   warps 0-3, 4-7: softmax and output of tile 0, 1;  warp 8: copies;  warp 9: products;
-//   warp 10: clears values that no row sees (what lies there need not be finite)
+//   warp 10: clears values that no row sees (what lies there need not be finite);
+//   warp 11: finds the items ahead of the others (each for itself took 1.5 us an item)
 //
 // Items (a pair of tiles and a head) are worked off by one block per SM: where there
 // are many, whole ones, the longest first; where there are few, the key tiles of all items
@@ -38,14 +39,14 @@ constexpr float kLn2 = 0.693147181f;
 template <class D>
 __device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16 ? 32.0f : 14.0f; }
 enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
-       kWaitCleared };
+       kWaitCleared, kWaitItem, kWaitPlace };
 
 template <int DP>
 struct Shape {
     static constexpr int half = kRows * 128;        // bytes of 128 rows of 64 elements
     static constexpr int tile = half * (DP / 64);
     static constexpr int stages = DP == 64 ? 8 : 4;
-    static constexpr int smem = (2 + stages) * tile + 3 * (AR_MAX_SEQUENCES + 1) * 4 + 1024;
+    static constexpr int smem = (2 + stages) * tile + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
     static constexpr int part = 2 * kRows * (DP + 2) * 4;
 };
 // More than half of an SM's shared memory for every shape: no second block of this kernel
@@ -74,33 +75,31 @@ __device__ __forceinline__ bool has_unseen(const Pair& p, int key0)
 }
 __device__ __forceinline__ int tile_of(const Pair& p, int x) { return x < p.first ? x : x + p.gap; }
 
-// In shared memory, [sequences (+ 1)]: pairs before each sequence, starts, lengths.
-struct Table {
-    int *first_pair, *starts, *lengths;
-};
-
-__device__ __forceinline__ int rows_of(const AttentionArgs& a, const Table& tab, int s)
+// tokens of a sequence in the call
+__device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
 {
-    const int r0 = tab.starts[s], r1 = tab.starts[s + 1];
+    const int r0 = a.starts[s], r1 = a.starts[s + 1];
+    *row0 = r0;
     return r0 >= 0 && r1 <= a.T && r1 > r0 ? r1 - r0 : 0;
 }
 
 // pair f of all: sequences in order, in each the last tokens first
-__device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const Table& tab, int f)
+__device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const int* first_pair, int f)
 {
     int lo = 0, hi = a.c.S;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tab.first_pair[mid] <= f)
+        if (first_pair[mid] <= f)
             lo = mid;
         else
             hi = mid;
     }
     Pair p;
     p.seq = lo;
-    const int n = rows_of(a, tab, lo), length = tab.lengths[lo];
-    const int t0 = (tab.first_pair[lo + 1] - 1 - f) * 2 * tok;
-    p.row0 = tab.starts[lo] + t0;
+    const int n = rows_of(a, lo, &p.row0);
+    const int length = clamp_length(a.c, a.c.lengths[lo]);
+    const int t0 = (first_pair[lo + 1] - 1 - f) * 2 * tok;
+    p.row0 += t0;
     p.tokens = min(2 * tok, n - t0);
     p.i0 = length - n + t0;
     p.end = max(p.i0 + p.tokens, 0);
@@ -112,14 +111,25 @@ __device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const T
     return p;
 }
 
-// The items of a block, one after the other: key tiles x0 .. x1 - 1 of a pair for a head.
+// What a block does next: key tiles x0 .. x1 - 1 of a pair for a head (none: nothing left);
+// where the item begins here and ends in another block, that block.
+struct Item {
+    Pair p;
+    int head, x0, x1, end_block, pad[2];
+};
+static_assert(sizeof(Item) == 64, "copied as four vectors");
+constexpr uint32_t kItems = 4;                      // found ahead
+constexpr int kTakers = 11;                         // warps 0-10
+
+// The items of a block, one after the other.
 struct Walk {
     int item, items, x, step;   // whole items: `step` counts them
     long long left;             // of a share: units left
-    Pair p;
-    int head, x0, x1;
+    long long end, total;       // of a share: where it ends in the list, and the list
+    int blocks;
 
-    __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const Table& tab)
+    __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const int* first_pair,
+                                         Item* to)
     {
         for (;;) {
             if (plan.whole) {
@@ -138,16 +148,19 @@ struct Walk {
                     return false;
             }
             const int f = item / a.c.heads;
-            head = item - f * a.c.heads;
-            p = pair_at(a, plan.tok, tab, f);
-            x0 = x;
-            x1 = plan.whole ? p.n : (int)min((long long)p.n, x0 + left);
+            to->head = item - f * a.c.heads;
+            to->p = pair_at(a, plan.tok, first_pair, f);
+            to->x0 = x;
+            to->x1 = plan.whole ? to->p.n : (int)min((long long)to->p.n, x + left);
+            to->end_block = 0;
             if (!plan.whole) {
-                left -= x1 - x0;
+                left -= to->x1 - x;
                 ++item;
                 x = 0;
+                if (to->x1 < to->p.n)       // the block that has the item's last unit
+                    to->end_block = (int)(((end + (to->p.n - to->x1)) * blocks - 1) / total);
             }
-            if (x1 > x0)
+            if (to->x1 > to->x0)
                 return true;
         }
     }
@@ -188,19 +201,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     using F = Shape<DP>;
     constexpr uint32_t kStages = F::stages;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 6 + 1];
+    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 6 + 1 + 2 * kItems];
+    __shared__ __align__(16) Item item_sh[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, begin_sh[2];
     __shared__ long long scan_sh[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t q_at = (smem_u32(dyn) + 1023u) & ~1023u, ring = q_at + 2 * F::tile;
-    Table tab;
-    tab.first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
-    tab.starts = tab.first_pair + AR_MAX_SEQUENCES + 1;
-    tab.lengths = tab.starts + AR_MAX_SEQUENCES + 1;
+    int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
                    wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
-                   pfull = sfull + 16, ofull = pfull + 32, done = ofull + 16;
+                   pfull = sfull + 16, ofull = pfull + 32, done = ofull + 16,
+                   ifull = done + 8, iempty = ifull + 8 * kItems;
     const Bail bail{smem_u32(&dead), status};
 
     if (tid == 0) {
@@ -220,6 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(ofull + 8 * t, 1);
         }
         bar_init(done, 1);
+        for (uint32_t i = 0; i < kItems; ++i) {
+            bar_init(ifull + 8 * i, 1);
+            bar_init(iempty + 8 * i, kTakers);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch_map(&map_q);
         tma_prefetch_map(&map_k);
@@ -235,45 +251,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     const uint32_t tmem = tmem_slot;
 
-    // pairs before each sequence
-    for (int s = tid; s <= a.c.S; s += kThreads) {
-        tab.starts[s] = a.starts[s];
-        if (s < a.c.S)
-            tab.lengths[s] = clamp_length(a.c, a.c.lengths[s]);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int before = 0;
-        for (int s0 = 0; s0 < a.c.S; s0 += 32) {
-            int n = 0;
-            if (s0 + lane < a.c.S)
-                n = (rows_of(a, tab, s0 + lane) + 2 * plan.tok - 1) / (2 * plan.tok);
-            int upto = n;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, m);
-                upto += lane >= m ? v : 0;
-            }
-            if (s0 + lane < a.c.S)
-                tab.first_pair[s0 + lane] = before + upto - n;
-            before += __shfl_sync(0xffffffffu, upto, 31);
+    // pairs before each sequence; whether any has rows without a place
+    int before = 0;
+    bool short_one = false;
+    for (int s0 = 0; s0 < a.c.S; s0 += kThreads) {
+        int n = 0, row0;
+        if (s0 + tid < a.c.S) {
+            n = rows_of(a, s0 + tid, &row0);
+            short_one |= clamp_length(a.c, a.c.lengths[s0 + tid]) < n;
+            n = (n + 2 * plan.tok - 1) / (2 * plan.tok);
         }
-        if (lane == 0)
-            tab.first_pair[a.c.S] = before;
+        int upto = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, m);
+            upto += lane >= m ? v : 0;
+        }
+        if (lane == 31)
+            scan_sh[warp] = upto;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            upto += w < warp ? (int)scan_sh[w] : 0;
+            all += (int)scan_sh[w];
+        }
+        if (s0 + tid < a.c.S)
+            first_pair[s0 + tid] = before + upto - n;
+        before += all;
+        __syncthreads();
     }
-    __syncthreads();
-    const int pairs = tab.first_pair[a.c.S];
+    const int pairs = before;
+    if (tid == 0)
+        first_pair[a.c.S] = pairs;
+    short_one = __syncthreads_or(short_one);
 
-    Walk start{0, pairs * a.c.heads, 0, 0, 0, {}, 0, 0, 0};
-    long long total = 0, u0 = 0;
-    int blocks = gridDim.x;
+    Walk walk{0, pairs * a.c.heads, 0, 0, 0, 0, 1, (int)gridDim.x};
     if (!plan.whole) {
         // this block's share of the list of key tiles, and where it begins
         const int per = (pairs + kThreads - 1) / kThreads;
         const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
         long long mine = 0;
-        for (int f = f0; f < f1; ++f)
-            mine += (long long)pair_at(a, plan.tok, tab, f).n * a.c.heads;
+        int n0 = 0;
+        for (int f = f0; f < f1; ++f) {
+            n0 = pair_at(a, plan.tok, first_pair, f).n;
+            mine += (long long)n0 * a.c.heads;
+        }
         long long upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -283,21 +306,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31)
             scan_sh[warp] = upto;
         __syncthreads();
+        long long total = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             upto += w < warp ? scan_sh[w] : 0;
             total += scan_sh[w];
         }
         // no more blocks than units: an item's blocks are then consecutive ones
-        blocks = (int)min((long long)blocks, max(total, 1ll));
+        const int blocks = (int)min((long long)gridDim.x, max(total, 1ll));
+        long long u0 = 0;
+        walk.total = total;
+        walk.blocks = blocks;
         if ((int)blockIdx.x < blocks) {
-            u0 = total * blockIdx.x / blocks;
-            start.left = total * (blockIdx.x + 1) / blocks - u0;
+            if (total < 1 << 22) {          // the products fit 32 bits
+                u0 = (unsigned)total * blockIdx.x / (unsigned)blocks;
+                walk.end = (unsigned)total * (blockIdx.x + 1) / (unsigned)blocks;
+            } else {
+                u0 = total * blockIdx.x / blocks;
+                walk.end = total * (blockIdx.x + 1) / blocks;
+            }
+            walk.left = walk.end - u0;
         }
         long long at = upto - mine;
-        if (start.left && u0 >= at && u0 < upto) {
+        if (walk.left && u0 >= at && u0 < upto) {
             for (int f = f0; f < f1; ++f) {
-                const int n = pair_at(a, plan.tok, tab, f).n;
+                const int n = per == 1 ? n0 : pair_at(a, plan.tok, first_pair, f).n;
                 const long long end = at + (long long)n * a.c.heads;
                 if (u0 < end) {
                     const int in = (int)(u0 - at);
@@ -311,12 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0)
             plan.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        start.item = begin_sh[0];
-        start.x = begin_sh[1];
+        walk.item = begin_sh[0];
+        walk.x = begin_sh[1];
     }
     // rows that see nothing, where that holds for a whole pair
-    for (int f = blockIdx.x; f < pairs; f += (int)gridDim.x) {
-        const Pair p = pair_at(a, plan.tok, tab, f);
+    for (int f = short_one ? (int)blockIdx.x : pairs; f < pairs; f += (int)gridDim.x) {
+        const Pair p = pair_at(a, plan.tok, first_pair, f);
         if (p.n > 0)
             continue;
         for (int i = tid; i < p.tokens * a.Hq; i += kThreads) {
@@ -329,16 +362,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    Walk w = start;
+    // The next item, by every lane of a warp or by one thread; false: none is left, or a wait gave up.
+    Item w;
+    uint32_t taken = 0;
+    bool ok = true;
+    const auto take = [&](bool whole_warp) {
+        const uint32_t i = taken % kItems;
+        ok = bar_wait(ifull + 8 * i, taken / kItems & 1, bail, kWaitItem);
+        if (whole_warp)
+            ok = __all_sync(0xffffffffu, ok);
+        if (!ok)
+            return false;
+        w = item_sh[i];
+        if (whole_warp)
+            __syncwarp();
+        if (!whole_warp || lane == 0)
+            bar_arrive(iempty + 8 * i);
+        ++taken;
+        return w.x1 > w.x0;
+    };
     if (warp >= 8) {
         regs_fewer<kRegsFew>();
         if (warp == 8) {
             // copies: per item the queries, then keys and values of a tile in turn
             uint32_t it = 0, uses[2] = {0, 0};
-            bool ok = true;
             const int page_rows = min(1 << a.c.page_shift, kKeys), boxes = kKeys / page_rows;
             const int box = lane % boxes, part = lane / boxes;      // part: which 64 elements
-            while (ok && w.next(a, plan, tab)) {
+            while (ok && take(true)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x) {
                     const int key = tile_of(w.p, x) * kKeys + box * page_rows;
                     int page = -1;
@@ -414,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t id_s = half_idesc(kRows, kKeys, bf16, false);
                 constexpr uint32_t id_o = half_idesc(kRows, DP, bf16, true);
                 uint32_t it = 0, uses[2] = {0, 0}, weights[2] = {0, 0}, clears = 0;
-                bool ok = true;
                 const auto scores = [&](int t, uint32_t s) {
                     const uint64_t q = smem_desc(q_at + t * F::tile), k = smem_desc(ring + s * F::tile);
 #pragma unroll
@@ -424,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(sfull + 8 * t);
                 };
-                while (ok && w.next(a, plan, tab)) {
+                while (ok && take(false)) {
                     const int tiles = w.p.tokens > plan.tok ? 2 : 1;
                     if (!(ok = bar_wait(full + 8 * (it % kStages), it / kStages & 1, bail, kWaitKeys)))
                         break;
@@ -497,8 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // then the stage's fill before this one is over, so that the wait for the fill is not
             // answered by an older one.
             uint32_t it = 0, asked = 0;
-            bool ok = true;
-            while (ok && w.next(a, plan, tab)) {
+            while (ok && take(true)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x, it += 2) {
                     const int key0 = tile_of(w.p, x) * kKeys;
                     if (!has_unseen(w.p, key0))
@@ -527,6 +575,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bar_arrive(cleared + 8 * s);
                 }
             }
+        } else if (lane == 0) {
+            // the items, and one without tiles behind the last
+            for (uint32_t i = 0; ok; ++i) {
+                if (!(ok = bar_wait(iempty + 8 * (i % kItems), (i / kItems & 1) ^ 1, bail, kWaitPlace)))
+                    break;
+                Item next;
+                const bool more = walk.next(a, plan, first_pair, &next);
+                if (!more)
+                    next.x0 = next.x1 = 0;
+                item_sh[i % kItems] = next;
+                bar_arrive(ifull + 8 * (i % kItems));
+                if (!more)
+                    break;
+            }
+            __syncwarp(1u);
         }
     } else {
         regs_more<kRegsMany>();
@@ -537,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
         const int in = r / a.G, g = r - in * a.G;       // token of the tile, head of the group
         uint32_t seen = 0, items = 0;
-        while (w.next(a, plan, tab)) {
+        while (take(true)) {
             const int tok0 = t * plan.tok;
             if (tok0 >= w.p.tokens)
                 continue;
@@ -684,23 +747,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 to[0] = top;
                 to[2 * kRows] = total_w;
                 to += 4 * kRows;
+                // a warp whose rows are of no token has nothing to say
+                if (__any_sync(0xffffffffu, live)) {
+                    uint32_t o[DP];
 #pragma unroll
-                for (int c = 0; c < DP; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_at + c, o);
-                    tmem_wait(o);
+                    for (int c = 0; c < DP; c += 32)
+                        tmem_ld32(o_at + c, o + c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        to[(c + e) * 2 * kRows] = __uint_as_float(o[e]);
+                    for (int c = 0; c < DP; c += 32)
+                        tmem_wait32(o + c);
+#pragma unroll
+                    for (int c = 0; c < DP; ++c)
+                        to[c * 2 * kRows] = __uint_as_float(o[c]);
                 }
-                if (which && tid == 0) {
-                    // the block that has the item's last unit
-                    const long long used_units = total * (blockIdx.x + 1) / blocks;
-                    const long long lastu = used_units + (w.p.n - w.x1) - 1;
-                    const int end = (int)(((lastu + 1) * blocks - 1) / total);
-                    plan.desc[blockIdx.x] =
-                        make_int4(end - (int)blockIdx.x + 1, w.p.row0, w.p.tokens, w.head);
-                }
+                if (which && tid == 0)
+                    plan.desc[blockIdx.x] = make_int4(w.end_block - (int)blockIdx.x + 1, w.p.row0,
+                                                      w.p.tokens, w.head);
             }
         }
         __syncwarp();
@@ -712,57 +774,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_free(tmem, 512);
 }
 
-// Items that several blocks share.  Block (b, y): the item that begins in block b, 16 of its
-// elements; a thread has a row.
+// Items that several blocks share.  Block (b, y): the item that begins in block b, 8 of its
+// elements; a thread has a row, and all of its loads of kJoinAhead parts in flight.
+constexpr int kJoinAhead = 4, kJoinDims = 8;
+
 template <class D, int DP>
 __global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan plan)
 {
-    constexpr int kEach = 16;
     pdl_trigger();
     pdl_wait();
     const int4 d = plan.desc[blockIdx.x];
     const int r = threadIdx.x, in = r % kRows / a.G, g = r % kRows - in * a.G;
-    const int token = r / kRows * plan.tok + in;
-    if (d.x == 0 || in >= plan.tok || token >= d.z)
+    const int token = r / kRows * plan.tok + in, d0 = blockIdx.y * kJoinDims;
+    if (d.x == 0 || in >= plan.tok || token >= d.z || d0 >= a.c.D)
         return;
-    const auto part = [&](int p) {
-        const int slot = p == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + p);
-        return reinterpret_cast<const float*>(plan.parts + (int64_t)slot * Shape<DP>::part) + r;
-    };
-    float top = -INFINITY;
-#pragma unroll 8
-    for (int p = 0; p < d.x; ++p)       // all of their loads in flight
-        top = fmaxf(top, part(p)[0]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc[kEach];
+    float m = -INFINITY, l = 0.0f, acc[kJoinDims];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e)
+    for (int e = 0; e < kJoinDims; ++e)
         acc[e] = 0.0f;
-    const int d0 = blockIdx.y * kEach;
-#pragma unroll 4
-    for (int p = 0; p < d.x; ++p) {
-        const float* s = part(p);
-        const float f = exp2_fast(s[0] - base);
-        sum = fmaf(s[2 * kRows], f, sum);
+    for (int p0 = 0; p0 < d.x; p0 += kJoinAhead) {
+        float pm[kJoinAhead], pl[kJoinAhead], v[kJoinAhead][kJoinDims];
 #pragma unroll
-        for (int e = 0; e < kEach; ++e)
-            acc[e] = fmaf(s[(2 + d0 + e) * 2 * kRows], f, acc[e]);
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const int p = p0 + i;
+            const int slot = p == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + p);
+            const float* s =
+                reinterpret_cast<const float*>(plan.parts + (int64_t)slot * Shape<DP>::part) + r;
+            pm[i] = p < d.x ? s[0] : -INFINITY;
+            pl[i] = p < d.x ? s[2 * kRows] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kJoinDims; ++e)
+                v[i][e] = p < d.x ? s[(2 + d0 + e) * 2 * kRows] : 0.0f;
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            top = fmaxf(top, pm[i]);
+        const float base = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - base);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < kJoinDims; ++e)
+            acc[e] *= f;
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const float wt = exp2_fast(pm[i] - base);
+            l = fmaf(pl[i], wt, l);
+#pragma unroll
+            for (int e = 0; e < kJoinDims; ++e)
+                acc[e] = fmaf(v[i][e], wt, acc[e]);
+        }
+        m = top;
     }
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const int row = d.y + token, h = d.w * a.G + g;
-    uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
 #pragma unroll
-    for (int e = 0; e < kEach; e += 8) {
-        if (d0 + e >= a.c.D)
-            continue;
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = acc[e + k] * inv;
-        *reinterpret_cast<uint4*>(to + 2 * (d0 + e)) = pack8<D>(f);
-    }
+    for (int e = 0; e < kJoinDims; ++e)
+        acc[e] *= inv;
+    *reinterpret_cast<uint4*>(a.out.p + row * a.out.row + h * a.out.head + 2 * d0) = pack8<D>(acc);
     if (a.lse && blockIdx.y == 0)
-        a.lse[(int64_t)row * a.Hq + h] = (top + log2f(sum)) * kLn2;
+        a.lse[(int64_t)row * a.Hq + h] = (m + log2f(l)) * kLn2;
 }
 
 // the stride of an extent of one: any multiple of 16
@@ -827,7 +897,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
                      plan, d.status + kStatusWords);
     if (e != cudaSuccess || plan.whole || blocks == 1)
         return e;
-    return launch_after(join_kernel<D, DP>, dim3(blocks, DP / 16), 2 * kRows, 0, s, a, plan);
+    return launch_after(join_kernel<D, DP>, dim3(blocks, DP / kJoinDims), 2 * kRows, 0, s, a, plan);
 }
 
 }  // namespace

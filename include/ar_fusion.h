@@ -766,7 +766,8 @@ int ar_fusion_prompt_attention(const ar_kv_cache* cache, const ar_head_rows* q,
 /* Device-side status of ar_fusion_prompt_attention on the current device, as
  * ar_fusion_matmul_status.  *detail: 1 the copies for a free stage, 2 for free
  * queries, 3 the products for queries, 4 for keys or values, 5 for weights, 6 the
- * softmax for scores, 7 for sums, 8 the clearing of unseen values, or -1. */
+ * softmax for scores, 7 for sums, 8 the clearing of unseen values, 9 any of them for the
+ * next item, 10 the search for items for a free place, or -1. */
 int ar_fusion_attention_status(void* stream, int* detail);
 
 /* ---------------------------------------------------------- utilities -- */
