@@ -3,11 +3,13 @@
 // Scores S = Q K^T and sums O += P V on the tensor cores, both in tensor memory.  The rows
 // of a tile are the query heads that share a head of the cache, of consecutive tokens
 // (128 / G tokens x G heads, so that a tile's rows see nearly the same keys); a block has
-// two tiles, which read the same keys and values from shared memory, 128 keys at a
-// time.  While the tensor cores work for one tile the four warps of the other turn its
+// two tiles, which read the same keys and values from shared memory, 128 keys a step: two
+// groups of 64 of those that the rows see (first tokens and window need no step each).
+// While the tensor cores work for one tile the four warps of the other turn its
 // scores into weights: a thread has a row, so its maximum and sum need no exchange,
 // and writes the weights back where the scores were, as the first operand of the
 // second product.  The sums are rescaled only where a row's maximum grew far (growth()).
+// An item's output is written while the first products of the next one run.
 //
 //   tensor memory: scores of tile 0, of tile 1, sums of tile 0, of tile 1, 128 columns each
 //   warps 0-3, 4-7: softmax and output of tile 0, 1;  warp 8: copies;  warp 9: products;
@@ -27,7 +29,7 @@ namespace arf {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRows = 128, kKeys = 128;             // of a tile, of a step
+constexpr int kRows = 128, kKeys = 128, kGroup = 64;   // of a tile, of a step, of a group
 constexpr int kRegsLaunch = 168, kRegsFew = 88, kRegsMany = 208;
 static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * kRegsLaunch, "register shares");
 constexpr float kLn2 = 0.693147181f;
@@ -65,15 +67,24 @@ struct Plan {
 struct Pair {
     int seq, row0, tokens, i0;
     int end, low, sinks;        // keys that any row sees: below end, from low on or below sinks
-    int first, gap, n;          // key tiles: x of n is tile x, or x + gap behind `first`
+    int first, gap, groups;     // of 64 keys: the first ones, then those from group first + gap on
+    int n;                      // steps of two groups
 };
 
-// whether a key tile holds keys that no row of the pair sees
+// the first key of group g; behind the last group: one that no row sees
+__device__ __forceinline__ int key_of(const Pair& p, int g)
+{
+    return g < p.groups ? (g < p.first ? g : g + p.gap) * kGroup : p.end;
+}
+// whether a group holds keys that no row of the pair sees
 __device__ __forceinline__ bool has_unseen(const Pair& p, int key0)
 {
-    return key0 + kKeys > p.end || (key0 < p.low && key0 + kKeys > p.sinks);
+    return key0 + kGroup > p.end || (key0 < p.low && key0 + kGroup > p.sinks);
 }
-__device__ __forceinline__ int tile_of(const Pair& p, int x) { return x < p.first ? x : x + p.gap; }
+__device__ __forceinline__ bool step_has_unseen(const Pair& p, int x)
+{
+    return has_unseen(p, key_of(p, 2 * x)) || has_unseen(p, key_of(p, 2 * x + 1));
+}
 
 // tokens of a sequence in the call
 __device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
@@ -105,17 +116,18 @@ __device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const i
     p.end = max(p.i0 + p.tokens, 0);
     p.low = a.window ? (int)max((long long)p.i0 - a.window + 1, 0ll) : 0;
     p.sinks = a.window ? min(a.sinks, p.end) : 0;
-    p.first = (p.sinks + kKeys - 1) / kKeys;
-    p.gap = max(0, min(p.low, p.end) / kKeys - p.first);
-    p.n = (p.end + kKeys - 1) / kKeys - p.gap;
+    p.first = (p.sinks + kGroup - 1) / kGroup;
+    p.gap = max(0, min(p.low, p.end) / kGroup - p.first);
+    p.groups = (p.end + kGroup - 1) / kGroup - p.gap;
+    p.n = (p.groups + 1) / 2;
     return p;
 }
 
-// What a block does next: key tiles x0 .. x1 - 1 of a pair for a head (none: nothing left);
+// What a block does next: steps x0 .. x1 - 1 of a pair for a head (none: nothing left);
 // where the item begins here and ends in another block, that block.
 struct Item {
     Pair p;
-    int head, x0, x1, end_block, pad[2];
+    int head, x0, x1, end_block, pad;
 };
 static_assert(sizeof(Item) == 64, "copied as four vectors");
 constexpr uint32_t kItems = 4;                      // found ahead
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using F = Shape<DP>;
     constexpr uint32_t kStages = F::stages;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 6 + 1 + 2 * kItems];
+    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 7 + 1 + 2 * kItems];
     __shared__ __align__(16) Item item_sh[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, begin_sh[2];
@@ -211,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
                    wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
-                   pfull = sfull + 16, ofull = pfull + 32, done = ofull + 16,
+                   pfull = sfull + 16, ofull = pfull + 32, ofree = ofull + 16,
+                   done = ofree + 16,
                    ifull = done + 8, iempty = ifull + 8 * kItems;
     const Bail bail{smem_u32(&dead), status};
 
@@ -230,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(pfull + 16 * t, 4);        // weights of the first 64 keys, of the others
             bar_init(pfull + 16 * t + 8, 4);
             bar_init(ofull + 8 * t, 1);
+            bar_init(ofree + 8 * t, 4);
         }
         bar_init(done, 1);
         for (uint32_t i = 0; i < kItems; ++i) {
@@ -384,20 +398,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         regs_fewer<kRegsFew>();
         if (warp == 8) {
-            // copies: per item the queries, then keys and values of a tile in turn
+            // copies: per item the first keys, the queries, then values and keys in turn
             uint32_t it = 0, uses[2] = {0, 0};
-            const int page_rows = min(1 << a.c.page_shift, kKeys), boxes = kKeys / page_rows;
+            const int page_rows = min(1 << a.c.page_shift, kGroup), boxes = kKeys / page_rows;
             const int box = lane % boxes, part = lane / boxes;      // part: which 64 elements
             while (ok && take(true)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x) {
-                    const int key = tile_of(w.p, x) * kKeys + box * page_rows;
+                    // a lane's box lies in one of the step's two groups
+                    const int in = box * page_rows;
+                    const int key = key_of(w.p, 2 * x + in / kGroup) + in % kGroup;
                     int page = -1;
                     if (key < w.p.end)
                         page = a.c.table[(int64_t)w.p.seq * a.c.max_pages + (key >> a.c.page_shift)];
                     // outside the map: zeros
                     if (page < 0 || page >= a.c.pages)
                         page = a.c.pages;
-                    const int row = key & ((1 << a.c.page_shift) - 1);
+                    const int row = page == a.c.pages ? 0 : key & ((1 << a.c.page_shift) - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         const uint32_t s = it % kStages;
@@ -408,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0)
                             bar_expect(full + 8 * s, F::tile);
                         __syncwarp();
-                        // a lane's box: at most 16 a half of the tile
-                        const uint32_t to = ring + s * F::tile + box * page_rows * 128;
+                        // at most 16 boxes a half of the tile
+                        const uint32_t to = ring + s * F::tile + in * 128;
                         for (int h = part; h < DP / 64; h += 32 / boxes)
                             tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
                                         row, w.head, page);
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                             }
                         }
-                        if (kv && lane == 0 && has_unseen(w.p, tile_of(w.p, x) * kKeys))
+                        if (kv && lane == 0 && step_has_unseen(w.p, x))
                             bar_arrive(wanted + 8 * s);
                     }
                 }
@@ -463,76 +479,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr bool bf16 = D::id == AR_DT_BF16;
                 constexpr uint32_t id_s = half_idesc(kRows, kKeys, bf16, false);
                 constexpr uint32_t id_o = half_idesc(kRows, DP, bf16, true);
-                uint32_t it = 0, uses[2] = {0, 0}, weights[2] = {0, 0}, clears = 0;
-                const auto scores = [&](int t, uint32_t s) {
-                    const uint64_t q = smem_desc(q_at + t * F::tile), k = smem_desc(ring + s * F::tile);
-#pragma unroll
-                    for (int i = 0; i < DP / 16; ++i) {
-                        const uint32_t off = (i / 4) * (F::half >> 4) + (i % 4) * 2;
-                        mma_half(tmem + t * 128, q + off, k + off, id_s, i > 0);
-                    }
-                    mma_commit(sfull + 8 * t);
+                // low words of the descriptors of the queries, and of stage 0 as keys and as values
+                const uint64_t desc_k = smem_desc(ring), desc_v = smem_desc_mn(ring, F::half);
+                const uint32_t q_lo = (uint32_t)smem_desc(q_at), k_lo = (uint32_t)desc_k,
+                               v_lo = (uint32_t)desc_v, k_hi = (uint32_t)(desc_k >> 32),
+                               v_hi = (uint32_t)(desc_v >> 32);
+                // queries taken, weights taken, items begun (bit t, modulo 2: of tile t)
+                uint32_t it = 0, uses = 0, weights = 0, begun = 3, clears = 0;
+                const auto landed = [&](uint32_t i) {
+                    ok = bar_wait(full + 8 * (i % kStages), i / kStages & 1, bail, kWaitKeys);
+                    return ok;
                 };
-                while (ok && take(false)) {
-                    const int tiles = w.p.tokens > plan.tok ? 2 : 1;
-                    if (!(ok = bar_wait(full + 8 * (it % kStages), it / kStages & 1, bail, kWaitKeys)))
-                        break;
-                    for (int t = 0; t < tiles && ok; ++t) {
-                        if (!(ok = bar_wait(qfull + 8 * t, uses[t] & 1, bail, kWaitQuery)))
-                            break;
-                        ++uses[t];
+                // scores of an item's step from the keys of stage i; of its first step the queries
+                // are waited for, behind its last they are done with
+                const auto scores = [&](uint32_t t, uint32_t i, bool first, bool last) {
+                    if (first) {
+                        ok = bar_wait(qfull + 8 * t, uses >> t & 1, bail, kWaitQuery);
+                        if (!ok)
+                            return;
+                        uses ^= 1u << t;
                         tc_fence_after();
-                        scores(t, it % kStages);
-                        if (w.x0 + 1 == w.x1)
-                            mma_commit(qempty + 8 * t);
                     }
-                    if (!ok)
-                        break;
+                    const uint32_t q = q_lo + t * (F::tile >> 4), k = k_lo + i % kStages * (F::tile >> 4);
+#pragma unroll
+                    for (int h = 0; h < DP / 64; ++h)
+                        mma4_half(tmem + t * 128, q + h * (F::half >> 4), k + h * (F::half >> 4), k_hi, id_s,
+                                  h > 0);
+                    mma_commit(sfull + 8 * t);
+                    if (last)
+                        mma_commit(qempty + 8 * t);
+                };
+                bool more = take(false);
+                uint32_t tiles = w.p.tokens > plan.tok ? 2 : 1;
+                if (more && landed(it)) {
+                    for (uint32_t t = 0; t < tiles && ok; ++t)
+                        scores(t, it, true, w.x0 + 1 == w.x1);
                     mma_commit(empty + 8 * (it % kStages));
                     ++it;
-                    for (int x = w.x0; x < w.x1 && ok; ++x) {
-                        const uint32_t sv = it % kStages, sk = (it + 1) % kStages;
-                        const bool last = x + 1 == w.x1;
-                        if (!(ok = bar_wait(full + 8 * sv, it / kStages & 1, bail, kWaitKeys)))
+                }
+                while (ok && more) {
+                    for (int x = w.x0, x0 = x, x1 = w.x1; x < x1 && ok; ++x) {
+                        // values of this step: stage it; keys of the next, of the next item behind
+                        // the last step: it + 1
+                        const uint32_t sv = it % kStages, now = tiles;
+                        const bool last = x + 1 == x1, unseen = step_has_unseen(w.p, x);
+                        uint32_t then = tiles;
+                        bool next_last = x + 2 == x1;
+                        if (last) {
+                            more = take(false);
+                            tiles = then = !more ? 0 : w.p.tokens > plan.tok ? 2 : 1;
+                            next_last = w.x0 + 1 == w.x1;
+                            if (!ok)
+                                break;
+                        }
+                        if (!landed(it))
                             break;
-                        if (has_unseen(w.p, tile_of(w.p, x) * kKeys)) {
+                        if (unseen) {
                             if (!(ok = bar_wait(cleared + 8 * sv, clears >> sv & 1, bail, kWaitCleared)))
                                 break;
                             clears ^= 1u << sv;
                         }
-                        for (int t = 0; t < tiles && ok; ++t) {
-                            const uint64_t v = smem_desc_mn(ring + sv * F::tile, F::half);
-                            for (int h = 0; h < 2 && ok; ++h) {
-                                if (!(ok = bar_wait(pfull + 16 * t + 8 * h, weights[t] & 1, bail,
-                                                    kWaitWeights)))
+                        const uint32_t v = v_lo + sv * (F::tile >> 4);
+                        for (uint32_t t = 0; t < 2; ++t) {
+                            if (t < now) {
+                                // the sums of the item before have been read
+                                if (x == x0) {
+                                    if (!(ok = bar_wait(ofree + 8 * t, begun >> t & 1, bail, kWaitSums)))
+                                        break;
+                                    begun ^= 1u << t;
+                                }
+                                const uint32_t o = tmem + 256 + t * 128, p = tmem + t * 128,
+                                               bar = pfull + 16 * t, par = weights >> t & 1;
+                                weights ^= 1u << t;
+                                if (!(ok = bar_wait(bar, par, bail, kWaitWeights)))
                                     break;
                                 tc_fence_after();
-#pragma unroll
-                                for (int i = 0; i < kKeys / 32; ++i)
-                                    mma_half_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * h + 8 * i,
-                                                v + (4 * h + i) * (2048 >> 4), id_o,
-                                                x > w.x0 || h > 0 || i > 0);
+                                mma4_half_ts(o, p, v, v_hi, id_o, x > x0);
+                                if (!(ok = bar_wait(bar + 8, par, bail, kWaitWeights)))
+                                    break;
+                                tc_fence_after();
+                                mma4_half_ts(o, p + 32, v + 512, v_hi, id_o, true);
+                                if (last)
+                                    mma_commit(ofull + 8 * t);
+                                if (t + 1 == now)
+                                    mma_commit(empty + 8 * sv);
                             }
-                            if (!ok)
-                                break;
-                            ++weights[t];
-                            if (t + 1 == tiles)
-                                mma_commit(empty + 8 * sv);
-                            if (last) {
-                                mma_commit(ofull + 8 * t);
-                                continue;
+                            if (t < then) {
+                                if (t == 0 && !landed(it + 1))
+                                    break;
+                                scores(t, it + 1, last, next_last);
+                                if (!ok)
+                                    break;
+                                if (t + 1 == then)
+                                    mma_commit(empty + 8 * ((it + 1) % kStages));
                             }
-                            if (t == 0 && !(ok = bar_wait(full + 8 * sk, (it + 1) / kStages & 1, bail,
-                                                          kWaitKeys)))
-                                break;
-                            tc_fence_after();
-                            scores(t, sk);
-                            if (x + 2 == w.x1)
-                                mma_commit(qempty + 8 * t);
-                            if (t + 1 == tiles)
-                                mma_commit(empty + 8 * sk);
                         }
-                        it += last ? 1 : 2;
+                        it += then ? 2 : 1;
                     }
                 }
                 if (!ok) {
@@ -548,8 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t it = 0, asked = 0;
             while (ok && take(true)) {
                 for (int x = w.x0; x < w.x1 && ok; ++x, it += 2) {
-                    const int key0 = tile_of(w.p, x) * kKeys;
-                    if (!has_unseen(w.p, key0))
+                    if (!step_has_unseen(w.p, x))
                         continue;
                     const uint32_t s = (it + 1) % kStages;
                     ok = bar_wait(wanted + 8 * s, asked >> s & 1, bail, kWaitCleared) &&
@@ -559,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok)
                         break;
                     for (int i = lane; i < kKeys * 8; i += 32) {
-                        const int key = key0 + i / 8;
+                        const int key = key_of(w.p, 2 * x + i / (8 * kGroup)) + i / 8 % kGroup;
                         if (key < w.p.end && (key >= w.p.low || key < w.p.sinks))
                             continue;
 #pragma unroll
@@ -600,6 +641,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
         const int in = r / a.G, g = r - in * a.G;       // token of the tile, head of the group
         uint32_t seen = 0, items = 0;
+        // the item whose sums are still to be read
+        bool held = false;
+        float held_top = 0.0f, held_sum = 0.0f;
+        int held_row = 0, held_head = 0, held_part = -1;        // row -1: of no token
+        const auto give = [&]() {
+            held = false;
+            bar_wait(ofull + 8 * t, items & 1, bail, kWaitSums);
+            ++items;
+            __syncwarp();
+            tc_fence_after();
+            const bool live = held_row >= 0;
+            const float inv = held_sum > 0.0f || held_sum != held_sum ? 1.0f / held_sum : 0.0f;
+            // a warp whose rows are of no token has nothing to say
+            const bool any = __any_sync(0xffffffffu, live);
+#pragma unroll 1
+            for (int c0 = 0; any && c0 < DP; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_at + c0, o);
+                tmem_wait32(o);
+                if (held_part >= 0) {
+                    float* part = reinterpret_cast<float*>(
+                                      plan.parts + (int64_t)(2 * blockIdx.x + held_part) * F::part) +
+                                  (c0 + 2) * 2 * kRows + t * kRows + r;
+                    if (live) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            part[c * 2 * kRows] = __uint_as_float(o[c]);
+                    }
+                    continue;
+                }
+                uint8_t* to = a.out.p + held_row * a.out.row + held_head * a.out.head + 2 * c0;
+#pragma unroll
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = pack2<D>(__uint_as_float(o[c + 2 * e]) * inv,
+                                        __uint_as_float(o[c + 2 * e + 1]) * inv);
+                    // whole sectors where the output allows it
+                    const int n = a.c.D - c0 - c;
+                    if (plan.wide && n >= 16) {
+                        if (live)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + 2 * c),
+                                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                                         "r"(v[6]), "r"(v[7])
+                                         : "memory");
+                    } else {
+                        if (live && n > 0)
+                            *reinterpret_cast<uint4*>(to + 2 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (live && n > 8)
+                            *reinterpret_cast<uint4*>(to + 2 * c + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(ofree + 8 * t);
+            if (!live)
+                return;
+            if (held_part >= 0) {
+                float* part = reinterpret_cast<float*>(
+                                  plan.parts + (int64_t)(2 * blockIdx.x + held_part) * F::part) +
+                              t * kRows + r;
+                part[0] = held_top;
+                part[2 * kRows] = held_sum;
+            } else if (a.lse) {
+                a.lse[(int64_t)held_row * a.Hq + held_head] = (held_top + log2f(held_sum)) * kLn2;
+            }
+        };
         while (take(true)) {
             const int tok0 = t * plan.tok;
             if (tok0 >= w.p.tokens)
@@ -607,10 +718,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = in < plan.tok && tok0 + in < w.p.tokens;
             const int i = live ? w.p.i0 + tok0 + in : -1;
             const int ia = w.p.i0 + tok0, ib = w.p.i0 + min(tok0 + plan.tok, w.p.tokens) - 1;
+            // steps full0 .. full1 - 1: every row sees every key
+            const int full0 = a.window ? (max(ib - a.window + kGroup, 0) / kGroup - w.p.gap + 1) / 2 : 0,
+                      full1 = (max(ia + 1, 0) / kGroup - w.p.gap) / 2;
             float top = -INFINITY;
             uint64_t sum = 0;
             for (int x = w.x0; x < w.x1; ++x, ++seen) {
-                const int key0 = tile_of(w.p, x) * kKeys;
                 bar_wait(sfull + 8 * t, seen & 1, bail, kWaitScores);
                 __syncwarp();
                 tc_fence_after();
@@ -621,38 +734,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tmem_wait32(s + 32 * c);
-                // every row sees every key?
-                if (!(key0 + kKeys - 1 <= ia &&
-                      (a.window == 0 || key0 > ib - a.window || key0 + kKeys <= a.sinks))) {
-                    const int hi = i + 1 - key0, lo = a.window ? i - a.window + 1 - key0 : 0,
-                              first = a.sinks - key0;
+                if (__builtin_expect(x < full0 || x >= full1, 0)) {
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
-                        const uint32_t seen_bits =
-                            below(hi - c) & (~below(lo - c) | below(first - c));
+                    for (int h = 0; h < 2; ++h) {
+                        const int key0 = key_of(w.p, 2 * x + h);
+                        const int hi = i + 1 - key0, lo = a.window ? i - a.window + 1 - key0 : 0,
+                                  first = a.sinks - key0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            s[c + e] = seen_bits >> e & 1 ? s[c + e] : 0xff800000u;
+                        for (int c = 0; c < kGroup; c += 32) {
+                            const uint32_t bits = below(hi - c) & (~below(lo - c) | below(first - c));
+                            if (__all_sync(0xffffffffu, bits == 0xffffffffu))
+                                continue;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[kGroup * h + c + e] = bits >> e & 1 ? s[kGroup * h + c + e] : 0xff800000u;
+                        }
                     }
                 }
-                // The weights of the first half by the maximum so far, while that of these scores
-                // is found; nearly always it is near enough.
-                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2);
-                uint32_t p[32];
-                uint64_t part[4] = {0, 0, 0, 0};
-                const auto weigh = [&](int c) {
-                    const float used = top == -INFINITY ? 0.0f : top;
-                    const uint64_t minus = pair_of(-used, -used);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int k = 64 * c + 2 * e;
-                        const float2 z = unpack_pair(fma3_pair(pack_pair(s[k], s[k + 1]), scale, minus));
-                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                        part[e & 3] = add_pair(part[e & 3], pair_of(e0, e1));
-                        p[e] = pack2<D>(e0, e1);
-                    }
-                };
-                weigh(0);
                 float m[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -662,15 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 12; c < kKeys; c += 2)
                     m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale_log2;
-                if (__any_sync(0xffffffffu, best > top + growth<D>())) {
+                if (__builtin_expect(__any_sync(0xffffffffu, best > top + growth<D>()), 0)) {
                     const float now = best > top + growth<D>() ? best : top;
                     const float f = now == top ? 1.0f : exp2_fast(top - now);
                     top = now;
                     sum = mul_pair(sum, pair_of(f, f));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        part[e] = 0;
-                    weigh(0);
                     if (x > w.x0) {
 #pragma unroll 1
                         for (int c = 0; c < DP; c += 16) {
@@ -684,87 +778,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                // The products of the first half of the weights begin while the second half is made.
+                const float used = top == -INFINITY ? 0.0f : top;
+                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2), minus = pair_of(-used, -used);
+                uint64_t part[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c == 1)
-                        weigh(1);
-                    tmem_st32(s_at + 32 * c, p);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int k = 64 * h + 2 * e;
+                        const float2 z = unpack_pair(fma3_pair(pack_pair(s[k], s[k + 1]), scale, minus));
+                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                        part[e & 3] = add_pair(part[e & 3], pair_of(e0, e1));
+                        p[e] = pack2<D>(e0, e1);
+                    }
+                    tmem_st32(s_at + 32 * h, p);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        bar_arrive(pfull + 16 * t + 8 * c);
+                        bar_arrive(pfull + 16 * t + 8 * h);
                 }
                 sum = add_pair(sum, add_pair(add_pair(part[0], part[1]), add_pair(part[2], part[3])));
+                if (__builtin_expect(held, 0))
+                    give();
             }
             const float2 two = unpack_pair(sum);
-            const float total_w = two.x + two.y;
-            bar_wait(ofull + 8 * t, items & 1, bail, kWaitSums);
-            ++items;
-            __syncwarp();
-            tc_fence_after();
-            const int row = w.p.row0 + tok0 + in, h = w.head * a.G + g;
-            const bool split = w.x0 > 0 || w.x1 < w.p.n;
-            if (!split) {
-                const float inv = total_w > 0.0f || total_w != total_w ? 1.0f / total_w : 0.0f;
-                uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
-                uint32_t o[DP];
-#pragma unroll
-                for (int c = 0; c < DP; c += 32)
-                    tmem_ld32(o_at + c, o + c);
-#pragma unroll
-                for (int c = 0; c < DP; c += 32)
-                    tmem_wait32(o + c);
-#pragma unroll
-                for (int c = 0; c < DP; c += 16) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = pack2<D>(__uint_as_float(o[c + 2 * e]) * inv,
-                                        __uint_as_float(o[c + 2 * e + 1]) * inv);
-                    // whole sectors where the output allows it
-                    if (plan.wide && c + 16 <= a.c.D) {
-                        if (live)
-                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + 2 * c),
-                                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-                                         "r"(v[6]), "r"(v[7])
-                                         : "memory");
-                    } else {
-                        if (live && c < a.c.D)
-                            *reinterpret_cast<uint4*>(to + 2 * c) = make_uint4(v[0], v[1], v[2], v[3]);
-                        if (live && c + 8 < a.c.D)
-                            *reinterpret_cast<uint4*>(to + 2 * c + 16) = make_uint4(v[4], v[5], v[6], v[7]);
-                    }
-                }
-                if (live && a.lse)
-                    a.lse[(int64_t)row * a.Hq + h] = (top + log2f(total_w)) * kLn2;
-            } else {
-                // a piece that begins here is part 1, one that began before part 0
-                const int which = w.x0 == 0 ? 1 : 0;
-                float* to = reinterpret_cast<float*>(plan.parts +
-                                                     (int64_t)(2 * blockIdx.x + which) * F::part) +
-                            t * kRows + r;
-                to[0] = top;
-                to[2 * kRows] = total_w;
-                to += 4 * kRows;
-                // a warp whose rows are of no token has nothing to say
-                if (__any_sync(0xffffffffu, live)) {
-                    uint32_t o[DP];
-#pragma unroll
-                    for (int c = 0; c < DP; c += 32)
-                        tmem_ld32(o_at + c, o + c);
-#pragma unroll
-                    for (int c = 0; c < DP; c += 32)
-                        tmem_wait32(o + c);
-#pragma unroll
-                    for (int c = 0; c < DP; ++c)
-                        to[c * 2 * kRows] = __uint_as_float(o[c]);
-                }
-                if (which && tid == 0)
-                    plan.desc[blockIdx.x] = make_int4(w.end_block - (int)blockIdx.x + 1, w.p.row0,
-                                                      w.p.tokens, w.head);
-            }
+            held = true;
+            held_top = top;
+            held_sum = two.x + two.y;
+            held_row = live ? w.p.row0 + tok0 + in : -1;
+            held_head = w.head * a.G + g;
+            // a piece that begins here is part 1, one that began before part 0
+            held_part = w.x0 > 0 ? 0 : w.x1 < w.p.n ? 1 : -1;
+            if (held_part == 1 && tid == 0)
+                plan.desc[blockIdx.x] = make_int4(w.end_block - (int)blockIdx.x + 1, w.p.row0, w.p.tokens,
+                                                  w.head);
         }
+        if (held)
+            give();
         __syncwarp();
     }
     tc_fence_before();
@@ -847,7 +900,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     plan.tok = kRows / a.G;
     plan.wide = ((uintptr_t)a.out.p | (uint64_t)a.out.row | (uint64_t)a.out.head) % 32 == 0;
     const uint64_t D_ = (uint64_t)a.c.D;
-    const uint32_t page = 1u << a.c.page_shift, box = page < (uint32_t)kKeys ? page : kKeys;
+    const uint32_t page = 1u << a.c.page_shift, box = page < (uint32_t)kGroup ? page : kGroup;
     CUtensorMap map_q, map_k, map_v;
     if (!rows_tensor_map(&map_q, D::id, a.q.p, {D_, (uint64_t)a.G, (uint64_t)a.c.heads, (uint64_t)a.T},
                          {stride_of(a.q.head), stride_of(a.q.head * a.G), stride_of(a.q.row)},
@@ -885,7 +938,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
             blocks = (int)items;
     } else {
         const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
-        const int64_t most = items * ((keys + kKeys - 1) / kKeys);
+        const int64_t most = items * ((keys + kKeys - 1) / kKeys + 1);
         if (most < blocks)
             blocks = (int)most;
         if (fit < blocks)

@@ -339,24 +339,45 @@ __host__ __device__ constexpr uint32_t half_idesc(int M, int N, bool bf16, bool 
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// d = a b (+ d): 16 of K, a in shared memory or (_ts) in tensor memory, there two
-// elements a column
-__device__ __forceinline__ void mma_half(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool add)
+// Four products, 64 of K: d = a b (+ d if `add`).  `a` and `b` are the low words of the
+// descriptors, the second the high word; `_ts`: a in tensor memory, two elements a column, b
+// MN-major (b_step 128) as above.  One asm block each, as below: what stands between a wait for
+// the operands and the first product is time that the tensor cores lack.
+__device__ __forceinline__ void mma4_half(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .b64 p, q;\n\t.reg .b32 x, y;\n\t.reg .pred first, yes;\n\t"
+        "setp.ne.b32 first, %5, 0;\n\tsetp.ne.b32 yes, 1, 0;\n\t"
+        "mov.b64 p, {%1, %3};\n\tmov.b64 q, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], p, q, %4, first;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], p, q, %4, yes;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], p, q, %4, yes;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
+        "mov.b64 p, {x, %3};\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], p, q, %4, yes;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void mma_half_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            bool add)
+__device__ __forceinline__ void mma4_half_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                             uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .b64 q;\n\t.reg .b32 x, y;\n\t.reg .pred first, yes;\n\t"
+        "setp.ne.b32 first, %5, 0;\n\tsetp.ne.b32 yes, 1, 0;\n\t"
+        "mov.b64 q, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], q, %4, first;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], q, %4, yes;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], q, %4, yes;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 q, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], q, %4, yes;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // E4M3 x E4M3 -> fp32, both K-major, M x N per instruction
