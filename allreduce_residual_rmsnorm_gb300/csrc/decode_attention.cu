@@ -13,6 +13,7 @@
 //
 // A warp has slices of its own: 4 KB of keys and 4 KB of values, a ring of kStages of
 // them filled by asynchronous copies, a running maximum and sum, and its own sums.
+// (Tensor-map copies, one thread's, were 3% faster for E4M3 and 5 to 6% slower for 16 bits.)
 // Four warps take the four slices of a unit in turn and meet at the end of a piece.
 //
 // All units of all sequences and heads are one list; a block takes an equal share of it
@@ -20,8 +21,6 @@
 // holds whole items, and at most two pieces of items that other blocks share: those go
 // to the workspace as sums, maximum and total, and join_kernel, launched behind it,
 // adds them in the order of the blocks.
-#include <limits.h>
-
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "matmul_internal.h"
@@ -38,7 +37,7 @@ constexpr int kBlocksPerSm = 2;
 constexpr float kLn2 = 0.693147181f;
 
 struct Split {
-    int4* desc;                         // [blocks]: parts, sequence, head and tile
+    int4* desc;                         // [blocks]: parts, sequence, head, tile
     uint8_t* parts;                     // [blocks][2] of part_bytes
     int whole;                          // 1: items are not split
 };
@@ -114,10 +113,10 @@ struct Seen {
     int length, low, sinks, first, gap, n;
 };
 template <int SL>
-__device__ __forceinline__ Seen seen_of(const AttentionArgs& a, int seq)
+__device__ __forceinline__ Seen seen_of(const AttentionArgs& a, int length)
 {
     Seen s;
-    s.length = clamp_length(a.c, a.c.lengths[seq]);
+    s.length = clamp_length(a.c, length);
     s.low = a.window ? max(0, s.length - a.window) : 0;
     s.sinks = min(a.sinks, s.length);
     s.first = (s.sinks + SL - 1) / SL;
@@ -127,33 +126,40 @@ __device__ __forceinline__ Seen seen_of(const AttentionArgs& a, int seq)
     return s;
 }
 
-// A place in the list of units: unit `unit` of `units` of head `head` (with its tile of
-// query heads) of sequence `seq`.
+// A place in the list of units: unit `unit` of `units` of tile `tile` of the query heads of head
+// `head` of sequence `seq`.  (Without divisions: a warp is one chain of instructions, and each
+// would be a tenth of a unit.)
 template <int SL>
 struct Cursor {
-    int seq, head, unit, units;
+    int seq, head, tile, unit, units;
+    const int32_t* table;       // of the sequence
+    int after;                  // length of the next sequence, asked for ahead
     Seen seen;
 
-    __device__ __forceinline__ void enter(const AttentionArgs& a, int s)
+    __device__ __forceinline__ void enter(const AttentionArgs& a, int s, int length)
     {
         seq = s;
-        seen = seen_of<SL>(a, s);
+        table = a.c.table + (int64_t)s * a.c.max_pages;
+        after = s + 1 < a.c.S ? a.c.lengths[s + 1] : 0;
+        seen = seen_of<SL>(a, length);
         units = (seen.n + kWarps - 1) / kWarps;
     }
-    // to the next unit; false: there is none
-    __device__ __forceinline__ void next(const AttentionArgs& a, int heads)
+    // to the next unit, while there is one
+    __device__ __forceinline__ void next(const AttentionArgs& a, int tiles)
     {
         if (++unit < units)
             return;
         unit = 0;
-        if (++head < heads)
+        if (++tile < tiles)
+            return;
+        tile = 0;
+        if (++head < a.c.heads)
             return;
         head = 0;
-        int s = seq;
         do {
-            if (++s == a.c.S)           // the end of the list: not used further
+            if (seq + 1 == a.c.S)       // the end of the list: not used further
                 return;
-            enter(a, s);
+            enter(a, seq + 1, after);
         } while (units == 0);
     }
 };
@@ -171,38 +177,46 @@ struct Form {
     }
 };
 
-// Copies of one slice of a cursor's unit into a stage, by one warp.
-template <class D, int DP, bool F8>
-__device__ __forceinline__ void load_slice(const AttentionArgs& a, const Cursor<Form<D, DP, F8>::SL>& c,
-                                           int head, int warp, int lane, uint32_t stage)
+// First key of the slice of a warp in a cursor's unit; -1: it has none.
+template <int SL>
+__device__ __forceinline__ int slice_key(const Cursor<SL>& c, int warp)
 {
-    using F = Form<D, DP, F8>;
     const int x = c.unit * kWarps + warp;
-    if (x < c.seen.n) {
-        const int key0 = (x < c.seen.first ? x : x + c.seen.gap) * F::SL;
-        // the page of 8 keys at a time
-        int page = -1;
-        const int mine = key0 + 8 * lane;
-        if (lane < F::SL / 8 && mine < c.seen.length)
-            page = a.c.table[(int64_t)c.seq * a.c.max_pages + (mine >> a.c.page_shift)];
+    return x < c.seen.n ? (x < c.seen.first ? x : x + c.seen.gap) * SL : -1;
+}
+// The page of 8 keys of that slice, by lane; -1: none.  Asked for a unit before its copies: with
+// the two together the answer's way, 0.7 us, was half of the time of a unit.
+template <int SL>
+__device__ __forceinline__ int slice_page(const AttentionArgs& a, const Cursor<SL>& c, int warp, int lane)
+{
+    const int key0 = slice_key(c, warp), mine = key0 + 8 * lane;
+    if (key0 < 0 || lane >= SL / 8 || mine >= c.seen.length)
+        return -1;
+    return c.table[mine >> a.c.page_shift];
+}
+// Copies of one slice into a stage, by one warp: a lane has a chunk of every kStep-th row.
+template <class F>
+__device__ __forceinline__ void load_slice(const AttentionArgs& a, int key0, int head, int page, int lane,
+                                           uint32_t stage)
+{
+    if (key0 >= 0) {
+        constexpr int kChunks = F::pitch / 16, kStep = 32 / kChunks;
+        const int chunk = lane % kChunks, row = lane / kChunks, mask = (1 << a.c.page_shift) - 1;
         if (page >= a.c.pages)
             page = -1;
-        constexpr int kChunks = F::pitch / 16, kStep = 32 / kChunks;    // rows a step
-        const int chunk = lane % kChunks;
-        const bool used = chunk * 16 < a.c.D * F::bytes;
         const uint8_t* k = a.c.k + head * a.c.k_head + chunk * 16;
         const uint8_t* v = a.c.v + head * a.c.v_head + chunk * 16;
+        const bool used = chunk * 16 < a.c.D * F::bytes;
 #pragma unroll
         for (int i = 0; i < kTile / 512; ++i) {
-            const int r = i * kStep + lane / kChunks;
+            const int r = i * kStep + row, in = (key0 + r) & mask;
             const int p = __shfl_sync(0xffffffffu, page, r >> 3);
-            const int in = (key0 + r) & ((1 << a.c.page_shift) - 1);
             const bool there = p >= 0;
-            const int64_t pp = there ? p : 0;
+            const int64_t pp = max(p, 0);
             if (used) {
                 const uint32_t to = stage + F::at(r, chunk);
-                copy16(to, k + pp * a.c.k_page + in * a.c.k_row, there);
-                copy16(to + kTile, v + pp * a.c.v_page + in * a.c.v_row, there);
+                copy16(to, k + (pp * a.c.k_page + in * a.c.k_row), there);
+                copy16(to + kTile, v + (pp * a.c.v_page + in * a.c.v_row), there);
             }
         }
     }
@@ -250,11 +264,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int heads = a.c.heads * tiles;        // items of a sequence
     float* sums = reinterpret_cast<float*>(dyn + kWarps * kStages * 2 * kTile);
     const uint32_t ring = smem_u32(dyn) + warp * kStages * 2 * kTile;
-
     pdl_trigger();
     // chunks behind the head's last element are never copied: zero once, for good
-    for (int i = DP > a.c.D ? tid : INT_MAX; i < kWarps * kStages * 2 * kTile / 16; i += kThreads)
-        reinterpret_cast<uint4*>(dyn)[i] = make_uint4(0, 0, 0, 0);
+    if (DP > a.c.D)
+        for (int i = tid; i < kWarps * kStages * 2 * kTile / 16; i += kThreads)
+            reinterpret_cast<uint4*>(dyn)[i] = make_uint4(0, 0, 0, 0);
     pdl_wait();
 
     // this block's share of the list of units, and where it begins
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int s0 = min(tid * per, a.c.S), s1 = min(s0 + per, a.c.S);
     long long mine = 0;
     for (int s = s0; s < s1; ++s)
-        mine += (long long)((seen_of<SL>(a, s).n + kWarps - 1) / kWarps) * heads;
+        mine += (long long)((seen_of<SL>(a, a.c.lengths[s]).n + kWarps - 1) / kWarps) * heads;
     long long upto = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -282,8 +296,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int block = blockIdx.x, blocks = (int)min((long long)gridDim.x, max(total, 1ll));
     long long u0 = total, u1 = total;
     if (block < blocks) {
-        u0 = total * block / blocks;
-        u1 = total * (block + 1) / blocks;
+        if (total < 1ll << 31) {        // total * block / blocks in 32 bits
+            const unsigned each = (unsigned)total / (unsigned)blocks,
+                           rest = (unsigned)total - each * (unsigned)blocks;
+            u0 = each * block + rest * block / (unsigned)blocks;
+            u1 = each * (block + 1) + rest * (block + 1) / (unsigned)blocks;
+        } else {
+            u0 = total * block / blocks;
+            u1 = total * (block + 1) / blocks;
+        }
     }
     if (sp.whole) {
         // items whose first unit lies in the share
@@ -292,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncthreads();
         long long at = upto - mine;
         for (int s = s0; s < s1; ++s) {
-            const int n = (seen_of<SL>(a, s).n + kWarps - 1) / kWarps;
+            const int n = (seen_of<SL>(a, a.c.lengths[s]).n + kWarps - 1) / kWarps;
             const long long end = at + (long long)n * heads;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         long long at = upto - mine;
         if (u0 < u1 && u0 >= at && u0 < upto) {
             for (int s = s0; s < s1; ++s) {
-                const int n = (seen_of<SL>(a, s).n + kWarps - 1) / kWarps;
+                const int n = (seen_of<SL>(a, a.c.lengths[s]).n + kWarps - 1) / kWarps;
                 const long long end = at + (long long)n * heads;
                 if (u0 < end) {
                     const int in = (int)(u0 - at);
@@ -326,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     // sequences without a key
     for (int s = block; s < a.c.S; s += (int)gridDim.x) {
-        if (seen_of<SL>(a, s).n > 0)
+        if (seen_of<SL>(a, a.c.lengths[s]).n > 0)
             continue;
         for (int i = tid; i < a.Hq * (a.c.D / 8); i += kThreads) {
             const int h = i / (a.c.D / 8), c = i % (a.c.D / 8);
@@ -344,8 +365,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         return;
 
     Cursor<SL> c, ahead;
-    c.enter(a, begin_sh[0]);
-    c.head = begin_sh[1];
+    c.enter(a, begin_sh[0], a.c.lengths[begin_sh[0]]);
+    c.head = begin_sh[1] / tiles;
+    c.tile = begin_sh[1] - c.head * tiles;
     c.unit = begin_sh[2];
     ahead = c;
     const long long count = u1 - u0;
@@ -354,14 +376,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         k_scale = a.c.scale[0];
         v_scale = a.c.scale[1];
     }
+    int page = slice_page(a, ahead, warp, lane);
+    const auto send = [&](int to) {
+        const int key0 = slice_key(ahead, warp), head = ahead.head, its = page;
+        ahead.next(a, tiles);
+        page = slice_page(a, ahead, warp, lane);
+        load_slice<F>(a, key0, head, its, lane, ring + to * 2 * kTile);
+    };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        if (i < count) {
-            load_slice<D, DP, F8>(a, ahead, ahead.head / tiles, warp, lane, ring + i * 2 * kTile);
-            ahead.next(a, heads);
-        } else {
+        if (i < count)
+            send(i);
+        else
             copies_commit();
-        }
     }
 
     uint32_t q[KS][NB][2];
@@ -370,9 +397,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     bool fresh = true, whole_start = c.unit == 0;
     int stage = 0;
     for (long long u = 0; u < count; ++u) {
-        const int head = c.head / tiles, tile = c.head - head * tiles;
-        const int rows = min(kRows, a.G - tile * kRows);
-        const int q_head = head * a.G + tile * kRows;
+        const int rows = min(kRows, a.G - c.tile * kRows);
+        const int q_head = c.head * a.G + c.tile * kRows;
         if (fresh) {
             fresh = false;
             const uint8_t* qp = a.q.p + c.seq * a.q.row + q_head * a.q.head;
@@ -440,15 +466,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         // the next copies go where the slice before this one was
         copies_wait<kStages - 2>();
         __syncwarp();
-        {
-            const int to = stage == 0 ? kStages - 1 : stage - 1;
-            if (u + kStages - 1 < count) {
-                load_slice<D, DP, F8>(a, ahead, ahead.head / tiles, warp, lane, ring + to * 2 * kTile);
-                ahead.next(a, heads);
-            } else {
-                copies_commit();
-            }
-        }
+        if (u + kStages - 1 < count)
+            send(stage == 0 ? kStages - 1 : stage - 1);
+        else
+            copies_commit();
         const int x = c.unit * kWarps + warp;
         if (x < c.seen.n) {
             const uint32_t kb = ring + stage * 2 * kTile, vb = kb + kTile;
@@ -499,14 +520,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             };
             const bool all = key0 + SL <= c.seen.length &&
                              (key0 >= c.seen.low || key0 + SL <= c.seen.sinks);
-            uint32_t keep[2 * NK];      // of a pair of keys: which half of a register
 #pragma unroll
             for (int k = 0; k < 2 * NK; ++k) {
-                keep[k] = 0xffffffffu;
                 const bool mine = all || sees(key0 + 8 * k + g);
-                if (!all)
-                    keep[k] = (sees(key0 + 8 * k + 2 * t) ? 0xffffu : 0u) |
-                              (sees(key0 + 8 * k + 2 * t + 1) ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -514,6 +530,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                         float& z = s[k >> 1][n][2 * (k & 1) + e];
                         z = mine ? z * factor[n][e] : -INFINITY;
                     }
+            }
+            // values of keys that are not seen need not be finite, and nothing times NaN is NaN
+            if (!all) {
+                for (int r = lane; r < SL; r += 32)
+                    if (!sees(key0 + r))
+#pragma unroll
+                        for (int i = 0; i < F::pitch; i += 16)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + r * F::pitch + i),
+                                         "r"(0)
+                                         : "memory");
+                __syncwarp();
             }
             float used[NB][2], now[NB][2];
             bool moved = false;
@@ -564,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 }
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                const uint32_t keep0 = keep[2 * k], keep1 = keep[2 * k + 1];
                 if constexpr (F8) {
 #pragma unroll
                     for (int j = 0; j < KS; j += 2) {
@@ -573,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                                                  j + (lane >> 4)));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t b0 = b[2 * i] & keep0, b1 = b[2 * i + 1] & keep1;
+                            const uint32_t b0 = b[2 * i], b1 = b[2 * i + 1];
                             const uint32_t f[4] = {e4m3_half2(__byte_perm(b0, 0, 0x4420)),
                                                    e4m3_half2(__byte_perm(b0, 0, 0x4431)),
                                                    e4m3_half2(__byte_perm(b1, 0, 0x4420)),
@@ -589,10 +615,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                         uint32_t b[4];
                         ldm4_trans(b, vb + F::at(16 * k + 8 * (lane >> 4) + (lane & 7),
                                                  2 * j + (lane >> 3 & 1)));
-                        const uint32_t f[4] = {b[0] & keep0, b[1] & keep0, b[2] & keep1, b[3] & keep1};
 #pragma unroll
                         for (int n = 0; n < NB; ++n)
-                            mma<F::bf16>(o[j][n], f, p[k][n][0], p[k][n][1]);
+                            mma<F::bf16>(o[j][n], b, p[k][n][0], p[k][n][1]);
                     }
                 }
             }
@@ -702,14 +727,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                         // the block that has the item's last unit
                         const long long last = u0 + u + (c.units - 1 - c.unit);
                         const int end = (int)(((last + 1) * blocks - 1) / total);
-                        sp.desc[block] = make_int4(end - block + 1, c.seq, c.head, 0);
+                        sp.desc[block] = make_int4(end - block + 1, c.seq, c.head, c.tile);
                     }
                 }
             }
             fresh = true;
             whole_start = true;
         }
-        c.next(a, heads);
+        c.next(a, tiles);
     }
 }
 
@@ -719,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 constexpr int kJoinThreads = 256, kJoinAhead = 8;
 
 template <class D, int DP, bool F8, int NB>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Split sp, int tiles)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Split sp)
 {
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_trigger();
@@ -761,10 +786,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Spl
         }
         m = top;
     }
-    const int head = d.z / tiles, tile = d.z - head * tiles;
-    if (h >= min(kRows, a.G - tile * kRows))
+    if (h >= min(kRows, a.G - d.w * kRows))
         return;
-    const int q_head = head * a.G + tile * kRows + h;
+    const int q_head = d.z * a.G + d.w * kRows + h;
     const float v_scale = F8 && a.c.scale ? a.c.scale[1] : 1.0f;
     const float inv = l > 0.0f || l != l ? v_scale / l : 0.0f;
     uint8_t* to = a.out.p + d.y * a.out.row + q_head * a.out.head;
@@ -776,7 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Spl
 template <class D, int DP, bool F8, int NB>
 cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
-    constexpr int kSmem = kWarps * kStages * 2 * kTile + 2 * kRows * DP * 4;
+    constexpr int kSmem = kWarps * kStages * 2 * kTile + 2 * 8 * NB * DP * 4;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(decode_attention_kernel<D, DP, F8, NB>,
@@ -805,7 +829,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     e = launch_after(decode_attention_kernel<D, DP, F8, NB>, blocks, kThreads, kSmem, s, a, sp, tiles);
     if (e != cudaSuccess || sp.whole || blocks == 1)
         return e;
-    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)), kJoinThreads, 0, s, a, sp, tiles);
+    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)), kJoinThreads, 0, s, a, sp);
 }
 
 template <class D, bool F8>
