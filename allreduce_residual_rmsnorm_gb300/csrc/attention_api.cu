@@ -200,10 +200,10 @@ int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,
                      tokens, cache->sequences);
     if (q && (rc = check_heads(q_heads, a.c.heads)) != AR_OK)
         return rc;
-    if (q && (int64_t)q_heads + 2 * (int64_t)a.c.heads > INT_MAX / (AR_MAX_HEAD_DIM / 8))
-        return afail(AR_ERR_UNSUPPORTED, "q_heads %d", q_heads);
-    if (a.c.heads > INT_MAX / (4 * AR_MAX_HEAD_DIM))
-        return afail(AR_ERR_UNSUPPORTED, "heads %d", a.c.heads);
+    // below 2^28 pieces of a row
+    if ((q ? (int64_t)q_heads : 0) + 2 * (int64_t)a.c.heads >= 1 << 24)
+        return afail(AR_ERR_UNSUPPORTED, "q_heads %d and twice heads %d beyond 2^24 - 1", q ? q_heads : 0,
+                     a.c.heads);
     if (rot < 0 || rot % 16 != 0 || rot > a.c.D)
         return afail(AR_ERR_INVALID, "rot %d is not a multiple of 16 in 0..%d", rot, a.c.D);
     if (axes < 1 || axes > AR_MAX_AXES)
