@@ -376,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    // fills of the ring and of the queries' places that warp 8 sent for
+    uint32_t sent = 0, asked_for[2] = {0, 0};
     // The next item, by every lane of a warp or by one thread; false: none is left, or a wait gave up.
     Item w;
     uint32_t taken = 0;
@@ -466,14 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, bar_wait(qempty + 8 * t, (uses[t] - 1) & 1, bail,
                                                           kWaitQueryFree));
             __syncwarp();
-            if (!ok) {
-                // what this warp sent for has to land
-                for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i)
-                    bar_drain(full + 8 * (i % kStages), i / kStages & 1);
-                for (int t = 0; t < 2; ++t)
-                    if (uses[t])
-                        bar_drain(qfull + 8 * t, (uses[t] - 1) & 1);
-            }
+            sent = it;
+            asked_for[0] = uses[0];
+            asked_for[1] = uses[1];
         } else if (warp == 9) {
             if (elect_one()) {
                 constexpr bool bf16 = D::id == AR_DT_BF16;
@@ -576,10 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         it += then ? 2 : 1;
                     }
-                }
-                if (!ok) {
-                    mma_commit(done);
-                    bar_drain(done, 0);
                 }
             }
             __syncwarp();
@@ -823,6 +816,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Without a wait that gave up every product has been taken and every copy is consumed.
+    // With one, whichever warp's it was, both end here before the block does.
+    if (*static_cast<volatile int*>(&dead)) {
+        if (warp == 8) {
+            for (uint32_t i = sent < kStages ? 0 : sent - kStages; i < sent; ++i)
+                bar_drain(full + 8 * (i % kStages), i / kStages & 1);
+            for (int t = 0; t < 2; ++t)
+                if (asked_for[t])
+                    bar_drain(qfull + 8 * t, (asked_for[t] - 1) & 1);
+        } else if (warp == 9) {
+            if (elect_one())
+                mma_commit(done);
+            __syncwarp();
+            bar_drain(done, 0);
+        }
+    }
     if (warp == 9)
         tmem_free(tmem, 512);
 }
