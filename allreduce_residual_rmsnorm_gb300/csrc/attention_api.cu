@@ -277,14 +277,12 @@ int ar_fusion_prompt_attention(const ar_kv_cache* cache, const ar_head_rows* q,
                                   workspace, workspace_bytes, &a, &e4m3);
     if (rc != AR_OK)
         return rc;
-    if (e4m3)
-        return afail(AR_ERR_UNSUPPORTED, "prompts over a cache of E4M3");
     if (cache->sequences == 0 || tokens == 0)
         return AR_OK;
     if (!aligned(starts, 4))
         return afail(AR_ERR_INVALID, "starts NULL or misaligned");
     a.starts = starts;
-    return launched(launch_prompt_attention(dtype, a, static_cast<cudaStream_t>(stream)),
+    return launched(launch_prompt_attention(dtype, e4m3, a, static_cast<cudaStream_t>(stream)),
                     "prompt attention launch");
 }
 

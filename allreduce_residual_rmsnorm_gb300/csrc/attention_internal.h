@@ -44,7 +44,7 @@ struct AttentionArgs {
     uint64_t work_bytes;
 };
 cudaError_t launch_decode_attention(int dtype, bool e4m3, const AttentionArgs& a, cudaStream_t s);
-cudaError_t launch_prompt_attention(int dtype, const AttentionArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_attention(int dtype, bool e4m3, const AttentionArgs& a, cudaStream_t s);
 
 // tokens of a sequence that the table can hold
 __device__ __forceinline__ int clamp_length(const CacheArgs& c, int length)

@@ -150,14 +150,17 @@ bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64
     const EncodeTiled fn = encode_tiled();
     if (!fn)
         return false;
-    const CUtensorMapDataType type = dtype == AR_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const bool codes = dtype == AR_DT_E4M3;
+    const CUtensorMapDataType type = codes                 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == AR_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
     const cuuint64_t s[3] = {strides[0], strides[1], strides[2]};
     const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     return fn(map, type, 4, const_cast<void*>(base), d, s, b, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              codes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

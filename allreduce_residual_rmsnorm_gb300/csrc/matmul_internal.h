@@ -17,8 +17,8 @@ bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
 bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, int dtype,
                     uint32_t box_rows, uint32_t box_cols);
 
-// Rows of 16-bit heads as boxes of 64 elements, 128-byte swizzle, zeros outside.
-// Strides in bytes, of dimensions 1 to 3.
+// Rows of 16-bit heads as boxes of 64 elements in the 128-byte swizzle, or (dtype AR_DT_E4M3) of
+// codes as boxes as they lie; zeros outside.  Strides in bytes, of dimensions 1 to 3.
 bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64_t (&dims)[4],
                      const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 

@@ -14,6 +14,8 @@
 //   tensor memory: scores of tile 0, of tile 1, sums of tile 0, of tile 1, 128 columns each
 //   warps 0-3, 4-7: softmax and output of tile 0, 1;  warp 8: copies;  warp 9: products;
 //   warp 10: clears values that no row sees (what lies there need not be finite);
+//   warps 12-15, with a cache of E4M3: turn its codes, which the copies leave beside, into 16-bit
+//   keys and values (and clear what no row sees: warp 10 rests);
 //   warp 11: finds the items ahead of the others (each for itself took 1.5 us an item)
 //
 // Items (a pair of tiles and a head) are worked off by one block per SM: where there
@@ -28,10 +30,14 @@
 namespace arf {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kRows = 128, kKeys = 128, kGroup = 64;   // of a tile, of a step, of a group
-constexpr int kRegsLaunch = 168, kRegsFew = 88, kRegsMany = 208;
-static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * kRegsLaunch, "register shares");
+// Registers of a thread at launch, of warps 8 on, of warps 0-7.
+template <bool F8>
+struct Regs {
+    static constexpr int threads = F8 ? 512 : 384;
+    static constexpr int launch = F8 ? 128 : 168, few = F8 ? 56 : 88, many = F8 ? 200 : 208;
+    static_assert((threads / 32 - 8) * few + 8 * many <= threads / 32 * launch, "register shares");
+};
 constexpr float kLn2 = 0.693147181f;
 // How far (in powers of two) a row's maximum may grow before its sums are rescaled: weights
 // are then up to 2^growth, as exact as below 1.  fp16 weights end at 2^16; with bf16 ones the
@@ -43,12 +49,14 @@ __device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16
 enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
        kWaitCleared, kWaitItem, kWaitPlace };
 
-template <int DP>
+template <int DP, bool F8 = false>
 struct Shape {
     static constexpr int half = kRows * 128;        // bytes of 128 rows of 64 elements
     static constexpr int tile = half * (DP / 64);
-    static constexpr int stages = DP == 64 ? 8 : 4;
-    static constexpr int smem = (2 + stages) * tile + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
+    static constexpr int stages = F8 ? (DP == 64 ? 6 : 3) : DP == 64 ? 8 : 4;
+    static constexpr int raws = F8 ? (DP == 64 ? 4 : 2) : 0;   // places for codes
+    static constexpr int raw = kKeys * DP;
+    static constexpr int smem = (2 + stages) * tile + raws * raw + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
     static constexpr int part = 2 * kRows * (DP + 2) * 4;
 };
 // More than half of an SM's shared memory for every shape: no second block of this kernel
@@ -131,7 +139,6 @@ struct Item {
 };
 static_assert(sizeof(Item) == 64, "copied as four vectors");
 constexpr uint32_t kItems = 4;                      // found ahead
-constexpr int kTakers = 11;                         // warps 0-10
 
 // The items of a block, one after the other.
 struct Walk {
@@ -197,41 +204,78 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
     return r;
 }
 
+// what a value's code is multiplied with
+template <bool F8>
+__device__ __forceinline__ float value_scale(const AttentionArgs& a)
+{
+    return F8 && a.c.scale ? a.c.scale[1] : 1.0f;
+}
 // the lowest n of 32 bits
 __device__ __forceinline__ uint32_t below(int n)
 {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
 }
 
-template <class D, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+// 16 E4M3 codes as 16-bit elements (exact; a NaN stays one)
+template <class D>
+__device__ __forceinline__ void widen(const uint4& codes, uint4& lo, uint4& hi)
+{
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint16_t two = (uint16_t)(c[i / 2] >> (16 * (i & 1)));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        if constexpr (D::id == AR_DT_BF16) {
+            const float2 f = unpack2<Fp16>(h);
+            h = pack2<Bf16>(f.x, f.y);
+        }
+        w[i] = h;
+    }
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void put16(uint32_t to, const uint4& v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+template <class D, int DP, bool F8>
+__global__ void __launch_bounds__(Regs<F8>::threads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k,
                             const __grid_constant__ CUtensorMap map_v, AttentionArgs a, Plan plan,
                             int* status)
 {
-    using F = Shape<DP>;
-    constexpr uint32_t kStages = F::stages;
+    using F = Shape<DP, F8>;
+    constexpr uint32_t kStages = F::stages, kRaws = F8 ? F::raws : 1;
+    constexpr int kThreads = Regs<F8>::threads;
+    constexpr int kTakers = F8 ? 14 : 11;           // warps that take items
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 7 + 1 + 2 * kItems];
+    __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 7 + 1 + 2 * kItems + 2 * kRaws];
     __shared__ __align__(16) Item item_sh[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, begin_sh[2];
     __shared__ long long scan_sh[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t q_at = (smem_u32(dyn) + 1023u) & ~1023u, ring = q_at + 2 * F::tile;
-    int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile);
+    int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile +
+                                             F::raws * F::raw);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
                    wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
                    pfull = sfull + 16, ofull = pfull + 32, ofree = ofull + 16,
                    done = ofree + 16,
-                   ifull = done + 8, iempty = ifull + 8 * kItems;
+                   ifull = done + 8, iempty = ifull + 8 * kItems, rfull = iempty + 8 * kItems,
+                   rempty = rfull + 8 * kRaws, raw_at = ring + kStages * F::tile;
     const Bail bail{smem_u32(&dead), status};
 
     if (tid == 0) {
         dead = 0;
         for (uint32_t s = 0; s < kStages; ++s) {
-            bar_init(full + 8 * s, 1);
+            bar_init(full + 8 * s, F8 ? 4 : 1);
             bar_init(empty + 8 * s, 1);
             bar_init(cleared + 8 * s, 1);
             bar_init(wanted + 8 * s, 1);
@@ -246,6 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(ofree + 8 * t, 4);
         }
         bar_init(done, 1);
+        for (uint32_t i = 0; F8 && i < kRaws; ++i) {
+            bar_init(rfull + 8 * i, 1);
+            bar_init(rempty + 8 * i, 4);
+        }
         for (uint32_t i = 0; i < kItems; ++i) {
             bar_init(ifull + 8 * i, 1);
             bar_init(iempty + 8 * i, kTakers);
@@ -398,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w.x1 > w.x0;
     };
     if (warp >= 8) {
-        regs_fewer<kRegsFew>();
+        regs_fewer<Regs<F8>::few>();
         if (warp == 8) {
             // copies: per item the first keys, the queries, then values and keys in turn
             uint32_t it = 0, uses[2] = {0, 0};
@@ -418,19 +466,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int row = page == a.c.pages ? 0 : key & ((1 << a.c.page_shift) - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
-                        const uint32_t s = it % kStages;
-                        ok = bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
+                        const uint32_t s = F8 ? it % kRaws : it % kStages;
+                        ok = F8 ? bar_wait(rempty + 8 * s, (it / kRaws & 1) ^ 1, bail, kWaitStage)
+                                : bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok)
                             break;
                         if (lane == 0)
-                            bar_expect(full + 8 * s, F::tile);
+                            bar_expect((F8 ? rfull : full) + 8 * s, F8 ? F::raw : F::tile);
                         __syncwarp();
                         // at most 16 boxes a half of the tile
-                        const uint32_t to = ring + s * F::tile + in * 128;
-                        for (int h = part; h < DP / 64; h += 32 / boxes)
-                            tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
-                                        row, w.head, page);
+                        if constexpr (F8) {
+                            if (part == 0)
+                                tma_load_4d(raw_at + s * F::raw + in * DP, kv ? &map_v : &map_k,
+                                            rfull + 8 * s, 0, row, w.head, page);
+                        } else {
+                            const uint32_t to = ring + s * F::tile + in * 128;
+                            for (int h = part; h < DP / 64; h += 32 / boxes)
+                                tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
+                                            row, w.head, page);
+                        }
                         __syncwarp();
                         // the queries behind the first keys: their place is free later
                         if (x == w.x0 && kv == 0) {
@@ -453,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                             }
                         }
-                        if (kv && lane == 0 && step_has_unseen(w.p, x))
+                        if (!F8 && kv && lane == 0 && step_has_unseen(w.p, x))
                             bar_arrive(wanted + 8 * s);
                     }
                 }
@@ -519,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // values of this step: stage it; keys of the next, of the next item behind
                         // the last step: it + 1
                         const uint32_t sv = it % kStages, now = tiles;
-                        const bool last = x + 1 == x1, unseen = step_has_unseen(w.p, x);
+                        const bool last = x + 1 == x1, unseen = !F8 && step_has_unseen(w.p, x);
                         uint32_t then = tiles;
                         bool next_last = x + 2 == x1;
                         if (last) {
@@ -576,7 +631,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == 10) {
+        } else if (F8 && warp >= 12) {
+            // 16 codes a lane at a time, of 32 keys a warp
+            constexpr int kLanes = DP / 16, kStep = 32 / kLanes;    // lanes of a key, keys at a time
+            const int chunk = lane % kLanes;
+            uint32_t it = 0;
+            while (ok && take(true)) {
+                for (int x = w.x0; x < w.x1 && ok; ++x) {
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const uint32_t r = it % kRaws, s = it % kStages;
+                        ok = bar_wait(rfull + 8 * r, it / kRaws & 1, bail, kWaitKeys) &&
+                             bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok)
+                            break;
+                        const int key0 = key_of(w.p, 2 * x + (warp - 12) / 2) + 32 * (warp & 1);
+#pragma unroll
+                        for (int i = 0; i < 32 / kStep; ++i) {
+                            const int in = kStep * i + lane / kLanes, at = 32 * (warp - 12) + in;
+                            uint4 c, lo, hi;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                                         : "r"(raw_at + r * F::raw + at * DP + 16 * chunk)
+                                         : "memory");
+                            const int key = key0 + in;
+                            // values that no row sees need not be finite
+                            if (kv && !(key < w.p.end && (key >= w.p.low || key < w.p.sinks)))
+                                c = make_uint4(0, 0, 0, 0);
+                            widen<D>(c, lo, hi);
+                            const uint32_t to = ring + s * F::tile + chunk / 4 * F::half + at * 128;
+                            const int c0 = chunk % 4 * 2;
+                            put16(to + ((c0 ^ (at & 7)) << 4), lo);
+                            put16(to + (((c0 + 1) ^ (at & 7)) << 4), hi);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            bar_arrive(full + 8 * s);
+                            bar_arrive(rempty + 8 * r);
+                        }
+                    }
+                }
+            }
+        } else if (!F8 && warp == 10) {
             // Values of keys that no row of the pair sees.  The copies say which stage it is: by
             // then the stage's fill before this one is over, so that the wait for the fill is not
             // answered by an older one.
@@ -609,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bar_arrive(cleared + 8 * s);
                 }
             }
-        } else if (lane == 0) {
+        } else if (warp == 11 && lane == 0) {
             // the items, and one without tiles behind the last
             for (uint32_t i = 0; ok; ++i) {
                 if (!(ok = bar_wait(iempty + 8 * (i % kItems), (i / kItems & 1) ^ 1, bail, kWaitPlace)))
@@ -623,16 +720,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more)
                     break;
             }
-            __syncwarp(1u);
         }
+        __syncwarp();
     } else {
-        regs_more<kRegsMany>();
+        regs_more<Regs<F8>::many>();
         // A wait that gives up is not looked at here: what is stored is then undefined, within the
         // output, and every later wait returns at once.
         const int t = warp >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
         const int in = r / a.G, g = r - in * a.G;       // token of the tile, head of the group
+        const float scale_log2 = a.scale_log2 * (F8 && a.c.scale ? a.c.scale[0] : 1.0f);
         uint32_t seen = 0, items = 0;
         // the item whose sums are still to be read
         bool held = false;
@@ -645,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             tc_fence_after();
             const bool live = held_row >= 0;
-            const float inv = held_sum > 0.0f || held_sum != held_sum ? 1.0f / held_sum : 0.0f;
+            const float inv = held_sum > 0.0f || held_sum != held_sum ? value_scale<F8>(a) / held_sum : 0.0f;
             // a warp whose rows are of no token has nothing to say
             const bool any = __any_sync(0xffffffffu, live);
 #pragma unroll 1
@@ -752,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 12; c < kKeys; c += 2)
                     m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale_log2;
+                const float best = fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale_log2;
                 if (__builtin_expect(__any_sync(0xffffffffu, best > top + growth<D>()), 0)) {
                     const float now = best > top + growth<D>() ? best : top;
                     const float f = now == top ? 1.0f : exp2_fast(top - now);
@@ -773,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // The products of the first half of the weights begin while the second half is made.
                 const float used = top == -INFINITY ? 0.0f : top;
-                const uint64_t scale = pair_of(a.scale_log2, a.scale_log2), minus = pair_of(-used, -used);
+                const uint64_t scale = pair_of(scale_log2, scale_log2), minus = pair_of(-used, -used);
                 uint64_t part[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -820,8 +918,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // With one, whichever warp's it was, both end here before the block does.
     if (*static_cast<volatile int*>(&dead)) {
         if (warp == 8) {
-            for (uint32_t i = sent < kStages ? 0 : sent - kStages; i < sent; ++i)
-                bar_drain(full + 8 * (i % kStages), i / kStages & 1);
+            constexpr uint32_t kPlaces = F8 ? kRaws : kStages;
+            for (uint32_t i = sent < kPlaces ? 0 : sent - kPlaces; i < sent; ++i)
+                bar_drain((F8 ? rfull : full) + 8 * (i % kPlaces), i / kPlaces & 1);
             for (int t = 0; t < 2; ++t)
                 if (asked_for[t])
                     bar_drain(qfull + 8 * t, (asked_for[t] - 1) & 1);
@@ -887,7 +986,7 @@ __global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan p
         }
         m = top;
     }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const float inv = l > 0.0f || l != l ? value_scale<true>(a) / l : 0.0f;     // no scale: 1
     const int row = d.y + token, h = d.w * a.G + g;
 #pragma unroll
     for (int e = 0; e < kJoinDims; ++e)
@@ -900,10 +999,10 @@ __global__ void __launch_bounds__(2 * kRows) join_kernel(AttentionArgs a, Plan p
 // the stride of an extent of one: any multiple of 16
 uint64_t stride_of(int64_t stride) { return stride ? (uint64_t)stride : 16u; }
 
-template <class D, int DP>
+template <class D, int DP, bool F8>
 cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
-    constexpr int smem = Shape<DP>::smem > kLeastSmem ? Shape<DP>::smem : kLeastSmem;
+    constexpr int smem = Shape<DP, F8>::smem > kLeastSmem ? Shape<DP, F8>::smem : kLeastSmem;
     static_assert(smem <= 227 * 1024 - 2048, "shared memory");
     Plan plan{};
     plan.tok = kRows / a.G;
@@ -911,26 +1010,28 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     const uint64_t D_ = (uint64_t)a.c.D;
     const uint32_t page = 1u << a.c.page_shift, box = page < (uint32_t)kGroup ? page : kGroup;
     CUtensorMap map_q, map_k, map_v;
+    const int type = F8 ? (int)AR_DT_E4M3 : D::id;
+    const uint32_t wide = F8 ? DP : 64;
     if (!rows_tensor_map(&map_q, D::id, a.q.p, {D_, (uint64_t)a.G, (uint64_t)a.c.heads, (uint64_t)a.T},
                          {stride_of(a.q.head), stride_of(a.q.head * a.G), stride_of(a.q.row)},
                          {64, (uint32_t)a.G, 1, (uint32_t)plan.tok}) ||
-        !rows_tensor_map(&map_k, D::id, a.c.k, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
+        !rows_tensor_map(&map_k, type, a.c.k, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
                          {stride_of(a.c.k_row), stride_of(a.c.k_head), stride_of(a.c.k_page)},
-                         {64, box, 1, 1}) ||
-        !rows_tensor_map(&map_v, D::id, a.c.v, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
+                         {wide, box, 1, 1}) ||
+        !rows_tensor_map(&map_v, type, a.c.v, {D_, page, (uint64_t)a.c.heads, (uint64_t)a.c.pages},
                          {stride_of(a.c.v_row), stride_of(a.c.v_head), stride_of(a.c.v_page)},
-                         {64, box, 1, 1}))
+                         {wide, box, 1, 1}))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         // fewer registers at launch than the shares add up to would wait for ever
         cudaFuncAttributes attr;
-        const cudaError_t ea = cudaFuncGetAttributes(&attr, prompt_attention_kernel<D, DP>);
+        const cudaError_t ea = cudaFuncGetAttributes(&attr, prompt_attention_kernel<D, DP, F8>);
         if (ea != cudaSuccess)
             return ea;
-        if (attr.numRegs < kRegsLaunch)
+        if (attr.numRegs < Regs<F8>::launch)
             return cudaErrorLaunchOutOfResources;
-        return cudaFuncSetAttribute(prompt_attention_kernel<D, DP>,
+        return cudaFuncSetAttribute(prompt_attention_kernel<D, DP, F8>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess)
@@ -955,24 +1056,30 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         plan.desc = reinterpret_cast<int4*>(a.work);
         plan.parts = a.work + 16 * (int64_t)blocks;
     }
-    e = launch_after(prompt_attention_kernel<D, DP>, blocks, kThreads, smem, s, map_q, map_k, map_v, a,
+    e = launch_after(prompt_attention_kernel<D, DP, F8>, blocks, Regs<F8>::threads, smem, s, map_q, map_k, map_v, a,
                      plan, d.status + kStatusWords);
     if (e != cudaSuccess || plan.whole || blocks == 1)
         return e;
     return launch_after(join_kernel<D, DP>, dim3(blocks, DP / kJoinDims), 2 * kRows, 0, s, a, plan);
 }
 
+template <class D>
+cudaError_t launch_d(bool e4m3, const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
+{
+    if (a.c.D <= 64)
+        return e4m3 ? launch_t<D, 64, true>(a, d, s) : launch_t<D, 64, false>(a, d, s);
+    return e4m3 ? launch_t<D, 128, true>(a, d, s) : launch_t<D, 128, false>(a, d, s);
+}
+
 }  // namespace
 
-cudaError_t launch_prompt_attention(int dtype, const AttentionArgs& a, cudaStream_t s)
+cudaError_t launch_prompt_attention(int dtype, bool e4m3, const AttentionArgs& a, cudaStream_t s)
 {
     DeviceInfo d;
     const cudaError_t e = device_info(&d);
     if (e != cudaSuccess)
         return e;
-    if (dtype == AR_DT_BF16)
-        return a.c.D <= 64 ? launch_t<Bf16, 64>(a, d, s) : launch_t<Bf16, 128>(a, d, s);
-    return a.c.D <= 64 ? launch_t<Fp16, 64>(a, d, s) : launch_t<Fp16, 128>(a, d, s);
+    return dtype == AR_DT_BF16 ? launch_d<Bf16>(e4m3, a, d, s) : launch_d<Fp16>(e4m3, a, d, s);
 }
 
 }  // namespace arf

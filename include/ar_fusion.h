@@ -752,7 +752,7 @@ int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
  * own index.
  *   q, out     [tokens][q_heads];  lse [tokens][q_heads] or NULL
  *   starts     device int32 [sequences + 1]
- * AR_DT_E4M3 caches are refused.  An infinite or NaN value of a key that one token of a
+ * An infinite or NaN value of a key that one token of a
  * sequence sees also reaches tokens next to it that do not see that key.
  * Device-side waits are bounded (2 s each); one that gives up leaves the outputs undefined
  * and is reported by ar_fusion_attention_status.

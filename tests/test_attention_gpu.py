@@ -270,8 +270,8 @@ def test_decode_same_bits_again(workspace):
 # ------------------------------------------------------------------ prompts
 
 def check_prompt(new, lengths, P, H, K, D, dtype, workspace, window=0, sinks=0, scale=None, hnd=False,
-                 seed=5, lse=True, factor=1.0, table=None, first=0, behind=0):
-    pages = R.Pages(lengths, P, K, D, dtype, seed=seed, hnd=hnd, extra=1)
+                 seed=5, lse=True, factor=1.0, table=None, first=0, behind=0, cache=None):
+    pages = R.Pages(lengths, P, K, D, cache or dtype, seed=seed, hnd=hnd, extra=1)
     if table is not None:
         table(pages.table)
     T = first + sum(new) + behind
@@ -279,17 +279,17 @@ def check_prompt(new, lengths, P, H, K, D, dtype, workspace, window=0, sinks=0, 
     q = (factor * torch.randn(T, H + 2 * K, D, generator=gen(seed + 1))).to(dtype)
     dq = q.cuda()[:, :H]
     q = q[:, :H]
-    kc, vc, dev_table, dev_lengths, _ = pages.cuda()
+    kc, vc, dev_table, dev_lengths, kv_scale = pages.cuda()
     out = torch.full((T, H, D + 8), 5.0, dtype=dtype, device="cuda")
     L = torch.full((T, H), 5.0, device="cuda") if lse else None
     if workspace is not None:
         workspace.fill_(255)
     B.ar_fusion_prompt_attention(dq, kc, vc, dev_table, dev_lengths, starts.cuda(), out[:, :, :D],
-                                 workspace, scale=scale, window=window, sinks=sinks, lse=L)
+                                 workspace, scale=scale, window=window, sinks=sinks, lse=L, kv_scale=kv_scale)
     torch.cuda.synchronize()
     assert B.ar_fusion_attention_status() == (B.AR_OK, -1)
     want = R.attention(q, pages.view(pages.k), pages.view(pages.v), pages.table, pages.lengths,
-                       starts, D ** -0.5 if scale is None else scale, window, sinks)
+                       starts, D ** -0.5 if scale is None else scale, window, sinks, pages.scales)
     R.check_attention(out[:, :, :D], L, want, dtype, dtype, splits=40)
     dead = torch.isnan(want[4][:, 0])
     assert bool((out[:, :, D:] == 5.0).all()) and bool((out.cpu()[dead] == 5.0).all())
@@ -303,6 +303,26 @@ def check_prompt(new, lengths, P, H, K, D, dtype, workspace, window=0, sinks=0, 
                                    (16, 1, 16), (33, 1, 128), (128, 1, 64)])
 def test_prompt(workspace, H, K, D, dtype):
     check_prompt([1, 0, 5, 64, 130, 33], [1, 4, 300, 64, 130, 200], 16, H, K, D, dtype, workspace)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("H,K,D", [(8, 1, 128), (8, 8, 128), (14, 2, 64), (15, 3, 80), (40, 2, 96),
+                                   (16, 1, 16), (33, 1, 128), (128, 1, 64)])
+def test_prompt_e4m3(workspace, H, K, D, dtype):
+    check_prompt([1, 0, 5, 64, 130, 33], [1, 4, 300, 64, 130, 200], 16, H, K, D, dtype, workspace,
+                 cache=E4M3)
+    check_prompt([70, 40], [300, 900], 8, H, K, D, dtype, workspace, 100, 9, hnd=True, cache=E4M3)
+    check_prompt([3, 100, 9], [5, 90, 3000], 128, H, K, D, dtype, None, cache=E4M3, behind=2)
+
+
+def test_prompt_e4m3_long_and_bad_pages(workspace):
+    def some(table):
+        table[0, 1], table[0, 3], table[1, 0] = -1, 1 << 29, -(1 << 31)
+    for dtype in (BF16, FP16):
+        check_prompt([100, 20, 2], [100, 20, 50], 16, 8, 2, 128, dtype, workspace, table=some, cache=E4M3)
+        check_prompt([3], [9011], 64, 8, 1, 128, dtype, workspace, cache=E4M3)
+        check_prompt([700], [1500], 64, 2, 1, 64, dtype, workspace, factor=20.0, cache=E4M3)
+        check_prompt([600], [600], 64, 6, 3, 64, dtype, workspace, 1024, 0, cache=E4M3)
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (16, 0), (33, 16), (100, 17), (64, 500),

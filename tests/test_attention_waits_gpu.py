@@ -42,19 +42,20 @@ def status(L):
 @pytest.mark.parametrize("new,lengths,H,K,D,window,sinks", [
     ([300, 1, 40], [300, 500, 900], 8, 2, 128, 0, 0), ([700], [700], 64, 8, 128, 100, 5),
     ([5000], [5000], 32, 8, 64, 0, 0), ([4, 3], [3000, 2000], 8, 1, 64, 0, 0)])
-def test_prompts_whose_waits_give_up_at_once(hasty, new, lengths, H, K, D, window, sinks):
-    pages = R.Pages(lengths, 64, K, D, torch.bfloat16, junk=False)
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float8_e4m3fn])
+def test_prompts_whose_waits_give_up_at_once(hasty, new, lengths, H, K, D, window, sinks, cache):
+    pages = R.Pages(lengths, 64, K, D, cache, junk=False)
     T = sum(new)
     starts = torch.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32).cuda()
     g = torch.Generator()
     g.manual_seed(3)
     q = torch.randn(T, H, D, generator=g).to(torch.bfloat16).cuda()
-    kc, vc, table, dev_lengths, _ = pages.cuda()
+    kc, vc, table, dev_lengths, kv_scale = pages.cuda()
     work = torch.empty(B.AR_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
     want, want_lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
 
     def call(L, out, lse):
-        cache = B._kv_cache(kc, vc, table, dev_lengths, None)
+        cache = B._kv_cache(kc, vc, table, dev_lengths, kv_scale)
         rows = [B._HeadRows(t.data_ptr(), t.stride(0), t.stride(1)) for t in (q, out)]
         assert L.ar_fusion_prompt_attention(
             cache, *rows, lse.data_ptr(), starts.data_ptr(), T, H, B.AR_DT_BF16, D ** -0.5, window,
