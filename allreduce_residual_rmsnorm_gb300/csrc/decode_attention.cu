@@ -30,11 +30,17 @@ namespace arf {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
 constexpr int kTile = 4096;             // bytes of keys, and of values, of a slice
 constexpr int kRows = 16;               // query heads of an item
-constexpr int kBlocksPerSm = 2;
 constexpr float kLn2 = 0.693147181f;
+
+// Blocks on an SM and slices in a warp's ring.  Two of three slices hold more bytes in flight than
+// three of two; but the codes of an E4M3 slice of the same bytes are twice the work, and want
+// the warps (147 -> 133 us, 5.5 -> 6.1 TB/s; 16 bits 83.4 -> 88.0 the other way, 131072 tokens).
+template <bool F8, int NB>
+struct Fit {
+    static constexpr int blocks = F8 && NB == 1 ? 3 : 2, stages = F8 && NB == 1 ? 2 : 3;
+};
 
 struct Split {
     int4* desc;                         // [blocks]: parts, sequence, head, tile
@@ -250,11 +256,11 @@ __device__ __forceinline__ void store_dims(uint8_t* to, int dims, int j, int g, 
 }
 
 template <class D, int DP, bool F8, int NB>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
     decode_attention_kernel(AttentionArgs a, Split sp, int tiles)
 {
     using F = Form<D, DP, F8>;
-    constexpr int SL = F::SL, NK = SL / 16, KS = DP / 16;
+    constexpr int SL = F::SL, NK = SL / 16, KS = DP / 16, kStages = Fit<F8, NB>::stages;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ float max_sh[kWarps][kRows], sum_sh[kWarps][kRows];
     __shared__ long long scan_sh[kWarps], where_sh[2];
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Spl
 template <class D, int DP, bool F8, int NB>
 cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
-    constexpr int kSmem = kWarps * kStages * 2 * kTile + 2 * 8 * NB * DP * 4;
+    constexpr int kSmem = kWarps * Fit<F8, NB>::stages * 2 * kTile + 2 * 8 * NB * DP * 4;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(decode_attention_kernel<D, DP, F8, NB>,
@@ -813,7 +819,7 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     constexpr int unit = kWarps * Form<D, DP, F8>::SL;
     const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
     const int64_t most = ((keys + unit - 1) / unit) * a.c.S * a.c.heads * tiles;
-    int blocks = kBlocksPerSm * d.sms;
+    int blocks = Fit<F8, NB>::blocks * d.sms;
     if (most < blocks)
         blocks = (int)most;
     // the workspace: a line for each block, then its two parts

@@ -54,7 +54,7 @@ struct Shape {
     static constexpr int half = kRows * 128;        // bytes of 128 rows of 64 elements
     static constexpr int tile = half * (DP / 64);
     static constexpr int stages = F8 ? (DP == 64 ? 6 : 3) : DP == 64 ? 8 : 4;
-    static constexpr int raws = F8 ? (DP == 64 ? 4 : 2) : 0;   // places for codes
+    static constexpr int raws = F8 ? (DP == 64 ? 4 : 3) : 0;   // places for codes
     static constexpr int raw = kKeys * DP;
     static constexpr int smem = (2 + stages) * tile + raws * raw + (AR_MAX_SEQUENCES + 1) * 4 + 1024;
     static constexpr int part = 2 * kRows * (DP + 2) * 4;
