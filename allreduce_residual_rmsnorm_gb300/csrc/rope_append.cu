@@ -6,10 +6,10 @@
 // so that both halves of 8 pairs are in its registers.  Every element is read once
 // and written once.  The row's place (its sequence, length and page) is a chain of
 // three loads, and the elements do not wait for it: the first kAhead pieces of
-// every thread are loaded before it.  Memory bounds it: 4 x 2048 rows of 32 + 8 + 8 heads
-// 36.5 us, 5.5 TB/s (stores without the streaming hint 38.0, without the bound on registers,
-// 7 blocks on an SM, 38.7, blocks of 64, 96, 192 and 256 threads 42.8, 37.3, 39.2, 51); 64 rows
-// of 8 + 1 + 1 heads 2.3, a launch.
+// every thread are loaded before it.  What bounds it is memory and the latency of that chain (8
+// rows on an SM at a time): 4 x 2048 rows of 32 + 8 + 8 heads 35.9 us, 5.6 TB/s (stores without
+// the streaming hint 4% more, 7 blocks on an SM 5%, blocks of 64, 96, 192 and 256 threads 17, 2,
+// 7 and 40%); 64 rows of 8 + 1 + 1 heads 2.1, a launch.
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "expert_vec.cuh"
@@ -67,7 +67,7 @@ template <class D, bool F8, int kAhead>
 __global__ void __launch_bounds__(kThreads, kAhead == kMostAhead ? 8 : 0)
     rope_append_kernel(RopeArgs a, Heads turning, Heads copying)
 {
-    __shared__ float2 cs[AR_MAX_HEAD_DIM / 2];
+    __shared__ __align__(16) float2 cs[AR_MAX_HEAD_DIM / 2];
     __shared__ int found, place[2];
     const int row = blockIdx.x, tid = threadIdx.x;
     if (tid == 0)
@@ -120,6 +120,22 @@ __global__ void __launch_bounds__(kThreads, kAhead == kMostAhead ? 8 : 0)
         hi = a.starts[tid + 1];
         length = a.c.lengths[tid];
     }
+    // what the turns need beside the place
+    float freq = 0.0f, inverse[2] = {1.0f, 1.0f};
+    int where = 0;
+    if (tid < a.rot / 2) {
+        freq = a.inv_freq[tid];
+        if (a.positions) {
+            int axis = 0;
+            while (tid >= a.ends[axis])     // ends[axes - 1] is rot / 2
+                ++axis;
+            where = a.positions[(int64_t)axis * a.T + row];
+        }
+    }
+    if (F8 && a.c.scale) {
+        inverse[0] = a.c.scale[0];
+        inverse[1] = a.c.scale[1];
+    }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
         const Piece p = pieces[j] = piece(tid + j * kThreads);
@@ -157,18 +173,10 @@ __global__ void __launch_bounds__(kThreads, kAhead == kMostAhead ? 8 : 0)
     }
     const bool placed = page >= 0 && page < a.c.pages;
     const int in_page = index & ((1 << a.c.page_shift) - 1);
-    if (tid < a.rot / 2) {
-        int axis = 0;
-        while (tid >= a.ends[axis])     // ends[axes - 1] is rot / 2
-            ++axis;
-        const int at = a.positions ? a.positions[(int64_t)axis * a.T + row] : index;
-        cs[tid] = turn(at, a.inv_freq[tid]);
-    }
-    float inverse[2] = {1.0f, 1.0f};
-    if (F8 && a.c.scale) {
-        inverse[0] = 1.0f / a.c.scale[0];
-        inverse[1] = 1.0f / a.c.scale[1];
-    }
+    if (tid < a.rot / 2)
+        cs[tid] = turn(a.positions ? where : index, freq);
+    inverse[0] = 1.0f / inverse[0];
+    inverse[1] = 1.0f / inverse[1];
     __syncthreads();
 
     const auto finish = [&](const Piece& p, const uint4& x0, const uint4& x1) {
@@ -180,11 +188,13 @@ __global__ void __launch_bounds__(kThreads, kAhead == kMostAhead ? 8 : 0)
             unpack8<D>(x1, f[1]);
         if (p.pair >= 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 c = cs[p.pair + e];
-                const float u = f[0][e], w = f[1][e];
-                f[0][e] = fmaf(u, c.x, -(w * c.y));
-                f[1][e] = fmaf(w, c.x, u * c.y);
+            for (int e = 0; e < 8; e += 2) {        // two pairs' cosines and sines a load
+                const float4 c = *reinterpret_cast<const float4*>(&cs[p.pair + e]);
+                const float u0 = f[0][e], w0 = f[1][e], u1 = f[0][e + 1], w1 = f[1][e + 1];
+                f[0][e] = fmaf(u0, c.x, -(w0 * c.y));
+                f[1][e] = fmaf(w0, c.x, u0 * c.y);
+                f[0][e + 1] = fmaf(u1, c.z, -(w1 * c.w));
+                f[1][e + 1] = fmaf(w1, c.z, u1 * c.w);
             }
         } else if (a.interleaved && p.kind < 2) {
 #pragma unroll
@@ -243,7 +253,7 @@ Heads heads_of(unsigned per)
 }
 
 // As many pieces ahead as the row gives a thread: those that are not there cost as much as the
-// others (7.2 instead of 3.9 us at 1479 rows of 15 + 5 heads).
+// others (7.2 instead of 4.0 us at 1479 rows of 15 + 5 + 5 heads of 80).
 template <class D, bool F8>
 cudaError_t launch_t(const RopeArgs& a, cudaStream_t s)
 {
