@@ -84,16 +84,6 @@ __device__ __forceinline__ int key_of(const Pair& p, int g)
 {
     return g < p.groups ? (g < p.first ? g : g + p.gap) * kGroup : p.end;
 }
-// whether a group holds keys that no row of the pair sees
-__device__ __forceinline__ bool has_unseen(const Pair& p, int key0)
-{
-    return key0 + kGroup > p.end || (key0 < p.low && key0 + kGroup > p.sinks);
-}
-__device__ __forceinline__ bool step_has_unseen(const Pair& p, int x)
-{
-    return has_unseen(p, key_of(p, 2 * x)) || has_unseen(p, key_of(p, 2 * x + 1));
-}
-
 // tokens of a sequence in the call
 __device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
 {
@@ -106,6 +96,7 @@ __device__ __forceinline__ int rows_of(const AttentionArgs& a, int s, int* row0)
 __device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const int* first_pair, int f)
 {
     int lo = 0, hi = a.c.S;
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (first_pair[mid] <= f)
@@ -132,19 +123,21 @@ __device__ __forceinline__ Pair pair_at(const AttentionArgs& a, int tok, const i
 }
 
 // What a block does next: steps x0 .. x1 - 1 of a pair for a head (none: nothing left);
-// where the item begins here and ends in another block, that block.
-struct Item {
+// where the item begins here and ends in another block, that block.  Steps clear0 .. clear1 - 1
+// hold no key that no row sees.
+struct alignas(16) Item {
     Pair p;
-    int head, x0, x1, end_block, pad;
+    int head, x0, x1, end_block, clear0, clear1;
+
+    __device__ __forceinline__ bool has_unseen(int x) const { return x < clear0 || x >= clear1; }
 };
-static_assert(sizeof(Item) == 64, "copied as four vectors");
 constexpr uint32_t kItems = 4;                      // found ahead
 
 // The items of a block, one after the other.
 struct Walk {
     int item, items, x, step;   // whole items: `step` counts them
-    long long left;             // of a share: units left
-    long long end, total;       // of a share: where it ends in the list, and the list
+    int left;                   // of a share: units left
+    int end, total;             // of a share: where it ends in the list, and the list
     int blocks;
 
     __device__ __forceinline__ bool next(const AttentionArgs& a, const Plan& plan, const int* first_pair,
@@ -170,20 +163,48 @@ struct Walk {
             to->head = item - f * a.c.heads;
             to->p = pair_at(a, plan.tok, first_pair, f);
             to->x0 = x;
-            to->x1 = plan.whole ? to->p.n : (int)min((long long)to->p.n, x + left);
+            to->x1 = plan.whole ? to->p.n : min(to->p.n, x + left);
             to->end_block = 0;
             if (!plan.whole) {
                 left -= to->x1 - x;
                 ++item;
                 x = 0;
                 if (to->x1 < to->p.n)       // the block that has the item's last unit
-                    to->end_block = (int)(((end + (to->p.n - to->x1)) * blocks - 1) / total);
+                    to->end_block =
+                        (int)(((long long)(end + (to->p.n - to->x1)) * blocks - 1) / total);
             }
+            to->clear0 = ((to->p.low + kGroup - 1) / kGroup - to->p.gap + 1) / 2;
+            to->clear1 = (to->p.end / kGroup - to->p.gap) / 2;
             if (to->x1 > to->x0)
                 return true;
         }
     }
 };
+
+// bar_wait in fewer instructions: there are two dozen of them, and with what records the error in
+// each the kernel's code did not stay in the instruction caches.  The block's flag holds which
+// wait gave up; the end of the kernel records it.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t dead, int where)
+{
+    if (bar_try(bar, parity))
+        return true;
+    uint32_t t0, t, gave_up;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+    for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
+        if (n % ARF_WAIT_TRIES)
+            continue;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gave_up) : "r"(dead) : "memory");
+        if (gave_up)
+            return false;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        if (t - t0 > (uint32_t)ARF_WAIT_NS) {
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(where) : "memory");
+            return false;
+        }
+    }
+    return true;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -256,10 +277,10 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     constexpr int kTakers = F8 ? 14 : 11;           // warps that take items
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t bars[4 * F::stages + 2 * 7 + 1 + 2 * kItems + 2 * kRaws];
-    __shared__ __align__(16) Item item_sh[kItems];
+    __shared__ Item item_sh[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, begin_sh[2];
-    __shared__ long long scan_sh[kThreads / 32];
+    __shared__ int scan_sh[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t q_at = (smem_u32(dyn) + 1023u) & ~1023u, ring = q_at + 2 * F::tile;
     int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile +
@@ -270,7 +291,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                    done = ofree + 16,
                    ifull = done + 8, iempty = ifull + 8 * kItems, rfull = iempty + 8 * kItems,
                    rempty = rfull + 8 * kRaws, raw_at = ring + kStages * F::tile;
-    const Bail bail{smem_u32(&dead), status};
+    const uint32_t bail = smem_u32(&dead);
 
     if (tid == 0) {
         dead = 0;
@@ -316,6 +337,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     // pairs before each sequence; whether any has rows without a place
     int before = 0;
     bool short_one = false;
+#pragma unroll 1
     for (int s0 = 0; s0 < a.c.S; s0 += kThreads) {
         int n = 0, row0;
         if (s0 + tid < a.c.S) {
@@ -335,8 +357,8 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         int all = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            upto += w < warp ? (int)scan_sh[w] : 0;
-            all += (int)scan_sh[w];
+            upto += w < warp ? scan_sh[w] : 0;
+            all += scan_sh[w];
         }
         if (s0 + tid < a.c.S)
             first_pair[s0 + tid] = before + upto - n;
@@ -353,49 +375,47 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         // this block's share of the list of key tiles, and where it begins
         const int per = (pairs + kThreads - 1) / kThreads;
         const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
-        long long mine = 0;
-        int n0 = 0;
+        int mine = 0, n0 = 0;
+#pragma unroll 1
         for (int f = f0; f < f1; ++f) {
             n0 = pair_at(a, plan.tok, first_pair, f).n;
-            mine += (long long)n0 * a.c.heads;
+            mine += n0 * a.c.heads;
         }
-        long long upto = mine;
+        int upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, m);
+            const int v = __shfl_up_sync(0xffffffffu, upto, m);
             upto += lane >= m ? v : 0;
         }
         if (lane == 31)
             scan_sh[warp] = upto;
         __syncthreads();
-        long long total = 0;
+        int total = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             upto += w < warp ? scan_sh[w] : 0;
             total += scan_sh[w];
         }
         // no more blocks than units: an item's blocks are then consecutive ones
-        const int blocks = (int)min((long long)gridDim.x, max(total, 1ll));
-        long long u0 = 0;
+        const int blocks = min((int)gridDim.x, max(total, 1));
+        int u0 = 0;
         walk.total = total;
         walk.blocks = blocks;
         if ((int)blockIdx.x < blocks) {
-            if (total < 1 << 22) {          // the products fit 32 bits
-                u0 = (unsigned)total * blockIdx.x / (unsigned)blocks;
-                walk.end = (unsigned)total * (blockIdx.x + 1) / (unsigned)blocks;
-            } else {
-                u0 = total * blockIdx.x / blocks;
-                walk.end = total * (blockIdx.x + 1) / blocks;
-            }
+            // total * block / blocks within 32 bits
+            const int each = total / blocks, rest = total - each * blocks;
+            u0 = each * blockIdx.x + rest * blockIdx.x / blocks;
+            walk.end = each * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / blocks;
             walk.left = walk.end - u0;
         }
-        long long at = upto - mine;
+        int at = upto - mine;
         if (walk.left && u0 >= at && u0 < upto) {
+#pragma unroll 1
             for (int f = f0; f < f1; ++f) {
                 const int n = per == 1 ? n0 : pair_at(a, plan.tok, first_pair, f).n;
-                const long long end = at + (long long)n * a.c.heads;
+                const int end = at + n * a.c.heads;
                 if (u0 < end) {
-                    const int in = (int)(u0 - at);
+                    const int in = u0 - at;
                     begin_sh[0] = f * a.c.heads + in / n;
                     begin_sh[1] = in % n;
                     break;
@@ -410,13 +430,16 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         walk.x = begin_sh[1];
     }
     // rows that see nothing, where that holds for a whole pair
+#pragma unroll 1
     for (int f = short_one ? (int)blockIdx.x : pairs; f < pairs; f += (int)gridDim.x) {
         const Pair p = pair_at(a, plan.tok, first_pair, f);
         if (p.n > 0)
             continue;
+#pragma unroll 1
         for (int i = tid; i < p.tokens * a.Hq; i += kThreads) {
             const int row = p.row0 + i / a.Hq, h = i % a.Hq;
             uint8_t* to = a.out.p + row * a.out.row + h * a.out.head;
+#pragma unroll 1
             for (int c = 0; c < a.c.D / 8; ++c)
                 *reinterpret_cast<uint4*>(to + 16 * c) = make_uint4(0, 0, 0, 0);
             if (a.lse)
@@ -432,7 +455,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     bool ok = true;
     const auto take = [&](bool whole_warp) {
         const uint32_t i = taken % kItems;
-        ok = bar_wait(ifull + 8 * i, taken / kItems & 1, bail, kWaitItem);
+        ok = wait_for(ifull + 8 * i, taken / kItems & 1, bail, kWaitItem);
         if (whole_warp)
             ok = __all_sync(0xffffffffu, ok);
         if (!ok)
@@ -453,6 +476,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
             const int page_rows = min(1 << a.c.page_shift, kGroup), boxes = kKeys / page_rows;
             const int box = lane % boxes, part = lane / boxes;      // part: which 64 elements
             while (ok && take(true)) {
+#pragma unroll 1
                 for (int x = w.x0; x < w.x1 && ok; ++x) {
                     // a lane's box lies in one of the step's two groups
                     const int in = box * page_rows;
@@ -467,8 +491,8 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         const uint32_t s = F8 ? it % kRaws : it % kStages;
-                        ok = F8 ? bar_wait(rempty + 8 * s, (it / kRaws & 1) ^ 1, bail, kWaitStage)
-                                : bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
+                        ok = F8 ? wait_for(rempty + 8 * s, (it / kRaws & 1) ^ 1, bail, kWaitStage)
+                                : wait_for(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok)
                             break;
@@ -482,15 +506,15 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                                             rfull + 8 * s, 0, row, w.head, page);
                         } else {
                             const uint32_t to = ring + s * F::tile + in * 128;
-                            for (int h = part; h < DP / 64; h += 32 / boxes)
-                                tma_load_4d(to + h * F::half, kv ? &map_v : &map_k, full + 8 * s, 64 * h,
-                                            row, w.head, page);
+                            if (part < DP / 64)
+                                tma_load_4d(to + part * F::half, kv ? &map_v : &map_k, full + 8 * s,
+                                            64 * part, row, w.head, page);
                         }
                         __syncwarp();
                         // the queries behind the first keys: their place is free later
                         if (x == w.x0 && kv == 0) {
                             for (int t = 0; t < 2 && t * plan.tok < w.p.tokens && ok; ++t) {
-                                ok = bar_wait(qempty + 8 * t, (uses[t] & 1) ^ 1, bail, kWaitQueryFree);
+                                ok = wait_for(qempty + 8 * t, (uses[t] & 1) ^ 1, bail, kWaitQueryFree);
                                 ok = __all_sync(0xffffffffu, ok);
                                 if (!ok)
                                     break;
@@ -508,19 +532,20 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                                 break;
                             }
                         }
-                        if (!F8 && kv && lane == 0 && step_has_unseen(w.p, x))
+                        if (!F8 && kv && lane == 0 && w.has_unseen(x))
                             bar_arrive(wanted + 8 * s);
                     }
                 }
             }
             // until every stage and the queries' places are free again: no copy and no arrival is
             // on its way when the block ends
+#pragma unroll 1
             for (uint32_t i = it < kStages ? 0 : it - kStages; i < it && ok; ++i)
-                ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % kStages), i / kStages & 1, bail,
+                ok = __all_sync(0xffffffffu, wait_for(empty + 8 * (i % kStages), i / kStages & 1, bail,
                                                       kWaitStage));
             for (int t = 0; t < 2 && ok; ++t)
                 if (uses[t])
-                    ok = __all_sync(0xffffffffu, bar_wait(qempty + 8 * t, (uses[t] - 1) & 1, bail,
+                    ok = __all_sync(0xffffffffu, wait_for(qempty + 8 * t, (uses[t] - 1) & 1, bail,
                                                           kWaitQueryFree));
             __syncwarp();
             sent = it;
@@ -539,14 +564,14 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                 // queries taken, weights taken, items begun (bit t, modulo 2: of tile t)
                 uint32_t it = 0, uses = 0, weights = 0, begun = 3, clears = 0;
                 const auto landed = [&](uint32_t i) {
-                    ok = bar_wait(full + 8 * (i % kStages), i / kStages & 1, bail, kWaitKeys);
+                    ok = wait_for(full + 8 * (i % kStages), i / kStages & 1, bail, kWaitKeys);
                     return ok;
                 };
                 // scores of an item's step from the keys of stage i; of its first step the queries
                 // are waited for, behind its last they are done with
                 const auto scores = [&](uint32_t t, uint32_t i, bool first, bool last) {
                     if (first) {
-                        ok = bar_wait(qfull + 8 * t, uses >> t & 1, bail, kWaitQuery);
+                        ok = wait_for(qfull + 8 * t, uses >> t & 1, bail, kWaitQuery);
                         if (!ok)
                             return;
                         uses ^= 1u << t;
@@ -570,11 +595,12 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                     ++it;
                 }
                 while (ok && more) {
+#pragma unroll 1
                     for (int x = w.x0, x0 = x, x1 = w.x1; x < x1 && ok; ++x) {
                         // values of this step: stage it; keys of the next, of the next item behind
                         // the last step: it + 1
                         const uint32_t sv = it % kStages, now = tiles;
-                        const bool last = x + 1 == x1, unseen = !F8 && step_has_unseen(w.p, x);
+                        const bool last = x + 1 == x1, unseen = !F8 && w.has_unseen(x);
                         uint32_t then = tiles;
                         bool next_last = x + 2 == x1;
                         if (last) {
@@ -587,7 +613,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                         if (!landed(it))
                             break;
                         if (unseen) {
-                            if (!(ok = bar_wait(cleared + 8 * sv, clears >> sv & 1, bail, kWaitCleared)))
+                            if (!(ok = wait_for(cleared + 8 * sv, clears >> sv & 1, bail, kWaitCleared)))
                                 break;
                             clears ^= 1u << sv;
                         }
@@ -596,18 +622,18 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                             if (t < now) {
                                 // the sums of the item before have been read
                                 if (x == x0) {
-                                    if (!(ok = bar_wait(ofree + 8 * t, begun >> t & 1, bail, kWaitSums)))
+                                    if (!(ok = wait_for(ofree + 8 * t, begun >> t & 1, bail, kWaitSums)))
                                         break;
                                     begun ^= 1u << t;
                                 }
                                 const uint32_t o = tmem + 256 + t * 128, p = tmem + t * 128,
                                                bar = pfull + 16 * t, par = weights >> t & 1;
                                 weights ^= 1u << t;
-                                if (!(ok = bar_wait(bar, par, bail, kWaitWeights)))
+                                if (!(ok = wait_for(bar, par, bail, kWaitWeights)))
                                     break;
                                 tc_fence_after();
                                 mma4_half_ts(o, p, v, v_hi, id_o, x > x0);
-                                if (!(ok = bar_wait(bar + 8, par, bail, kWaitWeights)))
+                                if (!(ok = wait_for(bar + 8, par, bail, kWaitWeights)))
                                     break;
                                 tc_fence_after();
                                 mma4_half_ts(o, p + 32, v + 512, v_hi, id_o, true);
@@ -640,8 +666,8 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                 for (int x = w.x0; x < w.x1 && ok; ++x) {
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         const uint32_t r = it % kRaws, s = it % kStages;
-                        ok = bar_wait(rfull + 8 * r, it / kRaws & 1, bail, kWaitKeys) &&
-                             bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
+                        ok = wait_for(rfull + 8 * r, it / kRaws & 1, bail, kWaitKeys) &&
+                             wait_for(empty + 8 * s, (it / kStages & 1) ^ 1, bail, kWaitStage);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok)
                             break;
@@ -679,16 +705,18 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
             // answered by an older one.
             uint32_t it = 0, asked = 0;
             while (ok && take(true)) {
+#pragma unroll 1
                 for (int x = w.x0; x < w.x1 && ok; ++x, it += 2) {
-                    if (!step_has_unseen(w.p, x))
+                    if (!w.has_unseen(x))
                         continue;
                     const uint32_t s = (it + 1) % kStages;
-                    ok = bar_wait(wanted + 8 * s, asked >> s & 1, bail, kWaitCleared) &&
-                         bar_wait(full + 8 * s, (it + 1) / kStages & 1, bail, kWaitKeys);
+                    ok = wait_for(wanted + 8 * s, asked >> s & 1, bail, kWaitCleared) &&
+                         wait_for(full + 8 * s, (it + 1) / kStages & 1, bail, kWaitKeys);
                     asked ^= 1u << s;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
+#pragma unroll 1
                     for (int i = lane; i < kKeys * 8; i += 32) {
                         const int key = key_of(w.p, 2 * x + i / (8 * kGroup)) + i / 8 % kGroup;
                         if (key < w.p.end && (key >= w.p.low || key < w.p.sinks))
@@ -708,8 +736,9 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
             }
         } else if (warp == 11 && lane == 0) {
             // the items, and one without tiles behind the last
+#pragma unroll 1
             for (uint32_t i = 0; ok; ++i) {
-                if (!(ok = bar_wait(iempty + 8 * (i % kItems), (i / kItems & 1) ^ 1, bail, kWaitPlace)))
+                if (!(ok = wait_for(iempty + 8 * (i % kItems), (i / kItems & 1) ^ 1, bail, kWaitPlace)))
                     break;
                 Item next;
                 const bool more = walk.next(a, plan, first_pair, &next);
@@ -738,7 +767,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         int held_row = 0, held_head = 0, held_part = -1;        // row -1: of no token
         const auto give = [&]() {
             held = false;
-            bar_wait(ofull + 8 * t, items & 1, bail, kWaitSums);
+            wait_for(ofull + 8 * t, items & 1, bail, kWaitSums);
             ++items;
             __syncwarp();
             tc_fence_after();
@@ -814,8 +843,9 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                       full1 = (max(ia + 1, 0) / kGroup - w.p.gap) / 2;
             float top = -INFINITY;
             uint64_t sum = 0;
+#pragma unroll 1
             for (int x = w.x0; x < w.x1; ++x, ++seen) {
-                bar_wait(sfull + 8 * t, seen & 1, bail, kWaitScores);
+                wait_for(sfull + 8 * t, seen & 1, bail, kWaitScores);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t s[kKeys];
@@ -916,9 +946,12 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     tc_fence_after();
     // Without a wait that gave up every product has been taken and every copy is consumed.
     // With one, whichever warp's it was, both end here before the block does.
-    if (*static_cast<volatile int*>(&dead)) {
+    if (const int where = *static_cast<volatile int*>(&dead)) {
+        if (tid == 0 && atomicCAS(status, 0, AR_ERR_TIMEOUT) == 0)
+            atomicExch(status + 1, where);
         if (warp == 8) {
             constexpr uint32_t kPlaces = F8 ? kRaws : kStages;
+#pragma unroll 1
             for (uint32_t i = sent < kPlaces ? 0 : sent - kPlaces; i < sent; ++i)
                 bar_drain((F8 ? rfull : full) + 8 * (i % kPlaces), i / kPlaces & 1);
             for (int t = 0; t < 2; ++t)
@@ -1042,13 +1075,13 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         return cudaErrorInvalidValue;
     int blocks = d.sms;
     const int64_t fit = (int64_t)(a.work_bytes / (16 + 2 * Shape<DP>::part));
-    plan.whole = items >= 4ll * d.sms || fit < 2;
+    const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
+    const int64_t most = items * ((keys + kKeys - 1) / kKeys + 1);     // steps, all in one list
+    plan.whole = items >= 4ll * d.sms || fit < 2 || most >= 1 << 30;
     if (plan.whole) {
         if (items < blocks)
             blocks = (int)items;
     } else {
-        const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
-        const int64_t most = items * ((keys + kKeys - 1) / kKeys + 1);
         if (most < blocks)
             blocks = (int)most;
         if (fit < blocks)
