@@ -21,6 +21,13 @@
 // holds whole items, and at most two pieces of items that other blocks share: those go
 // to the workspace as sums, maximum and total, and join_kernel, launched behind it,
 // adds them in the order of the blocks.
+//
+// 64 x 800-8000 tokens, 32 / 8 heads, bf16: 173 to 180 us, 6.4 to 6.7 TB/s (0.95 to 0.98 of a
+// copy); one sequence of 131072, 64 / 8 heads: 84 us, 6.4 TB/s; E4M3, 128 x 2048-4096, 64 / 8
+// heads: 133 to 143 us, 5.7 to 6.1 TB/s, what is left goes to the widening of the codes (issue
+// slots 55% used).  4 x 500-1000 tokens, 8 / 1 heads: 7.6 us, two launches and two reads behind
+// one another (page number, keys) with a join.  33 windows of 1000, 28 / 4 heads of 80: 17 us,
+// where a block has some ten units and fills its ring anew for the join of each item.
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "matmul_internal.h"
@@ -133,7 +140,7 @@ __device__ __forceinline__ Seen seen_of(const AttentionArgs& a, int length)
 }
 
 // Units of an item: of four slices, and one more for its end, which takes as long: without it
-// blocks with many short items were the last by far (33 windows of 1000 21.6 us, now 17.4).
+// blocks with many short items were the last by far (33 windows of 1000 21.6 us, now 17.1).
 __device__ __forceinline__ int units_of(const Seen& s)
 {
     return s.n ? (s.n + kWarps - 1) / kWarps + 1 : 0;
@@ -183,6 +190,10 @@ struct Form {
     static constexpr int pitch = DP * bytes;            // of a slice's row
     static constexpr int SL = kTile / pitch;            // keys of a slice
     static constexpr bool bf16 = !F8 && D::id == AR_DT_BF16;    // products' type
+    // The weights are 2^up times e^{s_j - max}.  fp16 keeps 11 bits down to 2^-14 only and nothing
+    // below 2^-25: of 131072 keys whose weights are 2^-25 each a share of 2^-8 was lost.  With 2^14
+    // for the largest all are kept to 2^-39.
+    static constexpr float up = bf16 ? 0.0f : 14.0f;
     // 16-byte chunk `c` of row r: the 8 rows of a matrix load in different banks
     static __device__ __forceinline__ uint32_t at(int r, int c)
     {
@@ -558,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
                     if (!sees(key0 + r))
 #pragma unroll
                         for (int i = 0; i < F::pitch; i += 16)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + r * F::pitch + i),
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             vb + r * F::pitch + i),
                                          "r"(0)
                                          : "memory");
                 __syncwarp();
@@ -595,6 +607,11 @@ __global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
                         top[n][e] = now[n][e];
                     }
             }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    used[n][e] -= F::up;
             uint32_t p[NK][NB][2];
 #pragma unroll
             for (int k = 0; k < NK; ++k)
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w)
                         l += sum_sh[w][h] * exp2_fast(max_sh[w][h] - base);
-                    best[n][e] = m;
+                    best[n][e] = m - F::up;
                     sum[n][e] = l;
                     const float f = exp2_fast(top[n][e] - base);
 #pragma unroll
@@ -850,7 +867,8 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     e = launch_after(decode_attention_kernel<D, DP, F8, NB>, blocks, kThreads, kSmem, s, a, sp, tiles);
     if (e != cudaSuccess || sp.whole || blocks == 1)
         return e;
-    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)), kJoinThreads, 0, s, a, sp);
+    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)),
+                        kJoinThreads, 0, s, a, sp);
 }
 
 template <class D, bool F8>

@@ -19,9 +19,20 @@
 //   warp 11: finds the items ahead of the others (each for itself took 1.5 us an item)
 //
 // Items (a pair of tiles and a head) are worked off by one block per SM: where there
-// are many, whole ones, the longest first; where there are few, the key tiles of all items
+// are many, whole ones, the longest first; where there are few, the steps of all items
 // are one list and a block takes an equal share of it.  Items that several blocks
 // share are added up by join_kernel from sums, maxima and totals in the workspace.
+//
+// Long prompts are bound by the tensor cores and the clock that their power leaves: 8192 tokens,
+// 32 / 8 heads of 128, bf16: 330 us, 1.66 PFLOP/s of the products that count (0.88 of a library
+// product's burst).  With a window of 1024 (3 x 3000-5000 tokens, 64 / 8 heads: 273 us, 1.17
+// PFLOP/s) a third of a tile's products are of keys that its rows do not see, and every item of
+// ten steps has a first and a last one.  Chunks of some hundred tokens (13 x 40-400 on 600-3000,
+// 14 / 2 heads of 64: 37 us) are bound by how long an item's chain of steps takes: a step's product,
+// its softmax and the second product follow one another, 1.1 us for each pair of them.
+// Over a cache of E4M3 the widening adds as many shared-memory bytes as the products read: 455 us.
+// 64 keys a step with two places for the scores took 450 us instead of 349 (twice the waits for as
+// many products), weights ahead of the maximum 27 us more (another pass over the registers).
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "matmul_internal.h"
@@ -39,13 +50,19 @@ struct Regs {
     static_assert((threads / 32 - 8) * few + 8 * many <= threads / 32 * launch, "register shares");
 };
 constexpr float kLn2 = 0.693147181f;
-// How far (in powers of two) a row's maximum may grow before its sums are rescaled: weights
-// are then up to 2^growth, as exact as below 1.  fp16 weights end at 2^16; with bf16 ones the
-// sums of n keys stay finite for values below 2^96 / n.  At 2^8 some row of 32 was rescaled
-// in two of three tiles of a windowed prompt, whose first tile has 4 keys (399 us, now
-// see below), at 0.4 us each.
+// How far (in powers of two) a row's maximum may grow before its sums are rescaled: weights are
+// then up to 2^growth, as exact as below 1.  A rescaling takes 0.4 us, and with 2^8 some row of
+// 32 wanted one in two of three steps of a windowed prompt that begins with a few first tokens.
+// With bf16 weights the sums of n keys stay finite for values below 2^96 / n.
+// fp16 weights end at 2^16, have fewer than 11 bits below 2^-14 and nothing below 2^-25: theirs are
+// 2^up times e^{s_j - top}, so that of the sum 2^-30 per key can be lost (with growth 14 and
+// up 0 it was 2^-25, 2^-8 of the sum of 131072 such keys, at 3 x 3000-5000 tokens with a window
+// of 1024 and 64 / 8 heads 294 us instead of 303; with 5 and 10 311, and 8192 tokens, 32 / 8
+// heads, 369 instead of 337).
 template <class D>
-__device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16 ? 32.0f : 14.0f; }
+__device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16 ? 32.0f : 10.0f; }
+template <class D>
+__device__ __forceinline__ constexpr float up() { return D::id == AR_DT_BF16 ? 0.0f : 5.0f; }
 enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
        kWaitCleared, kWaitItem, kWaitPlace };
 
@@ -286,9 +303,9 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     int* first_pair = reinterpret_cast<int*>(dyn + (q_at - smem_u32(dyn)) + (2 + F::stages) * F::tile +
                                              F::raws * F::raw);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, cleared = empty + 8 * kStages,
-                   wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages, qempty = qfull + 16, sfull = qempty + 16,
-                   pfull = sfull + 16, ofull = pfull + 32, ofree = ofull + 16,
-                   done = ofree + 16,
+                   wanted = cleared + 8 * kStages, qfull = wanted + 8 * kStages,
+                   qempty = qfull + 16, sfull = qempty + 16, pfull = sfull + 16,
+                   ofull = pfull + 32, ofree = ofull + 16, done = ofree + 16,
                    ifull = done + 8, iempty = ifull + 8 * kItems, rfull = iempty + 8 * kItems,
                    rempty = rfull + 8 * kRaws, raw_at = ring + kStages * F::tile;
     const uint32_t bail = smem_u32(&dead);
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
 
     Walk walk{0, pairs * a.c.heads, 0, 0, 0, 0, 1, (int)gridDim.x};
     if (!plan.whole) {
-        // this block's share of the list of key tiles, and where it begins
+        // this block's share of the list of steps, and where it begins
         const int per = (pairs + kThreads - 1) / kThreads;
         const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
         int mine = 0, n0 = 0;
@@ -521,8 +538,8 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                                 if (elect_one()) {
                                     bar_expect(qfull + 8 * t, DP / 64 * 128 * plan.tok * a.G);
                                     for (int h = 0; h < DP / 64; ++h)
-                                        tma_load_4d(q_at + t * F::tile + h * F::half, &map_q, qfull + 8 * t, 64 * h,
-                                                    0, w.head, w.p.row0 + t * plan.tok);
+                                        tma_load_4d(q_at + t * F::tile + h * F::half, &map_q, qfull + 8 * t,
+                                                    64 * h, 0, w.head, w.p.row0 + t * plan.tok);
                                 }
                                 __syncwarp();
                                 ++uses[t];
@@ -901,7 +918,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                 }
                 // The products of the first half of the weights begin while the second half is made.
                 const float used = top == -INFINITY ? 0.0f : top;
-                const uint64_t scale = pair_of(scale_log2, scale_log2), minus = pair_of(-used, -used);
+                const uint64_t scale = pair_of(scale_log2, scale_log2), minus = pair_of(up<D>() - used, up<D>() - used);
                 uint64_t part[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -927,7 +944,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
             }
             const float2 two = unpack_pair(sum);
             held = true;
-            held_top = top;
+            held_top = top - up<D>();
             held_sum = two.x + two.y;
             held_row = live ? w.p.row0 + tok0 + in : -1;
             held_head = w.head * a.G + g;
@@ -1089,8 +1106,8 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         plan.desc = reinterpret_cast<int4*>(a.work);
         plan.parts = a.work + 16 * (int64_t)blocks;
     }
-    e = launch_after(prompt_attention_kernel<D, DP, F8>, blocks, Regs<F8>::threads, smem, s, map_q, map_k, map_v, a,
-                     plan, d.status + kStatusWords);
+    e = launch_after(prompt_attention_kernel<D, DP, F8>, blocks, Regs<F8>::threads, smem, s, map_q, map_k,
+                     map_v, a, plan, d.status + kStatusWords);
     if (e != cudaSuccess || plan.whole || blocks == 1)
         return e;
     return launch_after(join_kernel<D, DP>, dim3(blocks, DP / kJoinDims), 2 * kRows, 0, s, a, plan);

@@ -657,7 +657,8 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
 /* Elements of a head; axes of a position. */
 #define AR_MAX_HEAD_DIM 128
 #define AR_MAX_AXES 4
-/* Bytes of workspace with which the attention calls split as far as they can. */
+/* Bytes of workspace that are enough for every split but one: prompts of heads above 64 elements
+ * share items among 126 blocks with them, and among all SMs with 40 MB. */
 #define AR_ATTENTION_WORKSPACE_BYTES (32 << 20)
 
 /* Rows of heads: element d of head h of row t is data[t * row + h * head + d].
@@ -678,8 +679,8 @@ typedef struct ar_head_rows {
  *   dtype        AR_DT_BF16 or AR_DT_FP16 (that of the call's rows), or AR_DT_E4M3
  *   pages        >= 1;  page_size a power of two, 8 .. 65536
  *   heads        >= 1;  head_dim a multiple of 8 (E4M3: 16), 8 .. AR_MAX_HEAD_DIM
- *   scale        device fp32 [2]: a key is its code times scale[0], a value its code times
- *                scale[1].  NULL: 1.  With AR_DT_E4M3 only
+ *   scale        device fp32 [2], positive and finite: a key is its code times scale[0], a
+ *                value its code times scale[1].  NULL: 1.  With AR_DT_E4M3 only
  *   page_table   device int32 [sequences][max_pages]
  *   lengths      device int32 [sequences]
  *   sequences    0 .. AR_MAX_SEQUENCES (0: nothing launched);  max_pages >= 1,
@@ -730,7 +731,9 @@ int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,
  *   s_j = scale * q . k_j,  out = sum_j e^{s_j} v_j / sum_j e^{s_j},
  *   lse = log sum_j e^{s_j}
  * in fp32 (the products of the matrix instructions; e^{s_j - max} is rounded to the
- * 16-bit type of the values' product), rounded to the element type once.  A token that
+ * 16-bit type of the values' product, the rows' or for this call over an E4M3 cache
+ * fp16; of a weight that fp16 cannot hold at most 2^-39 of the largest weight is lost,
+ * by ar_fusion_prompt_attention 2^-30), rounded to the element type once.  A token that
  * sees nothing gets zeros and -inf.  What keys and values hold that no token of the
  * call sees, NaN and infinities among it, changes nothing.
  *   q, out     [sequences][q_heads] of `dtype` (AR_DT_BF16 or AR_DT_FP16)
@@ -741,7 +744,7 @@ int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,
  *              sinks >= 0: first keys that stay visible (0 without a window)
  *   workspace  device memory, 16-byte aligned, written by this call alone while it
  *              runs; the long axis is split as far as workspace_bytes allow (NULL with
- *              0: not at all; AR_ATTENTION_WORKSPACE_BYTES are always enough)
+ *              0: not at all; AR_ATTENTION_WORKSPACE_BYTES: see there)
  * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */
 int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
                                const ar_head_rows* out, float* lse, int q_heads, int dtype,
@@ -752,8 +755,9 @@ int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
  * own index.
  *   q, out     [tokens][q_heads];  lse [tokens][q_heads] or NULL
  *   starts     device int32 [sequences + 1]
- * An infinite or NaN value of a key that one token of a
- * sequence sees also reaches tokens next to it that do not see that key.
+ * An infinite or NaN value of a key that one token of a sequence sees also reaches tokens
+ * next to it that do not see that key; with bf16 rows so do values above 2^96 divided by
+ * the number of keys, whose sums may leave fp32 before the quotient is taken.
  * Device-side waits are bounded (2 s each); one that gives up leaves the outputs undefined
  * and is reported by ar_fusion_attention_status.
  * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */

@@ -11,6 +11,8 @@ from allreduce_residual_rmsnorm_gb300 import binding as B
 pytestmark = pytest.mark.gpu
 BF16, FP16, E4M3 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
 U = R.U
+# of a fp16 weight, next to a largest one taken as 1, by the calls' contract
+LOST_ONE, LOST_PROMPT = 2.0 ** -39, 2.0 ** -30
 
 
 @pytest.fixture(scope="module")
@@ -174,7 +176,7 @@ def check_decode(lengths, P, H, K, D, dtype, cache_dtype, workspace, window=0, s
                        list(range(S + 1)), D ** -0.5 if scale is None else scale, window, sinks,
                        pages.scales)
     R.check_attention(out[:S, :, :D], L, want, dtype, FP16 if cache_dtype == E4M3 else dtype,
-                      splits=40)
+                      LOST_ONE, splits=40)
     assert bool((out[S] == 5.0).all()) and bool((out[:, :, D:] == 5.0).all())
     return out[:S, :, :D], L
 
@@ -290,7 +292,7 @@ def check_prompt(new, lengths, P, H, K, D, dtype, workspace, window=0, sinks=0, 
     assert B.ar_fusion_attention_status() == (B.AR_OK, -1)
     want = R.attention(q, pages.view(pages.k), pages.view(pages.v), pages.table, pages.lengths,
                        starts, D ** -0.5 if scale is None else scale, window, sinks, pages.scales)
-    R.check_attention(out[:, :, :D], L, want, dtype, dtype, splits=40)
+    R.check_attention(out[:, :, :D], L, want, dtype, dtype, LOST_PROMPT, splits=40)
     dead = torch.isnan(want[4][:, 0])
     assert bool((out[:, :, D:] == 5.0).all()) and bool((out.cpu()[dead] == 5.0).all())
     if lse:
@@ -403,3 +405,35 @@ def test_prompt_and_decode_agree(workspace):
     last = [0, 40, 140]
     B.ar_fusion_decode_attention(q[last].cuda(), kc, vc, table, dev_lengths, one, workspace)
     assert bool(((one.float() - out[last].float()).abs() <= 2.0 ** -6).all())
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("prompt", [False, True])
+def test_many_light_keys(workspace, prompt, dtype, cache):
+    """One key of weight 1 and value 0, and 65535 of 2^-25 whose values are all there is to the
+    output: they are half of what fp16 has next to a largest weight of 1."""
+    n, D, P = 65536, 64, 1024
+    k = torch.zeros(n // P, P, 1, D)
+    v = torch.ones(n // P, P, 1, D)
+    k[0, 5, 0, 0] = 25.0 if cache != E4M3 else 24.0
+    v[0, 5] = 0.0
+    k, v = k.to(cache), v.to(cache)
+    q = torch.zeros(2, 2, D)
+    q[:, :, 0] = 1.0
+    q = q.to(dtype)
+    table = torch.arange(n // P, dtype=torch.int32)[None]
+    lengths = torch.tensor([n], dtype=torch.int32)
+    starts = torch.tensor([0, 2 if prompt else 1], dtype=torch.int32)
+    T = int(starts[1])
+    scale = math.log(2.0) * (1.0 if cache != E4M3 else 25.0 / 24.0)
+    out = torch.empty(T, 2, D, dtype=dtype, device="cuda")
+    lse = torch.empty(T, 2, device="cuda")
+    args = [t.cuda() for t in (q[:T], k, v, table, lengths)]
+    if prompt:
+        B.ar_fusion_prompt_attention(*args, starts.cuda(), out, workspace, scale=scale, lse=lse)
+    else:
+        B.ar_fusion_decode_attention(*args, out, workspace, scale=scale, lse=lse)
+    want = R.attention(q[:T], k, v, table, lengths, starts, scale, 0, 0)
+    assert 2.0 ** -10 < float(want[0].min()) < 2.0 ** -8
+    R.check_attention(out, lse, want, dtype, FP16 if cache == E4M3 and not prompt else dtype,
+                      LOST_PROMPT if prompt else LOST_ONE, splits=200)

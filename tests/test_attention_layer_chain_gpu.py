@@ -162,8 +162,8 @@ def test_decode_steps_are_what_the_prompt_would_have_been(cuda_lib):
         assert torch.equal(qi, q[i:i + 1])
         want = R.attention(qi.cpu(), two.k.cpu(), two.v.cpu(), two.table.cpu(), length.cpu(), [0, 1],
                            Layer.D ** -0.5, 0, 0)
-        R.check_attention(out, None, want, BF16, BF16, splits=8)
-        R.check_attention(whole[i:i + 1], None, want, BF16, BF16, splits=8)
+        R.check_attention(out, None, want, BF16, BF16, 0.0, splits=8)
+        R.check_attention(whole[i:i + 1], None, want, BF16, BF16, 0.0, splits=8)
     assert torch.equal(one.k[one.table.long()], two.k[two.table.long()])
 
 
@@ -236,7 +236,7 @@ def test_an_e4m3_cache_in_decode_steps(cuda_lib):
         q = b["qkv"].view(2, H + 2 * K, Layer.D)[:, :H]         # rotated in place
         want = R.attention(q.cpu(), layer.k.cpu(), layer.v.cpu(), layer.table.cpu(), lengths.cpu(),
                            [0, 1, 2], Layer.D ** -0.5, 0, 0, layer.scale.double().tolist())
-        R.check_attention(b["att"], b["lse"], want, BF16, torch.float16, splits=8)
+        R.check_attention(b["att"], b["lse"], want, BF16, torch.float16, 2.0 ** -39, splits=8)
 
 
 def test_calls_on_a_given_stream_and_through_ctypes(cuda_lib, monkeypatch):
@@ -295,8 +295,8 @@ def test_caches_past_32_bits(cuda_lib):
     B.ar_fusion_prompt_attention(q.cuda(), kc, vc, table.cuda(), lengths.cuda(), starts.cuda(), out, work)
     B.ar_fusion_decode_attention(q[9:].cuda(), kc, vc, table.cuda(), lengths.cuda(), one, work)
     want = R.attention(q, *small, local, lengths, starts, D ** -0.5, 0, 0)
-    R.check_attention(out, None, want, BF16, BF16, splits=8)
-    R.check_attention(one, None, [w[9:] for w in want], BF16, BF16, splits=8)
+    R.check_attention(out, None, want, BF16, BF16, 0.0, splits=8)
+    R.check_attention(one, None, [w[9:] for w in want], BF16, BF16, 0.0, splits=8)
     new = torch.randn(10, K, D, generator=g).to(BF16).cuda()
     B.ar_fusion_rope_append(None, new, new, kc, vc, table.cuda(), lengths.cuda(), None, starts=starts.cuda())
     assert torch.equal(kc[at[3], 30:40], new) and torch.equal(vc[at[3], 30:40], new)
