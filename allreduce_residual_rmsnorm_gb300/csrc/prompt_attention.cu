@@ -25,11 +25,11 @@
 //
 // Long prompts are bound by the tensor cores and the clock that their power leaves: 8192 tokens,
 // 32 / 8 heads of 128, bf16: 330 us, 1.66 PFLOP/s of the products that count (0.88 of a library
-// product's burst).  With a window of 1024 (3 x 3000-5000 tokens, 64 / 8 heads: 273 us, 1.17
-// PFLOP/s) a third of a tile's products are of keys that its rows do not see, and every item of
-// ten steps has a first and a last one.  Chunks of some hundred tokens (13 x 40-400 on 600-3000,
-// 14 / 2 heads of 64: 37 us) are bound by how long an item's chain of steps takes: a step's product,
-// its softmax and the second product follow one another, 1.1 us for each pair of them.
+// product's burst), 1.5 us a step.  With a window of 1024 (3 x 3000-5000 tokens, 64 / 8 heads: 273
+// us, 1.17 PFLOP/s) a seventh of the products is of keys that their row does not see, and an item of
+// nine steps costs 3 us beside them: masks on its first and last steps, its output.  Chunks of some
+// hundred tokens (13 x 40-400 on 600-3000, 14 / 2 heads of 64: 37 us) are 14 steps a block, and as
+// long again for the start, the ends of the items and the join.
 // Over a cache of E4M3 the widening adds as many shared-memory bytes as the products read: 455 us.
 // 64 keys a step with two places for the scores took 450 us instead of 349 (twice the waits for as
 // many products), weights ahead of the maximum 27 us more (another pass over the registers).
