@@ -155,11 +155,13 @@ def test_append_many_sequences(cuda_lib):
 # --------------------------------------------------- one token per sequence
 
 def check_decode(lengths, P, H, K, D, dtype, cache_dtype, workspace, window=0, sinks=0, scale=None,
-                 hnd=False, seed=3, lse=True, factor=1.0, table=None, q=None):
+                 hnd=False, seed=3, lse=True, factor=1.0, table=None, q=None, touch=None):
     pages = R.Pages(lengths, P, K, D, cache_dtype, seed=seed, hnd=hnd, extra=1)
     S = len(lengths)
     if table is not None:
         table(pages.table)
+    if touch is not None:
+        touch(pages)
     if q is None:
         q = (factor * torch.randn(S, H + 3, D, generator=gen(seed + 1))).to(dtype)[:, 1:H + 1]
     kc, vc, dev_table, dev_lengths, kv_scale = pages.cuda()
@@ -272,10 +274,12 @@ def test_decode_same_bits_again(workspace):
 # ------------------------------------------------------------------ prompts
 
 def check_prompt(new, lengths, P, H, K, D, dtype, workspace, window=0, sinks=0, scale=None, hnd=False,
-                 seed=5, lse=True, factor=1.0, table=None, first=0, behind=0, cache=None):
+                 seed=5, lse=True, factor=1.0, table=None, first=0, behind=0, cache=None, touch=None):
     pages = R.Pages(lengths, P, K, D, cache or dtype, seed=seed, hnd=hnd, extra=1)
     if table is not None:
         table(pages.table)
+    if touch is not None:
+        touch(pages)
     T = first + sum(new) + behind
     starts = torch.tensor([first + sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32)
     q = (factor * torch.randn(T, H + 2 * K, D, generator=gen(seed + 1))).to(dtype)
@@ -437,3 +441,59 @@ def test_many_light_keys(workspace, prompt, dtype, cache):
     assert 2.0 ** -10 < float(want[0].min()) < 2.0 ** -8
     R.check_attention(out, lse, want, dtype, FP16 if cache == E4M3 and not prompt else dtype,
                       LOST_PROMPT if prompt else LOST_ONE, splits=200)
+
+
+def places(pages, b, index):
+    """Page and row of the tokens of sequence b with these indexes."""
+    P = pages.view(pages.k).shape[1]
+    return pages.table[b].long()[index // P], index % P
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_scores_that_climb(workspace, dtype, cache):
+    """Scores that rise along the cache for half of the heads, by more than a power of 2^32 within
+    some hundred keys, and fall for the others: sums are rescaled again and again."""
+    lengths = [700, 300]
+
+    def climb(pages):
+        for b, n in enumerate(lengths):
+            index = torch.arange(n)
+            at = places(pages, b, index)
+            k = pages.view(pages.k)
+            k[at[0], at[1], :, 0] = (index * 0.5).to(cache)[:, None]
+    for window, sinks in ((0, 0), (200, 10)):
+        check_decode(lengths, 16, 8, 2, 64, dtype, cache, workspace, window, sinks, scale=1.0,
+                     touch=climb)
+        check_prompt([300, 33], lengths, 16, 8, 2, 64, dtype, workspace, window, sinks, scale=1.0,
+                     touch=climb, cache=cache)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("window,sinks", [(70, 0), (100, 5), (64, 130), (128, 64)])
+def test_nothing_unseen_before_a_window(workspace, window, sinks, dtype, cache):
+    """NaN in every key and value between the first tokens and the first one that a row sees."""
+    lengths = [700, 300, 90]
+
+    def junk(new):
+        def touch(pages):
+            for b, (n, length) in enumerate(zip(new, lengths)):
+                index = torch.arange(sinks, max(sinks, length - n - window + 1))
+                at = places(pages, b, index)
+                for c in (pages.k, pages.v):
+                    pages.view(c)[at[0], at[1]] = torch.full((), math.nan).to(cache)
+        return touch
+    check_decode(lengths, 16, 8, 2, 64, dtype, cache, workspace, window, sinks, touch=junk([1, 1, 1]))
+    new = [150, 1, 40]
+    check_prompt(new, lengths, 16, 8, 2, 128, dtype, workspace, window, sinks, touch=junk(new),
+                 cache=cache)
+    check_prompt(new, lengths, 16, 8, 2, 128, dtype, None, window, sinks, touch=junk(new), cache=cache)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_sequences_that_share_pages(workspace, dtype, cache):
+    """A common beginning, and a page that stands twice in a sequence."""
+    def share(table):
+        table[1, :8] = table[0, :8]
+        table[2, 3] = table[2, 1]
+    check_decode([400, 300, 90], 32, 8, 2, 128, dtype, cache, workspace, table=share)
+    check_prompt([40, 40, 20], [400, 300, 90], 32, 8, 2, 128, dtype, workspace, table=share, cache=cache)
