@@ -53,16 +53,17 @@ constexpr float kLn2 = 0.693147181f;
 // How far (in powers of two) a row's maximum may grow before its sums are rescaled: weights are
 // then up to 2^growth, as exact as below 1.  A rescaling takes 0.4 us, and with 2^8 some row of
 // 32 wanted one in two of three steps of a windowed prompt that begins with a few first tokens.
-// With bf16 weights the sums of n keys stay finite for values below 2^96 / n.
-// fp16 weights end at 2^16, have fewer than 11 bits below 2^-14 and nothing below 2^-25: theirs are
-// 2^up times e^{s_j - top}, so that of the sum 2^-30 per key can be lost (with growth 14 and
+// The weights are 2^up times e^{s_j - top}.  bf16 ones from 2^-16 to 2^16: the sums of n keys stay
+// finite for values below 2^112 / n, and above the denormals for values above 2^-110.
+// fp16 weights end at 2^16, have fewer than 11 bits below 2^-14 and nothing below 2^-25: with 2^5 to
+// 2^15 for the largest, 2^-30 per key of the sum can be lost (with growth 14 and
 // up 0 it was 2^-25, 2^-8 of the sum of 131072 such keys, at 3 x 3000-5000 tokens with a window
 // of 1024 and 64 / 8 heads 294 us instead of 303; with 5 and 10 311, and 8192 tokens, 32 / 8
 // heads, 369 instead of 337).
 template <class D>
 __device__ __forceinline__ constexpr float growth() { return D::id == AR_DT_BF16 ? 32.0f : 10.0f; }
 template <class D>
-__device__ __forceinline__ constexpr float up() { return D::id == AR_DT_BF16 ? 0.0f : 5.0f; }
+__device__ __forceinline__ constexpr float up() { return D::id == AR_DT_BF16 ? -16.0f : 5.0f; }
 enum { kWaitStage = 1, kWaitQueryFree, kWaitQuery, kWaitKeys, kWaitWeights, kWaitScores, kWaitSums,
        kWaitCleared, kWaitItem, kWaitPlace };
 

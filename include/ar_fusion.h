@@ -756,7 +756,7 @@ int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
  *   q, out     [tokens][q_heads];  lse [tokens][q_heads] or NULL
  *   starts     device int32 [sequences + 1]
  * An infinite or NaN value of a key that one token of a sequence sees also reaches tokens
- * next to it that do not see that key; with bf16 rows so do values above 2^96 divided by
+ * next to it that do not see that key; with bf16 rows so do values above 2^112 divided by
  * the number of keys, whose sums may leave fp32 before the quotient is taken.
  * Device-side waits are bounded (2 s each); one that gives up leaves the outputs undefined
  * and is reported by ar_fusion_attention_status.

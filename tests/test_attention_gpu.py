@@ -497,3 +497,13 @@ def test_sequences_that_share_pages(workspace, dtype, cache):
         table[2, 3] = table[2, 1]
     check_decode([400, 300, 90], 32, 8, 2, 128, dtype, cache, workspace, table=share)
     check_prompt([40, 40, 20], [400, 300, 90], 32, 8, 2, 128, dtype, workspace, table=share, cache=cache)
+
+
+@pytest.mark.parametrize("power", [95, -100])
+def test_values_far_from_one(workspace, power):
+    """bf16 values whose sums of 700 keys fit fp32 with room for weights of 2^16 (or 2^-16)."""
+    def far(pages):
+        pages.v *= 2.0 ** power
+    for kw in ({}, {"window": 200, "sinks": 10}):
+        check_decode([700, 300], 16, 8, 2, 64, BF16, BF16, workspace, touch=far, factor=5.0, **kw)
+        check_prompt([300, 33], [700, 300], 16, 8, 2, 128, BF16, workspace, touch=far, factor=5.0, **kw)
