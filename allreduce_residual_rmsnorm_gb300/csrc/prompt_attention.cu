@@ -30,7 +30,7 @@
 // nine steps costs 3 us beside them: masks on its first and last steps, its output.  Chunks of some
 // hundred tokens (13 x 40-400 on 600-3000, 14 / 2 heads of 64: 37 us) are 14 steps a block, and as
 // long again for the start, the ends of the items and the join.
-// Over a cache of E4M3 the widening adds as many shared-memory bytes as the products read: 455 us.
+// Over a cache of E4M3 the four warps that widen its codes are the bound: 417 us.
 // 64 keys a step with two places for the scores took 450 us instead of 349 (twice the waits for as
 // many products), weights ahead of the maximum 27 us more (another pass over the registers).
 #include "ar_internal.h"
@@ -678,6 +678,10 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         } else if (F8 && warp >= 12) {
             // 16 codes a lane at a time, of 32 keys a warp
             constexpr int kLanes = DP / 16, kStep = 32 / kLanes;    // lanes of a key, keys at a time
+            // Loads in flight: the chain of a load, the conversions and the stores, one after the
+            // other, took 455 us for 8192 tokens, two at a time 438, four 417, eight spill (496).
+            constexpr int kAhead = 4;
+            static_assert(32 / kStep % kAhead == 0, "loads ahead");
             const int chunk = lane % kLanes;
             uint32_t it = 0;
             while (ok && take(true)) {
@@ -691,22 +695,31 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
                             break;
                         const int key0 = key_of(w.p, 2 * x + (warp - 12) / 2) + 32 * (warp & 1);
 #pragma unroll
-                        for (int i = 0; i < 32 / kStep; ++i) {
-                            const int in = kStep * i + lane / kLanes, at = 32 * (warp - 12) + in;
-                            uint4 c, lo, hi;
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
-                                         : "r"(raw_at + r * F::raw + at * DP + 16 * chunk)
-                                         : "memory");
-                            const int key = key0 + in;
-                            // values that no row sees need not be finite
-                            if (kv && !(key < w.p.end && (key >= w.p.low || key < w.p.sinks)))
-                                c = make_uint4(0, 0, 0, 0);
-                            widen<D>(c, lo, hi);
-                            const uint32_t to = ring + s * F::tile + chunk / 4 * F::half + at * 128;
-                            const int c0 = chunk % 4 * 2;
-                            put16(to + ((c0 ^ (at & 7)) << 4), lo);
-                            put16(to + (((c0 + 1) ^ (at & 7)) << 4), hi);
+                        for (int i0 = 0; i0 < 32 / kStep; i0 += kAhead) {
+                            uint4 codes[kAhead];
+#pragma unroll
+                            for (int i = 0; i < kAhead; ++i) {
+                                const int at = 32 * (warp - 12) + kStep * (i0 + i) + lane / kLanes;
+                                uint4& c = codes[i];
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                                             : "r"(raw_at + r * F::raw + at * DP + 16 * chunk)
+                                             : "memory");
+                            }
+#pragma unroll
+                            for (int i = 0; i < kAhead; ++i) {
+                                const int in = kStep * (i0 + i) + lane / kLanes, at = 32 * (warp - 12) + in;
+                                const int key = key0 + in;
+                                uint4 c = codes[i], lo, hi;
+                                // values that no row sees need not be finite
+                                if (kv && !(key < w.p.end && (key >= w.p.low || key < w.p.sinks)))
+                                    c = make_uint4(0, 0, 0, 0);
+                                widen<D>(c, lo, hi);
+                                const uint32_t to = ring + s * F::tile + chunk / 4 * F::half + at * 128;
+                                const int c0 = chunk % 4 * 2;
+                                put16(to + ((c0 ^ (at & 7)) << 4), lo);
+                                put16(to + (((c0 + 1) ^ (at & 7)) << 4), hi);
+                            }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
