@@ -26,7 +26,7 @@
 // copy); one sequence of 131072, 64 / 8 heads: 84 us, 6.4 TB/s; E4M3, 128 x 2048-4096, 64 / 8
 // heads: 133 to 143 us, 5.7 to 6.1 TB/s, what is left goes to the widening of the codes (issue
 // slots 55% used).  4 x 500-1000 tokens, 8 / 1 heads: 7.6 us, two launches and two reads behind
-// one another (page number, keys) with a join.  33 windows of 1000, 28 / 4 heads of 80: 17 us,
+// one another (page number, keys) with a join.  33 windows of 1000, 28 / 4 heads of 80: 16.3 us,
 // where a block has some ten units and fills its ring anew for the join of each item.
 #include "ar_internal.h"
 #include "attention_internal.h"
@@ -187,7 +187,7 @@ struct Cursor {
 template <class D, int DP, bool F8>
 struct Form {
     static constexpr int bytes = F8 ? 1 : 2;            // of an element of the cache
-    static constexpr int pitch = DP * bytes;            // of a slice's row
+    static constexpr int pitch = (DP <= 64 ? 64 : 128) * bytes;     // of a slice's row
     static constexpr int SL = kTile / pitch;            // keys of a slice
     static constexpr bool bf16 = !F8 && D::id == AR_DT_BF16;    // products' type
     // The weights are 2^up times e^{s_j - max}.  fp16 keeps 11 bits down to 2^-14 only and nothing
@@ -793,6 +793,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Spl
     // registers (j, n, e) and (j, n, e + 2)
     const int which = blockIdx.y * (kJoinThreads / 32) + (tid >> 5);
     const int e = which & 1, n = (which >> 1) % NB, j = (which >> 1) / NB;
+    if (j >= DP / 16)
+        return;
     const int h = head_of(n, e, t), at = ((j * NB + n) * 4 + e) * 32 + lane;
     float m = -INFINITY, l = 0.0f, f0 = 0.0f, f1 = 0.0f;
     for (int p0 = 0; p0 < d.x; p0 += kJoinAhead) {
@@ -867,16 +869,21 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     e = launch_after(decode_attention_kernel<D, DP, F8, NB>, blocks, kThreads, kSmem, s, a, sp, tiles);
     if (e != cudaSuccess || sp.whole || blocks == 1)
         return e;
-    return launch_after(join_kernel<D, DP, F8, NB>, dim3(blocks, DP / 16 * NB * 2 / (kJoinThreads / 32)),
-                        kJoinThreads, 0, s, a, sp);
+    constexpr int kJoinWarps = kJoinThreads / 32;
+    return launch_after(join_kernel<D, DP, F8, NB>,
+                        dim3(blocks, (DP / 16 * NB * 2 + kJoinWarps - 1) / kJoinWarps), kJoinThreads, 0, s,
+                        a, sp);
 }
 
 template <class D, bool F8>
 cudaError_t launch_d(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s)
 {
-    // heads in one or two groups of 8 columns
+    // heads in one or two groups of 8 columns; products of 96 elements where the head has no more (33
+    // windows of 1000, heads of 80: 17.2 -> 16.4 us; E4M3, 128 x 2048-4096 of 96: 204 -> 200)
     if (a.c.D <= 64)
         return a.G <= 8 ? launch_t<D, 64, F8, 1>(a, d, s) : launch_t<D, 64, F8, 2>(a, d, s);
+    if (a.c.D <= 96)
+        return a.G <= 8 ? launch_t<D, 96, F8, 1>(a, d, s) : launch_t<D, 96, F8, 2>(a, d, s);
     return a.G <= 8 ? launch_t<D, 128, F8, 1>(a, d, s) : launch_t<D, 128, F8, 2>(a, d, s);
 }
 
