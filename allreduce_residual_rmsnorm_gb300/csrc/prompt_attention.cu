@@ -352,27 +352,30 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
     pdl_wait();
     const uint32_t tmem = tmem_slot;
 
-    // pairs before each sequence; whether any has rows without a place
-    int before = 0;
-    bool short_one = false;
+    // pairs before each sequence; whether any has rows without a place.  Starts that decrease
+    // could give a row to several sequences, and more pairs than the host reckoned with.
+    unsigned before = 0;
+    bool short_one = false, falls = false;
 #pragma unroll 1
     for (int s0 = 0; s0 < a.c.S; s0 += kThreads) {
-        int n = 0, row0;
+        unsigned n = 0;
         if (s0 + tid < a.c.S) {
+            int row0;
             n = rows_of(a, s0 + tid, &row0);
-            short_one |= clamp_length(a.c, a.c.lengths[s0 + tid]) < n;
+            short_one |= clamp_length(a.c, a.c.lengths[s0 + tid]) < (int)n;
+            falls |= a.starts[s0 + tid + 1] < row0;
             n = (n + 2 * plan.tok - 1) / (2 * plan.tok);
         }
-        int upto = n;
+        unsigned upto = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, m);
+            const unsigned v = __shfl_up_sync(0xffffffffu, upto, m);
             upto += lane >= m ? v : 0;
         }
         if (lane == 31)
             scan_sh[warp] = upto;
         __syncthreads();
-        int all = 0;
+        unsigned all = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             upto += w < warp ? scan_sh[w] : 0;
@@ -381,9 +384,9 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         if (s0 + tid < a.c.S)
             first_pair[s0 + tid] = before + upto - n;
         before += all;
-        __syncthreads();
+        falls = __syncthreads_or(falls);
     }
-    const int pairs = before;
+    const int pairs = falls ? 0 : (int)before;
     if (tid == 0)
         first_pair[a.c.S] = pairs;
     short_one = __syncthreads_or(short_one);

@@ -150,20 +150,21 @@ __global__ void __launch_bounds__(kThreads, kAhead == kMostAhead ? 8 : 0)
     };
     int index, page;
     if (a.starts) {
+        bool falls = false;
         for (int s = tid; s < a.c.S; s += kThreads) {
             if (s >= kThreads) {
                 lo = a.starts[s];
                 hi = a.starts[s + 1];
                 length = a.c.lengths[s];
             }
-            // one sequence has the row, unless the starts run backwards
+            falls |= lo > hi;
+            // one sequence has the row, unless the starts decrease: then none has any
             if (lo >= 0 && lo <= row && row < hi && hi <= a.T && atomicExch(&found, 1) == 0) {
                 place[0] = clamp_length(a.c, length) - (hi - row);
                 place[1] = page_of(s, place[0]);
             }
         }
-        __syncthreads();
-        if (!found)
+        if (__syncthreads_or(falls) || !found)
             return;
         index = place[0];
         page = place[1];

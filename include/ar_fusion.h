@@ -640,8 +640,9 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
  * number of its rows.  A row whose index is negative (more rows than lengths[b])
  * has no place in the cache and sees no key.  Rows outside starts[0] ..
  * starts[sequences] - 1 are not read and what belongs to them is left as it was.
- * starts may not decrease nor leave 0 .. tokens: where it does, rows are left as
- * they were, nothing else is touched.
+ * starts may not decrease nor leave 0 .. tokens.  Where they decrease no sequence has a row;
+ * where one leaves 0 .. tokens the sequences on both sides of it have none.  Rows of no
+ * sequence are left as they were, and nothing else is touched.
  *
  * Pages.  The token of index i of sequence b lies in page
  * page_table[b][i / page_size], row i % page_size.  Entries behind a sequence's
