@@ -178,6 +178,13 @@ int take_attention(const ar_kv_cache* cache, const ar_head_rows* q, const ar_hea
 
 }  // namespace
 
+std::mutex& arf::launches_with(const void* workspace)
+{
+    static std::mutex locks[64];
+    // the upper bits of a product with 2^64 over the golden ratio: neighbours far apart
+    return locks[(uint64_t)(uintptr_t)workspace * 0x9e3779b97f4a7c15ull >> 58];
+}
+
 extern "C" {
 
 int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,

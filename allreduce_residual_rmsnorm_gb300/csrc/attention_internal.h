@@ -2,6 +2,8 @@
 // Each returns the cudaError_t of its launch; arguments are already checked.
 #pragma once
 
+#include <mutex>
+
 #include "expert_internal.h"
 
 namespace arf {
@@ -45,6 +47,11 @@ struct AttentionArgs {
 };
 cudaError_t launch_decode_attention(int dtype, bool e4m3, const AttentionArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_attention(int dtype, bool e4m3, const AttentionArgs& a, cudaStream_t s);
+// Held over the two launches of a call that is split.  Threads that call on one stream may share a
+// workspace; another's kernel between this one's and its join would overwrite the pieces, and each
+// join would add up what it finds, with the sizes of its own call.  A lock for the workspace's
+// address: calls with workspaces of their own seldom meet.
+std::mutex& launches_with(const void* workspace);
 
 // tokens of a sequence that the table can hold
 __device__ __forceinline__ int clamp_length(const CacheArgs& c, int length)

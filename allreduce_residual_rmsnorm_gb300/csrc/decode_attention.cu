@@ -866,8 +866,12 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         sp.desc = reinterpret_cast<int4*>(a.work);
         sp.parts = a.work + 16 * (int64_t)blocks;
     }
+    const bool joined = !sp.whole && blocks > 1;
+    std::unique_lock<std::mutex> both(launches_with(a.work), std::defer_lock);
+    if (joined)
+        both.lock();
     e = launch_after(decode_attention_kernel<D, DP, F8, NB>, blocks, kThreads, kSmem, s, a, sp, tiles);
-    if (e != cudaSuccess || sp.whole || blocks == 1)
+    if (e != cudaSuccess || !joined)
         return e;
     constexpr int kJoinWarps = kJoinThreads / 32;
     return launch_after(join_kernel<D, DP, F8, NB>,

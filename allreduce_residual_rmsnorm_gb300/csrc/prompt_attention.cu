@@ -1123,9 +1123,13 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
         plan.desc = reinterpret_cast<int4*>(a.work);
         plan.parts = a.work + 16 * (int64_t)blocks;
     }
+    const bool joined = !plan.whole && blocks > 1;
+    std::unique_lock<std::mutex> both(launches_with(a.work), std::defer_lock);
+    if (joined)
+        both.lock();
     e = launch_after(prompt_attention_kernel<D, DP, F8>, blocks, Regs<F8>::threads, smem, s, map_q, map_k,
                      map_v, a, plan, d.status + kStatusWords);
-    if (e != cudaSuccess || plan.whole || blocks == 1)
+    if (e != cudaSuccess || !joined)
         return e;
     return launch_after(join_kernel<D, DP>, dim3(blocks, DP / kJoinDims), 2 * kRows, 0, s, a, plan);
 }

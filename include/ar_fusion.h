@@ -629,8 +629,8 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
  * All of them are asynchronous on `stream`, run on the current device and keep
  * nothing between calls.  The two attention calls use a workspace of the caller:
  * its contents mean nothing before or after a call, so calls that follow one
- * another (on one stream, or ordered by events; captured or not) share one,
- * and calls that may run at the same time each need their own.  Outputs must not
+ * another (on one stream, from one host thread or several, or ordered by events; captured or
+ * not) share one, and calls that may run at the same time each need their own.  Outputs must not
  * overlap inputs, but for q_out of ar_fusion_rope_append, which may be q itself.
  *
  * Sequences.  `sequences` of them, with lengths[b] tokens each, the new ones
