@@ -31,6 +31,28 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
+// A host thread whose first call this is has no context yet: the runtime's calls take the current
+// device's, the driver's answer that there is none.
+bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, void* base, const cuuint64_t* sizes,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+            CUtensorMapL2promotion promotion)
+{
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    const auto once = [&] {
+        return fn(map, type, (cuuint32_t)dims, base, sizes, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = once();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = once();
+    return r == CUDA_SUCCESS;
+}
+
 // Looked up once per device
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -66,34 +88,24 @@ cudaError_t device_info(DeviceInfo* out)
 bool byte_tensor_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t depth,
                      uint32_t box_rows)
 {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn)
-        return false;
     const cuuint64_t dims[2] = {depth, rows};
     const cuuint64_t strides[1] = {depth};
     const cuuint32_t box[2] = {128, box_rows};
-    const cuuint32_t steps[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool out_tensor_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, int dtype,
                     uint32_t box_rows, uint32_t box_cols)
 {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn)
-        return false;
     const CUtensorMapDataType type = dtype == AR_DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                      : dtype == AR_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * (uint64_t)elem_bytes(dtype)};
     const cuuint32_t box[2] = {box_cols, box_rows};
-    const cuuint32_t steps[2] = {1, 1};
-    return fn(map, type, 2, base, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, type, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 // Which kernel, by the time that each would take, in microseconds of this device.
@@ -147,9 +159,6 @@ cudaError_t launch_matmul(int dtype, const MatmulArgs& a, cudaStream_t s)
 bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64_t (&dims)[4],
                      const uint64_t (&strides)[3], const uint32_t (&box)[4])
 {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn)
-        return false;
     const bool codes = dtype == AR_DT_E4M3;
     const CUtensorMapDataType type = codes                 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : dtype == AR_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -157,11 +166,9 @@ bool rows_tensor_map(CUtensorMap* map, int dtype, const void* base, const uint64
     const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
     const cuuint64_t s[3] = {strides[0], strides[1], strides[2]};
     const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
-    const cuuint32_t steps[4] = {1, 1, 1, 1};
-    return fn(map, type, 4, const_cast<void*>(base), d, s, b, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              codes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, type, 4, const_cast<void*>(base), d, s, b,
+                  codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  codes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 int read_status(int which, void* stream, int* detail, const char* message)

@@ -1,4 +1,6 @@
 """What the attention-layer calls promise at the edges of their contract."""
+import threading
+
 import pytest
 import torch
 
@@ -92,3 +94,95 @@ def test_starts_that_decrease_or_leave_the_rows(workspace, T, starts):
     want_q = q.clone()
     want_q[dead] = 5.0
     assert same(q_out, want_q)
+
+
+# ------------------------------------------- threads that share a stream and a workspace
+
+@pytest.mark.parametrize("native", [True, False])
+def test_two_threads_on_one_stream_with_one_workspace(workspace, monkeypatch, native):
+    """Split calls of other sizes and kinds, queued by two threads: each has its own answer."""
+    if not native:
+        monkeypatch.setattr(B, "_native", None)
+    stream = torch.cuda.Stream()
+
+    def job(lengths, new, H, K, seed):
+        pages = R.Pages(lengths, 16, K, 64, BF16, seed=seed, junk=False)
+        kc, vc, table, dev_lengths, _ = pages.cuda()
+        T = sum(new) if new else len(lengths)
+        q = torch.randn(T, H, 64, generator=gen(seed)).to(BF16).cuda()
+        starts = None if new is None else ints(*(sum(new[:b]) for b in range(len(new) + 1))).cuda()
+
+        def call(out):
+            if new is None:
+                B.ar_fusion_decode_attention(q, kc, vc, table, dev_lengths, out, workspace, stream=stream)
+            else:
+                B.ar_fusion_prompt_attention(q, kc, vc, table, dev_lengths, starts, out, workspace,
+                                             stream=stream)
+        return call, [torch.empty_like(q) for _ in range(300)]
+
+    jobs = [job([3000, 700], None, 8, 2, 5), job([900, 40, 2000], [7, 40, 3], 4, 2, 6)]
+    want = []
+    for call, outs in jobs:
+        torch.cuda.synchronize()
+        call(outs[0])
+        torch.cuda.synchronize()
+        want.append(outs[0].clone())
+
+    failed = []
+
+    def work(call, outs):
+        try:
+            for out in outs:
+                call(out)
+        except Exception as e:      # noqa: BLE001 -- a thread's error must reach the test
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and B.ar_fusion_attention_status() == (B.AR_OK, -1)
+    for (_, outs), w in zip(jobs, want):
+        assert all(torch.equal(out, w) for out in outs)
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("call", ["prompt", "product", "experts' product"])
+def test_the_first_call_of_a_thread(workspace, monkeypatch, call, native):
+    """A host thread that has made no CUDA call yet."""
+    if not native:
+        monkeypatch.setattr(B, "_native", None)
+    n = 300
+    if call == "prompt":
+        pages = R.Pages([n], 16, 2, 64, BF16, junk=False)
+        kc, vc, table, lengths, _ = pages.cuda()
+        q = torch.randn(n, 4, 64, generator=gen(1)).to(BF16).cuda()
+        starts = ints(0, n).cuda()
+        make = lambda: torch.empty_like(q)                                       # noqa: E731
+        run = lambda out: B.ar_fusion_prompt_attention(                          # noqa: E731
+            q, kc, vc, table, lengths, starts, out, workspace)
+    else:
+        a, b = (torch.randint(0, 120, (m, 256), generator=gen(m), dtype=torch.uint8).cuda() for m in (n, 128))
+        sa, sb = torch.ones(n, 2).cuda(), torch.ones(1, 2).cuda()
+        make = lambda: torch.empty(n, 128, device="cuda")                        # noqa: E731
+        run = lambda out: B.ar_fusion_matmul_fp8(a, sa, b, sb, out)              # noqa: E731
+        if call != "product":
+            offsets = ints(0, n).cuda()
+            run = lambda out: B.ar_fusion_expert_matmul_fp8(                     # noqa: E731
+                a, sa, b[None], sb[None], offsets, out)
+    want, got = make(), make()
+    run(want)
+    torch.cuda.synchronize()
+    failed = []
+
+    def first():
+        try:
+            run(got)
+        except Exception as e:      # noqa: BLE001 -- a thread's error must reach the test
+            failed.append(e)
+    t = threading.Thread(target=first)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not failed and torch.equal(got, want)
