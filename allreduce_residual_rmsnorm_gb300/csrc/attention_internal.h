@@ -53,6 +53,18 @@ cudaError_t launch_prompt_attention(int dtype, bool e4m3, const AttentionArgs& a
 // address: calls with workspaces of their own seldom meet.
 std::mutex& launches_with(const void* workspace);
 
+// Unit `in` of a list of items of n units each.  The units of one sequence's items pass 2^31 (at
+// 2^30 tokens and 128 heads), its items and the units of one do not.
+struct UnitPlace {
+    int item, unit;
+};
+__host__ __device__ inline UnitPlace unit_place(long long in, int n)
+{
+    if (in >> 31 == 0)
+        return UnitPlace{(int)((unsigned)in / (unsigned)n), (int)((unsigned)in % (unsigned)n)};
+    return UnitPlace{(int)(in / n), (int)(in % n)};
+}
+
 // tokens of a sequence that the table can hold
 __device__ __forceinline__ int clamp_length(const CacheArgs& c, int length)
 {

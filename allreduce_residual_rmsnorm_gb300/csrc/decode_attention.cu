@@ -362,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
                 const int n = units_of(seen_of<SL>(a, a.c.lengths[s]));
                 const long long end = at + (long long)n * heads;
                 if (u0 < end) {
-                    const int in = (int)(u0 - at);
+                    const UnitPlace p = unit_place(u0 - at, n);
                     begin_sh[0] = s;
-                    begin_sh[1] = in / n;
-                    begin_sh[2] = in % n;
+                    begin_sh[1] = p.item;
+                    begin_sh[2] = p.unit;
                     break;
                 }
                 at = end;
