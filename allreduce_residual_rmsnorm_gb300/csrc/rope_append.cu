@@ -7,7 +7,7 @@
 // and written once.  The row's place (its sequence, length and page) is a chain of
 // three loads, and the elements do not wait for it: the first kAhead pieces of
 // every thread are loaded before it.  What bounds it is memory and the latency of that chain (8
-// rows on an SM at a time): 4 x 2048 rows of 32 + 8 + 8 heads 35.9 us, 5.6 TB/s (stores without
+// rows on an SM at a time): 4 x 2048 rows of 32 + 8 + 8 heads 36.1 us, 5.6 TB/s (stores without
 // the streaming hint 4% more, 7 blocks on an SM 5%, blocks of 64, 96, 192 and 256 threads 17, 2,
 // 7 and 40%); 64 rows of 8 + 1 + 1 heads 2.1, a launch.
 #include "ar_internal.h"
@@ -30,30 +30,12 @@ struct Heads {
     }
 };
 
-// position * f / pi modulo 2, with f / pi = hi + lo: the product's high part loses
-// whole turns exactly (the remainder of two floats by a power of two is exact), its
-// rounding error comes back from the fused multiply-add.  |p| < 2^24: exact as a float.
-__device__ __forceinline__ float half_turns(float p, float hi, float lo)
-{
-    const float u = p * hi;
-    const float err = fmaf(p, hi, -u);
-    return (u - 2.0f * rintf(0.5f * u)) + fmaf(p, lo, err);
-}
-
-// cos and sin of position * f.  1 / pi in two floats; positions in two parts below
-// 2^24.  Off by a few 2^-24 at any position, where the product in 32 bits is off by
-// position * 2^-24.
+// cos and sin of an angle (half_turns: off by 2^-25 of half a turn at any position, where the
+// product in 32 bits is off by position * 2^-24).  A frequency that is not finite gives NaN.
 __device__ __forceinline__ float2 turn(int position, float f)
 {
-    const float kInvPi = 0.318309873f, kInvPiLow = 1.28412765e-8f;
-    const float hi = f * kInvPi;
-    const float lo = fmaf(f, kInvPi, -hi) + f * kInvPiLow;
-    const int low = position & 0xfff;
-    float t = half_turns((float)low, hi, lo);
-    if (position != low)
-        t += half_turns((float)(position >> 12), 4096.0f * hi, 4096.0f * lo);
     float2 r;
-    sincospif(t, &r.y, &r.x);
+    sincospif(half_turns(position, turns_of(f)) + (f - f), &r.y, &r.x);
     return r;
 }
 

@@ -1,5 +1,6 @@
 // Host-side checks of the attention-layer calls' own arithmetic (the same source the
-// kernels use, compiled for the CPU).  One check a run, by name; 0: it holds.
+// kernels use, compiled for the CPU).  One check a run, by name; 0: it holds (or was printed).
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <random>
@@ -42,11 +43,36 @@ int check_places()
     return 0;
 }
 
+// Angles for the test to look at: position, bits of the frequency, bits of half_turns.
+int print_turns()
+{
+    const auto line = [](int position, float f) {
+        const float t = arf::half_turns(position, arf::turns_of(f));
+        uint32_t a, b;
+        memcpy(&a, &f, 4);
+        memcpy(&b, &t, 4);
+        printf("%d %u %u\n", position, a, b);
+    };
+    const int ends[] = {0, 1, -1, 4095, 4096, (1 << 24) - 1, (1 << 24) + 1, INT32_MAX, INT32_MIN, -70000};
+    const float fs[] = {0.0f, 1.0f, -1.0f, 1e-4f, 2e-7f, 0.99999994f, 1.9999999f, 3.1415927f, 1000.5f,
+                        1e-30f, 1e-42f};
+    for (int p : ends)
+        for (float f : fs)
+            line(p, f);
+    for (int i = 0; i < 20000; ++i) {
+        const int bits = pick(1, 32);
+        const int position = (int)(uint32_t)(rng() >> (64 - bits));
+        const float u = (float)(rng() >> 40) * 0x1p-24f;
+        line(i & 1 ? -position : position, i % 3 ? powf(10.0f, -7.0f * u) : powf(2.0f, 10.0f * u));
+    }
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
 {
-    const struct { const char* name; int (*run)(); } checks[] = {{"places", check_places}};
+    const struct { const char* name; int (*run)(); } checks[] = {{"places", check_places}, {"turns", print_turns}};
     for (const auto& c : checks)
         if (argc > 1 && strcmp(argv[1], c.name) == 0)
             return c.run();

@@ -1,5 +1,7 @@
 """What the attention-layer calls promise at the edges of their contract."""
+import math
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
@@ -186,3 +188,52 @@ def test_the_first_call_of_a_thread(workspace, monkeypatch, call, native):
     t.join()
     torch.cuda.synchronize()
     assert not failed and torch.equal(got, want)
+
+
+# ------------------------------------------- angles of far positions
+
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bits", [12, 24, 26, 28, 30, 31])
+def test_angles_of_far_positions(cuda_lib, bits, interleaved):
+    """Rows (1, 0) give cos and sin themselves, and where those are small the output's own rounding
+    hides nothing.  The angle: half a turn off by 2^-25 and 2^-32, times pi 1.6 U; cos and sin by
+    2 U; the products with 1 and 0 are exact."""
+    T, D = 256, 128
+    g = gen(bits)
+    where = torch.randint(1 << (bits - 1), 1 << bits, (T,), generator=g)
+    where[::2] *= -1
+    where[:3] = torch.tensor([(1 << bits) - 1, -(1 << bits), 1 << (bits - 1)])
+    f = 1e4 ** (-torch.arange(0, D, 2) / D)
+    f[1] = -f[1]
+    x = torch.zeros(T, 1, D)
+    first = slice(0, D, 2) if interleaved else slice(0, D // 2)
+    second = slice(1, D, 2) if interleaved else slice(D // 2, D)
+    x[:, :, first] = 1.0
+    pages = R.Pages([T], 16, 1, D, FP16, junk=False)
+    kc, vc, table, lengths, _ = pages.cuda()
+    dx = x.to(FP16).cuda()
+    out = torch.empty_like(dx)
+    B.ar_fusion_rope_append(dx, dx, dx, kc, vc, table, lengths, f.cuda(), out, starts=ints(0, T).cuda(),
+                            positions=where.to(torch.int32).cuda(), interleaved=interleaved)
+    exact = [Fraction(v) / PI for v in f.tolist()]
+    half = torch.tensor([[float(p * e % 2) for e in exact] for p in where.tolist()], dtype=torch.float64)
+    got = out.cpu().double()[:, 0]
+    for part, want in ((first, torch.cos(math.pi * half)), (second, torch.sin(math.pi * half))):
+        off = (got[:, part] - want).abs()
+        tol = 4 * R.U + R.half_step(FP16) * want.abs() + 2.0 ** -25
+        assert bool((off <= tol).all()), ((off - tol).amax() / R.U, int((off > tol).sum()))
+    at = pages.table[0].long()[torch.arange(T) // 16]
+    assert torch.equal(kc[at, torch.arange(T) % 16], out)
+
+
+def test_a_frequency_that_is_not_finite_gives_nan(cuda_lib):
+    pages = R.Pages([4], 16, 1, 16, BF16, junk=False)
+    kc, vc, table, lengths, _ = pages.cuda()
+    x = torch.ones(4, 1, 16, dtype=BF16, device="cuda")
+    f = torch.tensor([1.0, math.inf, math.nan, -math.inf, 0.5, 0.0, 0.25, -1.0])
+    B.ar_fusion_rope_append(x, x, x, kc, vc, table, lengths, f.cuda(), starts=ints(0, 4).cuda())
+    bad = ~torch.isfinite(f)
+    assert torch.equal(torch.isnan(x.cpu()[:, 0]), torch.cat([bad, bad]).expand(4, 16))

@@ -1,6 +1,8 @@
 """The attention-layer kernels' own arithmetic, compiled for the host (no GPU)."""
 import os
+import struct
 import subprocess
+from fractions import Fraction
 
 import pytest
 
@@ -18,8 +20,28 @@ def check(tmp_path_factory):
     def run(name):
         r = subprocess.run([exe, name], capture_output=True, text=True)
         assert r.returncode == 0, r.stdout + r.stderr
+        return r.stdout
     return run
 
 
 def test_units_past_2_to_31(check):
     check("places")
+
+
+# to 2^-180
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+
+
+def test_angles_at_any_position(check):
+    """half_turns against exact arithmetic.  A turn's fixed-point part lacks 2 units of 2^-64 turns
+    from the inverse of 2 pi and one of each of two roundings down, times f where that is above 1;
+    the position takes them times itself, and they are rounded to a float once (2^-24 relative)."""
+    lines = check("turns").split("\n")[:-1]
+    assert len(lines) > 20000
+    for line in lines:
+        p, f, t = (int(x) for x in line.split())
+        f, t = (Fraction(struct.unpack("<f", struct.pack("<I", x))[0]) for x in (f, t))
+        off = (t - p * f / PI) % 2
+        off = min(off, 2 - off)
+        lacking = 2 * 4 * abs(p) * max(abs(f), 1) * Fraction(2) ** -64
+        assert off <= lacking + abs(t) * Fraction(2) ** -24, line
