@@ -378,15 +378,14 @@ __global__ void __launch_bounds__(kThreads, Fit<F8, NB>::blocks)
         if (seen_of<SL>(a, a.c.lengths[s]).n > 0)
             continue;
 #pragma unroll 1
-        for (int i = tid; i < a.Hq * (a.c.D / 8); i += kThreads) {
-            const int h = i / (a.c.D / 8), c = i % (a.c.D / 8);
-            *reinterpret_cast<uint4*>(a.out.p + s * a.out.row + h * a.out.head + 16 * c) =
-                make_uint4(0, 0, 0, 0);
-        }
-        if (a.lse)
+        for (int h = tid; h < a.Hq; h += kThreads) {
+            uint8_t* to = a.out.p + s * a.out.row + h * a.out.head;
 #pragma unroll 1
-            for (int h = tid; h < a.Hq; h += kThreads)
+            for (int c = 0; c < a.c.D / 8; ++c)
+                *reinterpret_cast<uint4*>(to + 16 * c) = make_uint4(0, 0, 0, 0);
+            if (a.lse)
                 a.lse[(int64_t)s * a.Hq + h] = -INFINITY;
+        }
     }
     if (tid == 0 && !sp.whole)
         sp.desc[block] = make_int4(0, 0, 0, 0);

@@ -237,3 +237,21 @@ def test_a_frequency_that_is_not_finite_gives_nan(cuda_lib):
     B.ar_fusion_rope_append(x, x, x, kc, vc, table, lengths, f.cuda(), starts=ints(0, 4).cuda())
     bad = ~torch.isfinite(f)
     assert torch.equal(torch.isnan(x.cpu()[:, 0]), torch.cat([bad, bad]).expand(4, 16))
+
+
+# ------------------------------------------- as many heads as there may be
+
+def test_one_token_without_keys_and_with_many_heads(workspace):
+    """2^27 query heads of 128 elements: 2^31 vectors of 16 bytes of zeros.  (The heads overlap, 16
+    bytes apart, so that they need no 34 GB.)"""
+    H, K, D = 1 << 27, 1 << 20, 128
+    rows = torch.full((8 * H + D,), 3.0, dtype=BF16, device="cuda")
+    q = rows.as_strided((1, H, D), (8 * H, 8, 1))
+    out_rows = torch.full((8 * H + D,), 5.0, dtype=BF16, device="cuda")
+    out = out_rows.as_strided((1, H, D), (8 * H, 8, 1))
+    pages = torch.zeros(8 * (K + 8) + D, dtype=BF16, device="cuda")
+    cache = pages.as_strided((1, 8, K, D), (8, 8, 8, 1))
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    B.ar_fusion_decode_attention(q, cache, cache, table, ints(0).cuda(), out, workspace)
+    torch.cuda.synchronize()
+    assert int((out_rows == 0).sum()) == 8 * H + D - 8 and bool((out_rows[8 * H + D - 8:] == 5.0).all())
