@@ -19,7 +19,8 @@
 //   warp 11: finds the items ahead of the others (each for itself took 1.5 us an item)
 //
 // Items (a pair of tiles and a head) are worked off by one block per SM: where there
-// are many, whole ones, the longest first; where there are few, the steps of all items
+// are many, whole ones, dealt out in the order of the sequences (in each the last tokens, which see
+// most, first); where there are few, the steps of all items and what the ends of items take (share_of)
 // are one list and a block takes an equal share of it.  Items that several blocks
 // share are added up by join_kernel from sums, maxima and totals in the workspace.
 //
@@ -28,7 +29,7 @@
 // product's burst), 1.5 us a step.  With a window of 1024 (3 x 3000-5000 tokens, 64 / 8 heads: 273
 // us, 1.17 PFLOP/s) a seventh of the products is of keys that their row does not see, and an item of
 // nine steps costs 3 us beside them: masks on its first and last steps, its output.  Chunks of some
-// hundred tokens (13 x 40-400 on 600-3000, 14 / 2 heads of 64: 37 us) are 14 steps a block, and as
+// hundred tokens (13 x 40-400 on 600-3000, 14 / 2 heads of 64: 34.5 us) are 14 steps a block, and as
 // long again for the start, the ends of the items and the join.
 // Over a cache of E4M3 the four warps that widen its codes are the bound: 417 us.
 // 64 keys a step with two places for the scores took 450 us instead of 349 (twice the waits for as
@@ -154,7 +155,7 @@ constexpr uint32_t kItems = 4;                      // found ahead
 // The items of a block, one after the other.
 struct Walk {
     int item, items, x, step;   // whole items: `step` counts them
-    int left;                   // of a share: units left
+    int left;                   // of a share: units left (share_of an item's steps)
     int end, total;             // of a share: where it ends in the list, and the list
     int blocks;
 
@@ -164,7 +165,7 @@ struct Walk {
         for (;;) {
             if (plan.whole) {
                 // back and forth over the blocks, so that the first does not get the
-                // longest of every round
+                // longest of a sequence in every round
                 const long long base = (long long)step * gridDim.x;
                 const int at = step & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
                 if (base >= items)
@@ -184,10 +185,10 @@ struct Walk {
             to->x1 = plan.whole ? to->p.n : min(to->p.n, x + left);
             to->end_block = 0;
             if (!plan.whole) {
-                left -= to->x1 - x;
+                left -= share_of(to->p.n) - x;
                 ++item;
                 x = 0;
-                if (to->x1 < to->p.n)       // the block that has the item's last unit
+                if (to->x1 < to->p.n)       // the block that has the item's last step
                     to->end_block =
                         (int)(((long long)(end + (to->p.n - to->x1)) * blocks - 1) / total);
             }
@@ -393,13 +394,13 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
 
     Walk walk{0, pairs * a.c.heads, 0, 0, 0, 0, 1, (int)gridDim.x};
     if (!plan.whole) {
-        // this block's share of the list of steps, and where it begins
+        // this block's share of the list of units, and where it begins
         const int per = (pairs + kThreads - 1) / kThreads;
         const int f0 = min(tid * per, pairs), f1 = min(f0 + per, pairs);
         int mine = 0, n0 = 0;
 #pragma unroll 1
         for (int f = f0; f < f1; ++f) {
-            n0 = pair_at(a, plan.tok, first_pair, f).n;
+            n0 = share_of(pair_at(a, plan.tok, first_pair, f).n);
             mine += n0 * a.c.heads;
         }
         int upto = mine;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(Regs<F8>::threads, 1)
         if (walk.left && u0 >= at && u0 < upto) {
 #pragma unroll 1
             for (int f = f0; f < f1; ++f) {
-                const int n = per == 1 ? n0 : pair_at(a, plan.tok, first_pair, f).n;
+                const int n = per == 1 ? n0 : share_of(pair_at(a, plan.tok, first_pair, f).n);
                 const int end = at + n * a.c.heads;
                 if (u0 < end) {
                     const int in = u0 - at;
@@ -1110,14 +1111,15 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     int blocks = d.sms;
     const int64_t fit = (int64_t)(a.work_bytes / (16 + 2 * Shape<DP>::part));
     const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
-    const int64_t most = items * ((keys + kKeys - 1) / kKeys + 1);     // steps, all in one list
-    plan.whole = items >= 4ll * d.sms || fit < 2 || most >= 1 << 30;
+    const int64_t steps = items * ((keys + kKeys - 1) / kKeys + 1);     // at most
+    plan.whole = items >= 4ll * d.sms || fit < 2 || steps + kItemEnd * items >= 1 << 30;
     if (plan.whole) {
         if (items < blocks)
             blocks = (int)items;
     } else {
-        if (most < blocks)
-            blocks = (int)most;
+        // no block for an item's end alone, where there is one for each step
+        if (steps < blocks)
+            blocks = (int)steps;
         if (fit < blocks)
             blocks = (int)fit;
         plan.desc = reinterpret_cast<int4*>(a.work);

@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstring>
 #include <random>
+#include <vector>
 
 #include "attention_internal.h"
 
@@ -43,6 +44,43 @@ int check_places()
     return 0;
 }
 
+// Equal shares of a list of items: steps and ends of items (two steps' time each) of the busiest block
+// against the mean.
+int check_shares()
+{
+    for (int trial = 0; trial < 200; ++trial) {
+        std::vector<int> items;
+        const int kind = trial % 4, n = pick(20, 600);
+        for (int i = 0; i < n; ++i)
+            items.push_back(kind == 0 ? pick(1, 4) : kind == 1 ? (n - i + 7) / 8 : kind == 2 ? pick(0, 200)
+                                                                                  : i ? 1 : 500);
+        long long total = 0;
+        for (int x : items)
+            total += arf::share_of(x);
+        const int blocks = total < 152 ? (int)total : 152;
+        std::vector<double> busy(blocks);
+        double all = 0;
+        long long at = 0;
+        for (int x : items) {
+            for (int step = 0; step < x; ++step) {
+                // the last block whose share begins at this step or before it
+                const int b = (int)(((at + step + 1) * blocks - 1) / total);
+                busy[b] += 1;
+                if (step + 1 == x)
+                    busy[b] += 2;
+            }
+            all += x ? x + 2 : 0;
+            at += arf::share_of(x);
+        }
+        double most = 0;
+        for (double b : busy)
+            most = b > most ? b : most;
+        // a share's whole units, and the end of an item that it has the last step of
+        HOLDS(most <= all / blocks + 3);
+    }
+    return 0;
+}
+
 // Angles for the test to look at: position, bits of the frequency, bits of half_turns.
 int print_turns()
 {
@@ -72,7 +110,8 @@ int print_turns()
 
 int main(int argc, char** argv)
 {
-    const struct { const char* name; int (*run)(); } checks[] = {{"places", check_places}, {"turns", print_turns}};
+    const struct { const char* name; int (*run)(); } checks[] = {{"places", check_places}, {"shares", check_shares},
+                                                          {"turns", print_turns}};
     for (const auto& c : checks)
         if (argc > 1 && strcmp(argv[1], c.name) == 0)
             return c.run();

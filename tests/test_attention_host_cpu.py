@@ -28,6 +28,10 @@ def test_units_past_2_to_31(check):
     check("places")
 
 
+def test_blocks_that_share_a_prompts_items_have_equal_work(check):
+    check("shares")
+
+
 # to 2^-180
 PI = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
 
