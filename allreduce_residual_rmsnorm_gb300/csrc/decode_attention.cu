@@ -851,14 +851,17 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     // at most so many units
     constexpr int unit = kWarps * Form<D, DP, F8>::SL;
     const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
-    const int64_t most = ((keys + unit - 1) / unit + 1) * a.c.S * a.c.heads * tiles;
+    const int64_t items = (int64_t)a.c.S * a.c.heads * tiles, most = ((keys + unit - 1) / unit + 1) * items;
     int blocks = Fit<F8, NB>::blocks * d.sms;
     if (most < blocks)
         blocks = (int)most;
-    // the workspace: a line for each block, then its two parts
+    // The workspace: a line for each block, then its two parts.  Without room for as many blocks as
+    // whole items keep busy, or one an SM, items stay whole (one sequence of 131072, 64 / 8 heads: 0.5 MB
+    // 568 us, 4 MB 93, 8 MB 85, none 2230; 64 x 800-8000, 32 / 8 heads, 512 items: 269, from 4 MB on 188).
     const int64_t fit = (int64_t)(a.work_bytes / (16 + 2 * part_bytes<DP>()));
+    const int busy = blocks < d.sms ? blocks : d.sms;
     Split sp{};
-    sp.whole = fit < (blocks < d.sms ? blocks : d.sms);
+    sp.whole = fit < (items < busy ? items : busy);
     if (!sp.whole) {
         if (fit < blocks)
             blocks = (int)fit;

@@ -1112,7 +1112,19 @@ cudaError_t launch_t(const AttentionArgs& a, const DeviceInfo& d, cudaStream_t s
     const int64_t fit = (int64_t)(a.work_bytes / (16 + 2 * Shape<DP>::part));
     const int64_t keys = (int64_t)a.c.max_pages << a.c.page_shift;
     const int64_t steps = items * ((keys + kKeys - 1) / kKeys + 1);     // at most
-    plan.whole = items >= 4ll * d.sms || fit < 2 || steps + kItemEnd * items >= 1 << 30;
+    // Whole items or equal shares.  The host knows neither lengths nor how many items there are, only
+    // the most there can be.  From four an SM on they are dealt out whole: a prompt of 8192 tokens, 32 /
+    // 8 heads, 330 us; but one of 131072 among 127 of 1000, 4 new tokens each, 64 / 8 heads, is one
+    // block's work, 1267 us where its bytes take 158.  Below that shares win where lengths are uneven
+    // or new tokens few (60 x 4 on 500-32000, 64 / 8 heads, 306 us, whole 367; 512 behind 4000, 32 / 8
+    // heads, 43 and 56), whole items for prompts without a cached part (3000 tokens, 32 / 8 heads, 60,
+    // in shares 78; 700, twice, 17.5 and 27).
+    // A workspace for much fewer blocks than whole items keep busy would slow the call down (512
+    // behind 4000, 72 items: 31 blocks 115 us, 63 blocks 64, whole 56; the three quarters
+    // leave AR_ATTENTION_WORKSPACE_BYTES' 126 blocks of 152).
+    const int64_t busy = items < d.sms ? items : d.sms;
+    plan.whole = items >= 4ll * d.sms || fit < 2 || 4 * fit < 3 * busy ||
+                 steps + kItemEnd * items >= 1 << 30;
     if (plan.whole) {
         if (items < blocks)
             blocks = (int)items;

@@ -255,3 +255,41 @@ def test_one_token_without_keys_and_with_many_heads(workspace):
     B.ar_fusion_decode_attention(q, cache, cache, table, ints(0).cuda(), out, workspace)
     torch.cuda.synchronize()
     assert int((out_rows == 0).sum()) == 8 * H + D - 8 and bool((out_rows[8 * H + D - 8:] == 5.0).all())
+
+
+# ------------------------------------------- small workspaces
+
+def one_call(lengths, new, H, K, D, nbytes, seed=7):
+    """out, and whether the workspace was written."""
+    pages = R.Pages(lengths, 64, K, D, BF16, seed=seed, junk=False)
+    kc, vc, table, dev_lengths, _ = pages.cuda()
+    T = len(lengths) if new is None else sum(new)
+    q = torch.randn(T, H, D, generator=gen(seed)).to(BF16)
+    work = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") if nbytes else None
+    out, lse = torch.empty_like(q).cuda(), torch.empty(T, H, device="cuda")
+    starts = list(range(T + 1)) if new is None else [sum(new[:b]) for b in range(len(new) + 1)]
+    if new is None:
+        B.ar_fusion_decode_attention(q.cuda(), kc, vc, table, dev_lengths, out, work, lse=lse)
+    else:
+        B.ar_fusion_prompt_attention(q.cuda(), kc, vc, table, dev_lengths, ints(*starts).cuda(), out, work,
+                                     lse=lse)
+    torch.cuda.synchronize()
+    want = R.attention(q, pages.k, pages.v, pages.table, pages.lengths, ints(*starts), D ** -0.5, 0, 0)
+    R.check_attention(out, lse, want, BF16, BF16, 0.0, splits=40)
+    return out, work is not None and bool((work != 255).any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_workspace_of_a_few_blocks_is_not_used_for_many_items(cuda_lib, D):
+    """700 tokens, 16 heads of their own: a block of whole items for each of 152 SMs, against three."""
+    want, _ = one_call([700], [700], 16, 16, D, 0)
+    got, used = one_call([700], [700], 16, 16, D, 1 << 20)
+    assert not used and torch.equal(got, want)
+    assert one_call([700], [700], 16, 16, D, 40 << 20)[1]
+
+
+@pytest.mark.parametrize("lengths,H,K,nbytes,used", [
+    ([20011], 8, 1, 200_000, True), ([20011, 3], 8, 2, 200_000, True), ([20011], 8, 1, 16_000, False),
+    ([900] * 20, 8, 2, 200_000, False), ([5000], 33, 1, 60_000, True)])
+def test_one_token_is_split_where_the_workspace_holds_more_than_the_items(cuda_lib, lengths, H, K, nbytes, used):
+    assert one_call(lengths, None, H, K, 128, nbytes)[1] == used
