@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over the paged cache.
 //
-// Memory bounds it: every key and value is read once, for all the query heads that
+// Memory bounds it: every key and value is read once for each 16 of the query heads that
 // share it.  Those are the 8 columns of m16n8k16 products (two of them for 9 to 16 heads):
 // S^T = K Q^T, O^T = V^T P^T, keys and values straight from shared memory as first operands, the
 // weights turned by movmatrix from one product's result to the next one's operand.
@@ -26,8 +26,12 @@
 // copy); one sequence of 131072, 64 / 8 heads: 84 us, 6.4 TB/s; E4M3, 128 x 2048-4096, 64 / 8
 // heads: 133 to 143 us, 5.7 to 6.1 TB/s, what is left goes to the widening of the codes (issue
 // slots 55% used).  4 x 500-1000 tokens, 8 / 1 heads: 7.6 us, two launches and two reads behind
-// one another (page number, keys) with a join.  33 windows of 1000, 28 / 4 heads of 80: 16.3 us,
-// where a block has some ten units and fills its ring anew for the join of each item.
+// one another (page number, keys) with a join.  33 windows of 1000, 28 / 4 heads of 80: 16.3 us: a
+// block has some ten units, and the one that stands for an item's end has no slice, so that a place
+// of the ring is empty whenever an item ends.
+// 9 to 16 heads per key: 64 x 800-8000 tokens, 64 / 4 heads, 99 us, 5.8 TB/s; E4M3, 128 / 8 heads, 176,
+// 4.6 TB/s (twice the weights and products for the bytes).  More read the keys again for every
+// 16: 32 x 8000, 16 / 1 heads 30 us, 32 / 1 49, 64 / 1 86, 128 / 1 161.
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "matmul_internal.h"

@@ -34,6 +34,8 @@
 // Over a cache of E4M3 the four warps that widen its codes are the bound: 417 us.
 // 64 keys a step with two places for the scores took 450 us instead of 349 (twice the waits for as
 // many products), weights ahead of the maximum 27 us more (another pass over the registers).
+// Heads of 64 elements: 8192 tokens 282 us, 0.97 PFLOP/s: the products halve, the softmax does not.
+// Heads of 72 to 112 elements take the time of 128 (80: 320 us, 96: 331): zeros to 128 in both products.
 #include "ar_internal.h"
 #include "attention_internal.h"
 #include "matmul_internal.h"

@@ -7,7 +7,7 @@
 // and written once.  The row's place (its sequence, length and page) is a chain of
 // three loads, and the elements do not wait for it: the first kAhead pieces of
 // every thread are loaded before it.  What bounds it is memory and the latency of that chain (8
-// rows on an SM at a time): 4 x 2048 rows of 32 + 8 + 8 heads 36.1 us, 5.6 TB/s (stores without
+// rows on an SM at a time): 4 x 2048 rows of 32 + 8 + 8 heads 36.3 us, 5.5 TB/s (stores without
 // the streaming hint 4% more, 7 blocks on an SM 5%, blocks of 64, 96, 192 and 256 threads 17, 2,
 // 7 and 40%); 64 rows of 8 + 1 + 1 heads 2.1, a launch.
 #include "ar_internal.h"
@@ -18,7 +18,7 @@ namespace arf {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMostAhead = 3;   // pieces of 16 elements in flight per thread
+constexpr int kMostAhead = 3;   // pieces of 16 elements in flight per thread (16 to 48 bytes spill)
 
 // The division of a piece's number by the pieces of a head, as a multiplication: exact below
 // 2^32 / per, and there are below 2^28 pieces of at most 16 a head.

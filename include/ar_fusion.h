@@ -658,8 +658,8 @@ int ar_fusion_combine(const void* rows_in, int in_rows, const int32_t* position,
 /* Elements of a head; axes of a position. */
 #define AR_MAX_HEAD_DIM 128
 #define AR_MAX_AXES 4
-/* Bytes of workspace that are enough for every split but one: prompts of heads above 64 elements
- * share items among 126 blocks with them, and among all SMs with 40 MB. */
+/* Bytes of workspace that an attention call can use, but for prompts of heads above 64 elements:
+ * they share their work among 126 blocks with these, and among all SMs with 40 MB. */
 #define AR_ATTENTION_WORKSPACE_BYTES (32 << 20)
 
 /* Rows of heads: element d of head h of row t is data[t * row + h * head + d].
@@ -680,8 +680,8 @@ typedef struct ar_head_rows {
  *   dtype        AR_DT_BF16 or AR_DT_FP16 (that of the call's rows), or AR_DT_E4M3
  *   pages        >= 1;  page_size a power of two, 8 .. 65536
  *   heads        >= 1;  head_dim a multiple of 8 (E4M3: 16), 8 .. AR_MAX_HEAD_DIM
- *   scale        device fp32 [2], positive and finite: a key is its code times scale[0], a
- *                value its code times scale[1].  NULL: 1.  With AR_DT_E4M3 only
+ *   scale        device fp32 [2], positive and finite with finite inverses: a key is its code
+ *                times scale[0], a value its code times scale[1].  NULL: 1.  With AR_DT_E4M3 only
  *   page_table   device int32 [sequences][max_pages]
  *   lengths      device int32 [sequences]
  *   sequences    0 .. AR_MAX_SEQUENCES (0: nothing launched);  max_pages >= 1,
@@ -734,18 +734,22 @@ int ar_fusion_rope_append(const ar_kv_cache* cache, const ar_head_rows* q,
  * in fp32 (the products of the matrix instructions; e^{s_j - max} is rounded to the
  * 16-bit type of the values' product, the rows' or for this call over an E4M3 cache
  * fp16; of a weight that fp16 cannot hold at most 2^-39 of the largest weight is lost,
- * by ar_fusion_prompt_attention 2^-30), rounded to the element type once.  A token that
+ * of one that bf16 cannot hold 2^-125, by ar_fusion_prompt_attention 2^-30 and 2^-109),
+ * rounded to the element type once.  A token that
  * sees nothing gets zeros and -inf.  What keys and values hold that no token of the
  * call sees, NaN and infinities among it, changes nothing.
  *   q, out     [sequences][q_heads] of `dtype` (AR_DT_BF16 or AR_DT_FP16)
  *   lse        device fp32 [sequences][q_heads] or NULL
  *   q_heads    a multiple of cache->heads, at most AR_MAX_HEAD_GROUP times it
- *   scale      positive and finite
+ *   scale      positive and finite; with the cache's scale[0] and log2 e a normal fp32 number, too
  *   window     0 (all keys) or the number of last keys, the token's own among them;
  *              sinks >= 0: first keys that stay visible (0 without a window)
  *   workspace  device memory, 16-byte aligned, written by this call alone while it
- *              runs; the long axis is split as far as workspace_bytes allow (NULL with
- *              0: not at all; AR_ATTENTION_WORKSPACE_BYTES: see there)
+ *              runs (NULL with 0: none).  A sequence's keys are split over the GPU where
+ *              there is room for the pieces of one block an SM, or of as many blocks as there
+ *              are groups of up to 16 query heads of a head and sequence; with less they are not
+ * The bits of a result are the same in every call of the same sizes, lengths and workspace_bytes on
+ * the same kind of GPU: these say in which pieces and order keys are added up.
  * Errors: AR_ERR_INVALID, AR_ERR_UNSUPPORTED (dtype, limits), AR_ERR_CUDA. */
 int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
                                const ar_head_rows* out, float* lse, int q_heads, int dtype,
@@ -756,6 +760,11 @@ int ar_fusion_decode_attention(const ar_kv_cache* cache, const ar_head_rows* q,
  * own index.
  *   q, out     [tokens][q_heads];  lse [tokens][q_heads] or NULL
  *   starts     device int32 [sequences + 1]
+ *   workspace  as above, but what is shared out are the keys of some rows (two tiles of 128 / G
+ *              tokens, G query heads of a head): among one block an SM, or as many as there
+ *              is room for, while `tokens` and sequences make at most four such items an SM.
+ *              With room for less than three quarters of the blocks that the items keep busy, or
+ *              with more items, whatever the workspace, an item is one block's work
  * An infinite or NaN value of a key that one token of a sequence sees also reaches tokens
  * next to it that do not see that key; with bf16 rows so do values above 2^112 divided by
  * the number of keys, whose sums may leave fp32 before the quotient is taken.
