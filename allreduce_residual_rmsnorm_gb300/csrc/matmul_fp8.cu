@@ -31,8 +31,8 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// A host thread whose first call this is has no context yet: the runtime's calls take the current
-// device's, the driver's answer that there is none.
+// A host thread whose first call this is has no current context yet: the CUDA runtime's calls make
+// the device's current, this one, of the driver API, answers that there is none.
 bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, void* base, const cuuint64_t* sizes,
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
             CUtensorMapL2promotion promotion)
